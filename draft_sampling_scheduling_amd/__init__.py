@@ -110,6 +110,8 @@ def lib():
         L.dspark_read_probe.argtypes = [vp, sz, i, vp, vp, vp, vp]
         L.dspark_read_probe.restype = i
         L.dspark_version.restype = C.c_char_p
+        from . import target
+        target.set_argtypes(L)
         _lib = L
     return _lib
 
@@ -570,3 +572,21 @@ def sps_interpolate(B_list, sps_at, B0, B1):
                                       out.ctypes.data_as(C.c_void_p))
     _raise("dspark_sps_interpolate", rc)
     return out
+
+
+# ----------------------------------------------------------------------------------------
+# the target's side of a cycle (include/dspark_target.h): resolved on first use, so that
+# importing this package stays free of torch
+# ----------------------------------------------------------------------------------------
+_TARGET = ("cache_plan", "cache_plan_workspace_bytes", "cache_append", "tree_attention",
+           "tree_attention_workspace_bytes", "target_logits", "cache_commit",
+           "cache_commit_workspace_bytes", "TARGET_EXPORTS", "FAULT_PAGE", "FAULT_TREE",
+           "FAULT_PARAM", "MAX_TREE_NODES")
+
+
+def __getattr__(name):
+    if name in _TARGET:
+        from . import target
+        value = globals()[name] = getattr(target, name)
+        return value
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

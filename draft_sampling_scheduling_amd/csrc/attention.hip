@@ -1,0 +1,760 @@
+// attention.hip -- attention of a step's rows (a chain or a tree of drafted tokens, one
+// token, or a piece of a prompt) over the paged cache.
+//
+// For a request with n rows over ctx + n tokens, the n * (Hq / Hkv) query rows that share a
+// cache head are the columns of two matrix products per 32 tokens, both taken transposed:
+//   S^T = K Q^T   (tokens x rows)      and      O^T += V^T P^T   (D x rows),
+// with one pass over K and V and the running maximum m and sum l of the softmax,
+//   P = exp(S - m),  O = O exp(m_old - m) + P V,  l = l exp(m_old - m) + sum P.
+// Transposed, a lane holds one query row's scores (its accumulator column), so maxima and
+// sums are in-lane but for one half-wave exchange, and the 16 scores a lane ends S^T with are,
+// unmoved, the operand that O^T takes: the order of the tokens in the second contraction is
+// free as long as V follows it.
+//
+// Bound: the cache is read once, M = n Hq / Hkv multiply-adds per element of it, so HBM
+// bounds it up to M of a few hundred; what the design needs is bytes in flight.
+//   - A wave owns 32-token tiles: it copies a tile's K and V rows straight to its own LDS
+//     (16 bytes a lane), two tiles deep, waits on its own copies only, and keeps m, l, O in
+//     registers.  No barrier in the loop; two waves share a workgroup and merge at the end.
+//   - The tokens of all requests and heads form one list of rounds (64 tokens x one row tile of
+//     one head), cut evenly over a fixed grid, so ragged lengths balance and a single long
+//     request fills the chip.  A piece of a row tile's list that is not all of it goes to
+//     the workspace, and a second kernel joins the pieces in order.
+#include <type_traits>
+
+#include "sweep.h"
+#include "target.h"
+
+namespace dspark {
+
+constexpr int kAttWaves = 2;
+constexpr int kAttThreads = kAttWaves * kWave;
+constexpr int kTok = 32;                     // tokens of a wave's tile
+constexpr int kRound = kAttWaves * kTok;     // tokens of a round
+constexpr int kStages = 2;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+struct AttParams {
+  int R, rows, Hq, Hkv, G;  // G = Hq / Hkv
+  int lg, max_pages, n_pages;
+  const void* q;
+  int64_t q_row;
+  const void *k, *v;
+  int64_t page_b, head_b, tok_b;  // strides in bytes
+  const int32_t *table, *ctx, *row_off;
+  const uint64_t* anc;
+  float scale;
+  void* o;
+  float* lse;
+  int32_t* status;
+  float* part;   // [grid][2][MR][D + 2]: O, then m, then l of each row
+  int4* joint;   // [grid] what the second kernel joins (see AttJoint)
+};
+
+// a request's rows and tokens, as the host of the data should have them, clamped
+struct AttReq {
+  int a, n, ctx;
+};
+
+__device__ __forceinline__ AttReq att_req(const AttParams& p, int q, bool tell) {
+  const int cap = p.max_pages << p.lg;
+  int a = p.row_off[q], e = p.row_off[q + 1], c = p.ctx[q];
+  bool bad = a < 0 || e < a || e > p.rows;
+  a = a < 0 ? 0 : (a > p.rows ? p.rows : a);
+  e = e < a ? a : (e > p.rows ? p.rows : e);
+  int n = e - a;
+  if (n > cap) {
+    n = cap;
+    bad = true;
+  }
+  if (n > 0 && (c < 0 || c > cap - n)) {
+    c = c < 0 ? 0 : cap - n;
+    bad = true;
+  }
+  if (tell) {
+    if (bad) raise_fault(p.status, DSPARK_FAULT_LEN);
+    if (p.anc && n > DSPARK_MAX_TREE_NODES) raise_fault(p.status, DSPARK_FAULT_TREE);
+  }
+  return {a, n, c};
+}
+
+// uniform loads through the scalar cache (the arrays are inputs, constant during the call)
+__device__ __forceinline__ int sload(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)p)[i];
+}
+
+// a value that every lane holds alike, as a scalar
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uni(int64_t x) {
+  return (int64_t)(((uint64_t)(uint32_t)uni((int)(x >> 32)) << 32) | (uint32_t)uni((int)x));
+}
+
+// ---------------------------------------------------------------------------------------
+// Per element type: the tile's geometry in LDS, the fragments, and the two products.
+// A tile's rows lie RB bytes apart in 16-byte chunks; chunk c of row r is at chunk
+// c ^ kswz(r) (K) or c ^ vswz(r) (V), which spreads what one LDS instruction reads over the
+// banks: 16 rows at one chunk (K), 4 rows at 4 neighbouring chunks (V, bf16), rows 4 apart (V,
+// float).  Both maps act on disjoint bits of r, so map(i | j) = map(i) ^ map(j).
+// ---------------------------------------------------------------------------------------
+template <class T, int D>
+struct Tile {
+  static constexpr bool kBf = std::is_same<T, uint16_t>::value;
+  static constexpr int kE = kBf ? 2 : 4;
+  static constexpr int RB = D * kE;            // bytes of a row
+  static constexpr int CPR = RB / 16;          // chunks of a row
+  static constexpr int RPC = kWave / CPR;      // rows one copy instruction moves
+  static constexpr int NC = kTok / RPC;        // copies of one operand's tile
+  static constexpr int BYTES = kTok * RB;      // one operand's tile
+  static constexpr int KSTEPS = D / (kBf ? 16 : 8);  // 16-byte fragments of a row per half-wave
+  static __host__ __device__ constexpr int kswz(int r) { return CPR >= 16 ? (r & 15) : ((r >> 1) & 7); }
+  static __host__ __device__ constexpr int vswz(int r) {
+    if (!kBf) return ((r >> 2) & 1) << 3;
+    return CPR >= 16 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+  }
+};
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+#define DSPARK_LDS __attribute__((address_space(3)))
+
+template <class V>
+__device__ __forceinline__ V lds_get(uint32_t a) {
+  return *(const DSPARK_LDS V*)(uintptr_t)a;
+}
+template <class V>
+__device__ __forceinline__ void lds_put(uint32_t a, V x) {
+  *(DSPARK_LDS V*)(uintptr_t)a = x;
+}
+// the value, its origin hidden: what is computed from it stays where it stands (a loop's
+// addresses are one instruction each, and would cost a register each if hoisted)
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// K's fragment of step s times every row tile's Q fragment
+template <class T>
+__device__ __forceinline__ void mfma_qk(u32x4 a, u32x4 b, f32x16& acc) {
+  if constexpr (std::is_same<T, uint16_t>::value) {
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                  __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+  } else {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], acc, 0, 0, 0);
+  }
+}
+
+// token of accumulator register r of half-wave h, within a tile; also d within 32 for O^T
+__device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
+
+template <class T, int D, int MT>
+struct AttWave {
+  using L = Tile<T, D>;
+  static constexpr int ND = D / 32;
+
+  const AttParams& p;
+  int lane, n, h;           // n: lane's column (query row of the tile), h: half-wave
+  uint32_t base;            // this wave's LDS
+  // segment
+  const char *kh, *vh;      // cache bases of the head
+  const int32_t* pages;     // the request's block table
+  int ctx, len, last_page;  // committed tokens, tokens in all, page of the last token
+  u32x4 qf[MT][L::KSTEPS];
+  uint64_t see[MT];         // tree: nodes (bit j - 1) the lane's row sees
+  int node[MT];             // chain: the lane's node
+  // state
+  f32x16 o[MT][ND];
+  float m[MT], l[MT];       // m: the largest score so far times scale * log2(e)
+
+  __device__ __forceinline__ AttWave(const AttParams& p_, uint32_t base_)
+      : p(p_), lane(threadIdx.x & 63), n(lane & 31), h(lane >> 5), base(base_) {}
+
+  // The copies of tile t0's K and V rows into stage s.  A copy's rows (at most 8, aligned)
+  // share a page.  Rows past the last token read inside its page; nothing reads past it.
+  __device__ __forceinline__ void page_ids(int t0, int (&pg)[4]) const {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      int i = (t0 + 8 * g) >> p.lg;
+      i = i < last_page ? i : last_page;
+      pg[g] = sload(pages, i);
+    }
+  }
+  __device__ __forceinline__ void copy_tile(int t0, int (&pg)[4], int s) const {
+    bool bad = false;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const bool out = pg[g] < 0 || pg[g] >= p.n_pages;
+      bad = bad || out;
+      pg[g] = out ? 0 : pg[g];
+    }
+    if (bad && lane == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
+    const int lr = lane / L::CPR, pos = lane % L::CPR;
+    const uint32_t row = (uint32_t)(lr * (int)p.tok_b);
+    const uint32_t to = base + s * 2 * L::BYTES;
+    const int in_page = (1 << p.lg) - 1;
+#pragma unroll
+    for (int c = 0; c < L::NC; ++c) {
+      const int64_t off = pg[(c * L::RPC) >> 3] * p.page_b + (int64_t)((t0 + c * L::RPC) & in_page) * p.tok_b;
+      const uint32_t kc = (uint32_t)((pos ^ L::kswz(lr) ^ L::kswz(c * L::RPC)) << 4);
+      const uint32_t vc = (uint32_t)((pos ^ L::vswz(lr) ^ L::vswz(c * L::RPC)) << 4);
+      dma16s(kh + off, row + kc, to + c * 1024);
+      dma16s(vh + off, row + vc, to + L::BYTES + c * 1024);
+    }
+  }
+
+  // One tile in stage s: tokens t0 .. t0 + 31.  `edge`: some of them are of the block, or
+  // behind it.
+  __device__ __forceinline__ void tile(int t0, int s, bool edge) {
+    const uint32_t ks = base + s * 2 * L::BYTES, vs = ks + L::BYTES;
+    f32x16 sc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) sc[mt] = f32x16{};
+    {
+      const uint32_t krow = here(ks + n * L::RB), kx = here((uint32_t)(h ^ L::kswz(n)) << 4);
+#pragma unroll
+      for (int st = 0; st < L::KSTEPS; ++st) {
+        const u32x4 a = lds_get<u32x4>(krow + (kx ^ (uint32_t)(st << 5)));
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) mfma_qk<T>(a, qf[mt][st], sc[mt]);
+      }
+    }
+    bool odd = false;  // the tile's V holds infinities or NaN
+    if (edge) {
+      mask(t0, sc);
+      odd = clean_values(t0, vs);
+    }
+    const float c2 = p.scale * kLog2e;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float mx = sc[mt][0];
+#pragma unroll
+      for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[mt][r]);
+      mx = half_max(mx);
+      const float mn = fmaxf(m[mt], mx * c2);
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      if (__ballot(mn > m[mt])) {  // some row's maximum grew: what is summed so far shrinks
+        const float f = __builtin_amdgcn_exp2f(m[mt] - ref);
+        l[mt] *= f;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) o[mt][dt][r] *= f;
+        m[mt] = mn;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        sc[mt][r] = __builtin_amdgcn_exp2f(fmaf(sc[mt][r], c2, -ref));
+        sum += sc[mt][r];
+      }
+      l[mt] += sum;  // this half-wave's tokens; the halves are added at the end
+    }
+    if (odd) odd_values(ks, vs, sc);  // leaves V's tile at 0
+    if constexpr (L::kBf) {
+      // O^T += V^T P^T, 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens
+      // of it, rounded to bf16 (each weight off by 2^-8 of itself at most, as o is when stored);
+      // V's fragment is two transposing reads of 4 tokens x 16 d.  Rows 8 apart share a
+      // swizzle, so a lane has one address per 32 d and the rest are immediates.
+      const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
+      const uint32_t vrow = here(vs + r0 * L::RB + (j & 1) * 8);
+      const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ L::vswz(r0)) << 4);
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        bf16x8 pb[MT];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) pb[mt][e] = (__bf16)sc[mt][8 * st + e];
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) {
+          union {
+            s16x4 half[2];
+            bf16x8 all;
+          } a;
+          const uint32_t at = vrow + (vx ^ (uint32_t)(dt << 6));
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            a.half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (DSPARK_LDS s16x4*)(uintptr_t)(at + 8 * (2 * st + b) * L::RB));
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.all, pb[mt], o[mt][dt], 0, 0, 0);
+        }
+      }
+    } else {
+      // register r is token reg_row(r, h): the two halves' tokens are one step's pair
+      const uint32_t vrow = here(vs + 4 * h * L::RB + (n & 3) * 4);
+      const uint32_t vx = here((uint32_t)((n >> 2) ^ L::vswz(4 * h)) << 4);
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) {
+          const float a = lds_get<float>(vrow + (vx ^ (uint32_t)(dt << 7)) + reg_row(r, 0) * L::RB);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, sc[mt][r], o[mt][dt], 0, 0, 0);
+        }
+    }
+  }
+
+  // scores of tokens that the lane's row does not see: -inf
+  __device__ __forceinline__ void mask(int t0, f32x16 (&sc)[MT]) const {
+    const bool tree = p.anc != nullptr;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int j = t0 + reg_row(r, h) - ctx;
+        const bool below = tree ? j <= 64 && ((see[mt] >> ((j - 1) & 63)) & 1) : j <= node[mt];
+        const bool ok = (j <= 0 || below) && j < len - ctx;
+        sc[mt][r] = ok ? sc[mt][r] : -INFINITY;
+      }
+  }
+
+  // V rows behind the last token become 0 (they may hold anything, and 0 * NaN is none);
+  // whether the rows left hold infinities or NaN
+  __device__ __forceinline__ bool clean_values(int t0, uint32_t vs) const {
+    bool bad = false;
+#pragma unroll 1
+    for (int i = lane; i < L::NC * kWave; i += kWave) {
+      const uint32_t at = vs + i * 16;
+      if (t0 + i / L::CPR >= len) lds_put<u32x4>(at, u32x4{0, 0, 0, 0});
+      const u32x4 x = lds_get<u32x4>(at);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        bad = bad || (x[w] & 0x7F800000u) == 0x7F800000u;
+        if (L::kBf) bad = bad || (x[w] & 0x7F80u) == 0x7F80u;
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    return __ballot(bad) != 0;
+  }
+
+  // The product with a V tile that holds infinities or NaN: a weight of 0 leaves a token out
+  // (a matrix product would make 0 * inf of it).  The weights go through the K tile's LDS,
+  // which the scores no longer need; the tile is 0 afterwards.
+  __device__ __forceinline__ void odd_values(uint32_t ks, uint32_t vs, const f32x16 (&sc)[MT]) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r) lds_put<float>(ks + (reg_row(r, h) * 32 + n) * 4, sc[mt][r]);
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll 1
+      for (int t = 0; t < kTok; ++t) {
+        const float w = lds_get<float>(ks + (t * 32 + n) * 4);
+        if (w == 0.0f) continue;
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt) {
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int d = 32 * dt + reg_row(r, h);
+            const uint32_t at =
+                vs + t * L::RB + (((d * L::kE / 16) ^ L::vswz(t)) << 4) + (d * L::kE) % 16;
+            float x;
+            if constexpr (L::kBf)
+              x = bf16_to_f32(lds_get<uint16_t>(at));
+            else
+              x = lds_get<float>(at);
+            o[mt][dt][r] = fmaf(w, x, o[mt][dt][r]);
+          }
+          asm volatile("" ::: "memory");
+        }
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+#pragma unroll 1
+    for (int i = lane; i < L::NC * kWave; i += kWave) lds_put<u32x4>(vs + i * 16, u32x4{0, 0, 0, 0});
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+
+  // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
+  __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr,
+                                          int wave) {
+    const int M = rq.n * p.G;
+    ctx = rq.ctx;
+    pages = p.table + (int64_t)q * p.max_pages;
+    kh = static_cast<const char*>(p.k) + head * p.head_b;
+    vh = static_cast<const char*>(p.v) + head * p.head_b;
+    len = rq.ctx + rq.n;
+    last_page = (len - 1) >> p.lg;
+    // a chain's row tile sees no node after its last row's
+    int most = len;
+    if (!p.anc) {
+      const int last = m0 + 32 * MT - 1 < M - 1 ? m0 + 32 * MT - 1 : M - 1;
+      most = rq.ctx + last / p.G + 1;
+    }
+    const int first = r0 * kRound + wave * kTok;
+    int end = (r0 + nr) * kRound;
+    end = end < most ? end : most;
+    const int nt = first < end ? (end - first + kRound - 1) / kRound : 0;
+    int pg[4];
+    if (nt > 0) {
+      page_ids(first, pg);
+      copy_tile(first, pg, 0);
+      page_ids(first + kRound, pg);  // past the end: the last page's
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int mi = m0 + 32 * mt + n;
+      const bool live = mi < M;
+      const int i = live ? mi / p.G : 0, g = live ? mi % p.G : 0;
+      const char* src = static_cast<const char*>(p.q) +
+                        ((int64_t)(rq.a + i) * p.q_row + (int64_t)(head * p.G + g) * D) * L::kE;
+#pragma unroll
+      for (int st = 0; st < L::KSTEPS; ++st) {
+        qf[mt][st] = u32x4{0, 0, 0, 0};
+        if (live) qf[mt][st] = *reinterpret_cast<const u32x4*>(src + (2 * st + h) * 16);
+      }
+      node[mt] = i;
+      see[mt] = p.anc ? p.anc[rq.a + i] : 0;
+      m[mt] = -INFINITY;
+      l[mt] = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) o[mt][dt] = f32x16{};
+    }
+    for (int k = 0; k < nt; ++k) {
+      const int t0 = first + k * kRound, s = k & 1;
+      if (k + 1 < nt) {
+        copy_tile(t0 + kRound, pg, s ^ 1);
+        page_ids(t0 + 2 * kRound, pg);
+        vm_wait<2 * L::NC>();
+      } else {
+        vm_wait<0>();
+      }
+      tile(t0, s, t0 + kTok > ctx);
+      // the stage is free once its reads have returned
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) l[mt] = half_sum(l[mt]);
+  }
+};
+
+// One segment of a workgroup's share, as the second kernel finds it: a row tile whose list is
+// cut has its pieces at workgroups first .. first + count - 1, in slot 0 (their first
+// segment), but for the first piece, which may be its workgroup's last (slot 1).
+//   joint[b] = (q, head, row tile, count | slot of the first piece << 30), first = b - 1;
+//   count 0: nothing to join
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(kAttThreads, 1) attention_kernel(AttParams p) {
+  using L = Tile<T, D>;
+  constexpr int MR = 32 * MT, ND = D / 32;
+  extern __shared__ uint4 lds[];
+  __shared__ int64_t sums[kAttWaves];
+  __shared__ int64_t total_s;
+  __shared__ int start_s;
+  __shared__ int64_t start_off;
+  const int tid = threadIdx.x, wave = uni(tid >> 6);
+  const int b = blockIdx.x;
+
+  // the list of rounds: per head, request after request, row tile after row tile
+  auto units = [&](const AttReq& r) -> int64_t {
+    return (int64_t)((r.n * p.G + MR - 1) / MR) * ((r.ctx + r.n + kRound - 1) / kRound);
+  };
+  const int per = (p.R + kAttThreads - 1) / kAttThreads;
+  const int lo = min(p.R, tid * per), hi = min(p.R, lo + per);
+  int64_t mine = 0;
+  for (int q = lo; q < hi; ++q) {
+    const AttReq r = att_req(p, q, b == 0);
+    mine += r.n > 0 ? units(r) : 0;
+  }
+  const int64_t upto = block_scan<kAttThreads>(mine, sums);
+  if (tid == kAttThreads - 1) total_s = upto;
+  __syncthreads();
+  const int64_t W = uni(total_s), U = W * p.Hkv;
+  const int64_t P = U < gridDim.x ? U : gridDim.x;
+  if (tid == 0) p.joint[b] = make_int4(0, 0, 0, 0);
+  if (b >= P) return;
+  const int64_t u0 = U * b / P, u1 = U * (b + 1) / P;
+  int head = (int)(u0 / W);
+  {
+    const int64_t w = u0 % W;
+    if (w >= upto - mine && w < upto) {
+      int64_t at = upto - mine;
+      for (int q = lo; q < hi; ++q) {
+        const AttReq r = att_req(p, q, false);
+        const int64_t x = r.n > 0 ? units(r) : 0;
+        if (w < at + x) {
+          start_s = q;
+          start_off = w - at;
+          break;
+        }
+        at += x;
+      }
+    }
+  }
+  __syncthreads();
+  int q = uni(start_s);
+  int64_t off = uni(start_off);  // rounds of q's list before this workgroup's
+
+  const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
+  AttWave<T, D, MT> wv(p, base + wave * kStages * 2 * L::BYTES);
+  for (int64_t u = u0; u < u1;) {
+    AttReq rq = att_req(p, q, false);
+    rq.a = uni(rq.a);
+    rq.n = uni(rq.n);
+    rq.ctx = uni(rq.ctx);
+    const int64_t rounds = (rq.ctx + rq.n + kRound - 1) / kRound;
+    const int64_t tiles = (rq.n * p.G + MR - 1) / MR;
+    if (rq.n == 0 || off >= tiles * rounds) {  // on to the next request, or the next head
+      off = 0;
+      if (++q == p.R) {
+        q = 0;
+        ++head;
+      }
+      continue;
+    }
+    const int mt0 = (int)(off / rounds), r0 = (int)(off % rounds);
+    const int nr = (int)(u1 - u < rounds - r0 ? u1 - u : rounds - r0);
+    wv.segment(rq, q, head, mt0 * MR, r0, nr, wave);
+
+    // the second wave's sums into the first's, through LDS
+    __syncthreads();
+    float* x = reinterpret_cast<float*>(lds);
+    const int lane = tid & 63;
+    if (wave == 1) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) x[((mt * ND + dt) * 16 + r) * 64 + lane] = wv.o[mt][dt][r];
+        x[(MT * ND * 16 + 2 * mt) * 64 + lane] = wv.m[mt];
+        x[(MT * ND * 16 + 2 * mt + 1) * 64 + lane] = wv.l[mt];
+      }
+    }
+    __syncthreads();
+    const bool whole = r0 == 0 && nr == rounds;
+    if (wave == 0) {
+      const int M = rq.n * p.G;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const float m2 = x[(MT * ND * 16 + 2 * mt) * 64 + lane];
+        const float l2 = x[(MT * ND * 16 + 2 * mt + 1) * 64 + lane];
+        const float mm = fmaxf(wv.m[mt], m2);
+        const float ref = mm == -INFINITY ? 0.0f : mm;
+        const float f1 = __builtin_amdgcn_exp2f(wv.m[mt] - ref);
+        const float f2 = __builtin_amdgcn_exp2f(m2 - ref);
+        const float ll = wv.l[mt] * f1 + l2 * f2;
+        const int row = 32 * mt + wv.n, mi = mt0 * MR + row;
+        if (mi >= M) continue;
+        const int i = mi / p.G, a = head * p.G + mi % p.G;
+        if (whole) {
+          const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+          T* out = static_cast<T*>(p.o) + ((int64_t)(rq.a + i) * p.Hq + a) * D;
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+              f32x4 y;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = 4 * r4 + e;
+                y[e] = (wv.o[mt][dt][r] * f1 + x[((mt * ND + dt) * 16 + r) * 64 + lane] * f2) * inv;
+              }
+              T* to = out + 32 * dt + 8 * r4 + 4 * wv.h;
+              if constexpr (L::kBf) {
+                bf16x4 z;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = (__bf16)y[e];
+                *reinterpret_cast<bf16x4*>(to) = z;
+              } else {
+                *reinterpret_cast<f32x4*>(to) = y;
+              }
+            }
+          if (p.lse && wv.h == 0)
+            p.lse[(int64_t)(rq.a + i) * p.Hq + a] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
+        } else {
+          const int slot = u == u0 ? 0 : 1;
+          float* part = p.part + ((int64_t)b * 2 + slot) * MR * (D + 2);
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+            for (int r4 = 0; r4 < 4; ++r4) {
+              f32x4 y;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int r = 4 * r4 + e;
+                y[e] = wv.o[mt][dt][r] * f1 + x[((mt * ND + dt) * 16 + r) * 64 + lane] * f2;
+              }
+              *reinterpret_cast<f32x4*>(part + row * D + 32 * dt + 8 * r4 + 4 * wv.h) = y;
+            }
+          if (wv.h == 0) {
+            part[MR * D + row] = mm;
+            part[MR * (D + 1) + row] = ll;
+          }
+        }
+      }
+    }
+    if (tid == 0 && u == u0 && r0 > 0) {
+      // this workgroup begins inside the row tile's list [s, e): the first to do so says
+      // who holds its pieces
+      const int64_t s = u - r0, e = s + rounds;
+      const int64_t first = ((s + 1) * P - 1) / U, last = (e * P - 1) / U;
+      if (first == b - 1)
+        p.joint[b] = make_int4(q, head, mt0,
+                               (int)(last - first + 1) | (U * first / P >= s ? 0 : 1 << 30));
+    }
+    __syncthreads();  // LDS is the next segment's
+    u += nr;
+    off += nr;
+  }
+}
+
+// Joins the pieces of the row tiles that are cut: a wave per row, pieces in order.
+template <class T, int D, int MT>
+__global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
+  constexpr int MR = 32 * MT, E = D / kWave;
+  const int b = blockIdx.x;
+  const int4 jt = p.joint[b];
+  const int count = jt.w & 0x3fffffff;
+  if (count == 0) return;
+  const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
+  const AttReq rq = att_req(p, jt.x, false);
+  const int mi = jt.z * MR + row;
+  if (mi >= rq.n * p.G) return;
+  const float* part0 = p.part + ((int64_t)(b - 1) * 2 + (jt.w >> 30)) * MR * (D + 2);
+  auto piece = [&](int k) {
+    return k == 0 ? part0 : p.part + (int64_t)(b - 1 + k) * 2 * MR * (D + 2);
+  };
+  // the largest maximum, a lane per piece
+  float mx = -INFINITY;
+  for (int k = lane; k < count; k += kWave) mx = fmaxf(mx, piece(k)[MR * D + row]);
+  mx = wave_max(mx);
+  const float ref = mx == -INFINITY ? 0.0f : mx;
+  float acc[E], ll = 0.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll 4
+  for (int k = 0; k < count; ++k) {
+    const float* x = piece(k);
+    const float f = __builtin_amdgcn_exp2f(x[MR * D + row] - ref);
+    ll = fmaf(x[MR * (D + 1) + row], f, ll);
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + E * lane + e], f, acc[e]);
+  }
+  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
+  const int i = mi / p.G, a = jt.y * p.G + mi % p.G;
+  T* out = static_cast<T*>(p.o) + ((int64_t)(rq.a + i) * p.Hq + a) * D + E * lane;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    if constexpr (std::is_same<T, uint16_t>::value)
+      out[e] = __builtin_bit_cast(uint16_t, (__bf16)(acc[e] * inv));
+    else
+      out[e] = acc[e] * inv;
+  }
+  if (p.lse && lane == 0) p.lse[(int64_t)(rq.a + i) * p.Hq + a] = (mx + __builtin_amdgcn_logf(ll)) * kLn2;
+}
+
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+// Row tiles of 32 query rows where a request's rows need no more (rows / R of them times
+// heads to a cache head, the bound the host knows), else of 64: a cache tile is then read for
+// twice the rows.
+static int att_mt(int R, int rows, int G, dspark_dtype dt) {
+  if (dt == DSPARK_F32) return 1;
+  return (int64_t)((rows + R - 1) / R) * G <= 32 ? 1 : 2;
+}
+
+static int att_lds(int D, dspark_dtype dt) {
+  return kAttWaves * kStages * 2 * kTok * D * (dt == DSPARK_BF16 ? 2 : 4);
+}
+
+// workgroups: as many as stay resident (two a CU where LDS holds two)
+static int att_grid(int D, dspark_dtype dt) {
+  return device_cus() * (2 * att_lds(D, dt) <= 160 * 1024 ? 2 : 1);
+}
+
+static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
+  Carve cv(ws);
+  const size_t grid = (size_t)att_grid(D, dt);
+  p.joint = cv.take<int4>(grid);
+  p.part = cv.take<float>(grid * 2 * 32 * att_mt(R, rows, G, dt) * (D + 2));
+  return cv.bytes();
+}
+
+static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt) {
+  return R >= 0 && rows >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && (D == 64 || D == 128) &&
+         (dt == DSPARK_F32 || dt == DSPARK_BF16) && (int64_t)rows * Hq < ((int64_t)1 << 31);
+}
+
+template <class T, int D, int MT>
+static int att_launch(const AttParams& p, hipStream_t stream) {
+  constexpr dspark_dtype dt = std::is_same<T, uint16_t>::value ? DSPARK_BF16 : DSPARK_F32;
+  static std::atomic<uint64_t> raised;
+  auto kern = attention_kernel<T, D, MT>;
+  const int sh = att_lds(D, dt), grid = att_grid(D, dt);
+  ensure_dynamic_lds(reinterpret_cast<const void*>(kern), sh, raised);
+  kern<<<grid, kAttThreads, sh, stream>>>(p);
+  attention_join_kernel<T, D, MT><<<dim3(grid, 8 * MT), 256, 0, stream>>>(p);
+  return launch_status();
+}
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" size_t dspark_tree_attention_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
+                                                        dspark_dtype dt) {
+  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || R == 0) return 0;
+  AttParams p{};
+  return att_carve(p, nullptr, R, rows, Hq / Hkv, D, dt);
+}
+
+extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt,
+                                     int page_size, int max_pages, int n_pages, const void* q,
+                                     int64_t q_row, const void* k_cache, const void* v_cache,
+                                     int64_t page_stride, int64_t head_stride, int64_t tok_stride,
+                                     const int32_t* table, const int32_t* ctx,
+                                     const int32_t* row_off, const uint64_t* anc, float scale,
+                                     void* o, float* lse, int32_t* dev_status, void* ws,
+                                     size_t ws_bytes, hipStream_t stream) {
+  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || max_pages < 1 || !pages_ok(page_size, n_pages) ||
+      !pages_ok(page_size, max_pages) || !(scale > 0.0f) || scale > FLT_MAX)
+    return DSPARK_EINVAL;
+  const size_t e = dt == DSPARK_BF16 ? 2 : 4;
+  if (!stride_ok(q_row, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||
+      !stride_ok(tok_stride, e) || tok_stride > (1 << 24))
+    return DSPARK_EINVAL;
+  if (R == 0 || rows == 0) return DSPARK_OK;
+  if (!q || !k_cache || !v_cache || !table || !ctx || !row_off || !o || !ws || !aligned16(q) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(ws))
+    return DSPARK_EINVAL;
+  AttParams p{};
+  p.R = R;
+  p.rows = rows;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.lg = log2_of(page_size);
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.q = q;
+  p.q_row = q_row;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.page_b = page_stride * (int64_t)e;
+  p.head_b = head_stride * (int64_t)e;
+  p.tok_b = tok_stride * (int64_t)e;
+  p.table = table;
+  p.ctx = ctx;
+  p.row_off = row_off;
+  p.anc = anc;
+  p.scale = scale;
+  p.o = o;
+  p.lse = lse;
+  p.status = dev_status;
+  if (ws_bytes < att_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
+  const int mt = att_mt(R, rows, p.G, dt);
+  if (dt == DSPARK_BF16) {
+    if (D == 64)
+      return mt == 1 ? att_launch<uint16_t, 64, 1>(p, stream) : att_launch<uint16_t, 64, 2>(p, stream);
+    return mt == 1 ? att_launch<uint16_t, 128, 1>(p, stream) : att_launch<uint16_t, 128, 2>(p, stream);
+  }
+  return D == 64 ? att_launch<float, 64, 1>(p, stream) : att_launch<float, 128, 1>(p, stream);
+}

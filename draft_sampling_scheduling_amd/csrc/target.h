@@ -1,0 +1,41 @@
+// target.h -- helpers shared by the kernels of the target's side of a cycle (cache.hip,
+// attention.hip, logits.hip).
+#pragma once
+
+#include "../../include/dspark_target.h"
+#include "dev.h"
+#include "host.h"
+
+namespace dspark {
+
+// 64-bit inclusive scan over the whole workgroup (NT threads, a multiple of 64, every thread
+// calls); `sums` is LDS of NT / 64 entries, free again after the call's last barrier.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums) {
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int64_t u = __shfl_up(v, o, kWave);
+    if (lane >= o) v += u;
+  }
+  if (lane == kWave - 1) sums[wave] = v;
+  __syncthreads();
+  int64_t base = 0;
+#pragma unroll
+  for (int w = 0; w < NT / kWave; ++w) base += w < wave ? sums[w] : 0;
+  __syncthreads();
+  return base + v;
+}
+
+inline bool page_size_ok(int ps) { return ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0; }
+inline int log2_of(int p) { return __builtin_ctz((unsigned)p); }
+
+// a cache of n_pages pages whose tokens and slots fit 31 bits
+inline bool pages_ok(int page_size, int64_t pages) {
+  return page_size_ok(page_size) && pages >= 1 && pages * page_size < ((int64_t)1 << 31);
+}
+
+// element strides whose byte distances keep 16-byte loads aligned
+inline bool stride_ok(int64_t s, size_t esz) { return s >= 0 && (s * (int64_t)esz) % 16 == 0; }
+
+}  // namespace dspark

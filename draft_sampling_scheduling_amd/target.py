@@ -1,0 +1,345 @@
+"""The target's side of a decode cycle: binding of include/dspark_target.h.
+
+  cache_plan      rows, pages and cache slots of a step, from lengths on the device
+  cache_append    the step's keys and values into the paged cache
+  tree_attention  the step's rows (a chain, a tree, a piece of a prompt) over the cache
+  target_logits   penalties, biases and grammar masks, into the layout verify() reads
+  cache_commit    after verify(): accepted path moved, lengths advanced, pages given back
+
+As in the other calls, tensors are device tensors, work goes to the current stream (of the
+tensors' device), bad shapes and types raise before anything is enqueued, and faults in the
+data set bits of `status` ([1] int32, nullable).  A cache is [n_pages][Hkv][page_size][D]
+with any strides over contiguous rows of D: transpose(1, 2) of [n_pages][page_size][Hkv][D]
+serves too.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+FAULT_PAGE, FAULT_TREE, FAULT_PARAM = 8, 16, 32
+MAX_TREE_NODES = 65
+TARGET_EXPORTS = ("dspark_cache_plan_workspace_bytes", "dspark_cache_plan",
+                  "dspark_cache_append", "dspark_tree_attention_workspace_bytes",
+                  "dspark_tree_attention", "dspark_target_logits",
+                  "dspark_cache_commit_workspace_bytes", "dspark_cache_commit")
+
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+
+
+def set_argtypes(L):
+    """ctypes signatures of the library's target-side entry points."""
+    i, i64, sz, vp, f = C.c_int, C.c_int64, C.c_size_t, C.c_void_p, C.c_float
+    L.dspark_cache_plan_workspace_bytes.argtypes = [i]
+    L.dspark_cache_plan_workspace_bytes.restype = sz
+    L.dspark_cache_plan.argtypes = ([i] * 6 + [vp] * 7 + [i] + [vp] * 7 + [sz, vp])
+    L.dspark_cache_append.argtypes = ([i] * 6 + [vp] * 2 + [i64] * 2 + [vp] * 4 + [i64] * 3 +
+                                      [vp] * 2)
+    L.dspark_tree_attention_workspace_bytes.argtypes = [i] * 6
+    L.dspark_tree_attention_workspace_bytes.restype = sz
+    L.dspark_tree_attention.argtypes = ([i] * 9 + [vp, i64] + [vp] * 2 + [i64] * 3 + [vp] * 4 +
+                                        [f] + [vp] * 4 + [sz, vp])
+    L.dspark_target_logits.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 4 + [i] + [vp] * 7 +
+                                       [i, vp, i, i] + [vp] * 4)
+    L.dspark_cache_commit_workspace_bytes.argtypes = [i]
+    L.dspark_cache_commit_workspace_bytes.restype = sz
+    L.dspark_cache_commit.argtypes = ([i] * 5 + [vp] * 9 + [i] * 5 + [vp] * 2 + [i64] * 4 +
+                                      [vp] * 2 + [sz, vp])
+    for name in TARGET_EXPORTS:
+        if not name.endswith("_bytes"):
+            getattr(L, name).restype = i
+
+
+# ----------------------------------------------------------------------------------------
+# checks and calls
+# ----------------------------------------------------------------------------------------
+def _device(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    return t.device
+
+
+def _chk(t, name, dev, shape, dtype, dense=True):
+    """One tensor argument; returns its address.  A None in `shape` matches any size."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    have = t.shape
+    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
+        raise ValueError(f"{name} has shape {tuple(have)}, expected {shape}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, *a):
+    return None if t is None else _chk(t, *a)
+
+
+def _dt(t, name):
+    if t.dtype is _BF16:
+        return 1
+    if t.dtype is _F32:
+        return 0
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _strides(t, last):
+    """Strides of the leading dimensions (0 for a dimension of size 1, whose stride is never
+    used) of a tensor whose last `last` dimensions are dense."""
+    n = t.dim() - last
+    dense = 1
+    for k in range(t.dim() - 1, n - 1, -1):
+        if t.shape[k] != 1 and t.stride(k) != dense:
+            return None
+        dense *= t.shape[k]
+    return [t.stride(k) if t.shape[k] > 1 else 0 for k in range(n)]
+
+
+def _cache(k_cache, v_cache, dev, dims):
+    """Shape and strides of a pair of caches (`dims`: 4, or 5 with a leading layer)."""
+    kp = _chk(k_cache, "k_cache", dev, (None,) * dims, k_cache.dtype, False)
+    vp = _chk(v_cache, "v_cache", dev, tuple(k_cache.shape), k_cache.dtype, False)
+    st = _strides(k_cache, 1)
+    if st is None or _strides(v_cache, 1) is None:
+        raise ValueError("the caches' last dimension must be contiguous")
+    if st != _strides(v_cache, 1):
+        raise ValueError("k_cache and v_cache differ in strides")
+    return kp, vp, tuple(k_cache.shape), st
+
+
+def _call(dev, fn, *args):
+    """fn(*args, stream) on `dev`; raises on a refusal."""
+    from . import DsparkError, lib
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, torch.cuda.current_stream().cuda_stream)
+    if rc != 0:
+        raise DsparkError(fn, rc)
+
+
+def _workspace(nbytes, dev, ws):
+    if ws is None:
+        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
+    else:
+        if ws.device != dev or not ws.is_contiguous():
+            raise ValueError(f"ws must be a contiguous tensor on {dev}")
+        if ws.numel() * ws.element_size() < nbytes:
+            raise ValueError("workspace too small")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def cache_plan_workspace_bytes(R) -> int:
+    from . import lib
+    return int(lib().dspark_cache_plan_workspace_bytes(R))
+
+
+def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, extra=0,
+               parent=None, out=None, ws=None, status=None):
+    """Rows, pages and slots of a step in which request q brings lens[q] + extra rows behind
+    its ctx[q] committed tokens (extra=1: lens is the scheduler's ell, the anchor comes on
+    top).  Pages that the rows lack are taken from the end of free_pages[:n_free], in place:
+    table [R][max_pages], held [R] and n_free [1] are updated.  parent [R][width]: drafted
+    trees (parent[q][i] < i is the node above node i >= 1).  `rows` bounds the step's rows.
+    Returns dict(row_off [R+1], req, position, slot [rows], and with parent anc [rows] int64);
+    a caller-supplied `out` may leave "req" and "position" out.  Rows behind row_off[-1] are
+    left as they were."""
+    dev = _device(lens, "lens")
+    R = lens.shape[0]
+    a = [_chk(lens, "lens", dev, (R,), _I32), _chk(ctx, "ctx", dev, (R,), _I32),
+         _chk(held, "held", dev, (R,), _I32), _chk(table, "table", dev, (R, None), _I32),
+         _chk(free_pages, "free_pages", dev, (None,), _I32),
+         _chk(n_free, "n_free", dev, (1,), _I32),
+         _opt(parent, "parent", dev, (R, None), _I32)]
+    if out is None:
+        out = dict(row_off=torch.empty(R + 1, dtype=_I32, device=dev))
+        for k in ("req", "position", "slot"):
+            out[k] = torch.empty(rows, dtype=_I32, device=dev)
+        if parent is not None:
+            out["anc"] = torch.empty(rows, dtype=_I64, device=dev)
+    b = [_chk(out["row_off"], "row_off", dev, (R + 1,), _I32),
+         _opt(out.get("req"), "req", dev, (rows,), _I32),
+         _opt(out.get("position"), "position", dev, (rows,), _I32),
+         _chk(out["slot"], "slot", dev, (rows,), _I32),
+         None if parent is None else _chk(out["anc"], "anc", dev, (rows,), _I64),
+         _opt(status, "status", dev, (1,), _I32)]
+    if R == 0:
+        out["row_off"].zero_()
+        return out
+    ws, wp, wb = _workspace(cache_plan_workspace_bytes(R), dev, ws)
+    _call(dev, "dspark_cache_plan", R, rows, page_size, table.shape[1], free_pages.shape[0],
+          extra, *a, 0 if parent is None else parent.shape[1], *b, wp, wb)
+    return out
+
+
+def cache_append(k, v, k_cache, v_cache, slot, *, n_rows=None, status=None):
+    """Row i's keys and values (k, v [rows][Hkv][D], rows any stride apart, as slices of a
+    fused projection are) into cache slot slot[i] (-1: skipped).  n_rows: a device int32 [1];
+    rows at and behind it are skipped (a plan's row_off[-1:])."""
+    dev = _device(k, "k")
+    kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
+    rows = k.shape[0]
+    dt = _dt(k_cache, "k_cache")
+    a, b = (_chk(x, s, dev, (rows, Hkv, D), k_cache.dtype, False) for x, s in ((k, "k"), (v, "v")))
+    ks, vs = _strides(k, 2), _strides(v, 2)
+    if ks is None or vs is None:
+        raise ValueError("k and v must be dense within a row")
+    _call(dev, "dspark_cache_append", rows, Hkv, D, dt, page, P, a, b, ks[0], vs[0],
+          _chk(slot, "slot", dev, (rows,), _I32), _opt(n_rows, "n_rows", dev, (1,), _I32), kp, vp,
+          *st, _opt(status, "status", dev, (1,), _I32))
+
+
+def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt) -> int:
+    from . import lib
+    return int(lib().dspark_tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt))
+
+
+def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=None, out=None,
+                   ws=None, status=None):
+    """Attention of a step's packed rows q [rows][Hq][D] over the paged cache, their own keys
+    and values appended: every row sees its request's ctx tokens, the anchor (node 0), and of
+    the block's further nodes those up to its own (anc=None), or those whose bit is set in
+    anc [rows] int64 (a plan's).  scale: of the scores, default D ** -0.5.
+    Returns dict(o [rows][Hq][D], lse [rows][Hq] float32); a caller-supplied `out` may leave
+    "lse" out.  Rows behind row_off[-1] are left as they were."""
+    dev = _device(q, "q")
+    kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
+    dt = _dt(q, "q")
+    qp = _chk(q, "q", dev, (None, None, D), k_cache.dtype, False)
+    rows, Hq = q.shape[0], q.shape[1]
+    qs = _strides(q, 2)
+    if qs is None:
+        raise ValueError("q must be dense within a row")
+    tp = _chk(table, "table", dev, (None, None), _I32)
+    R = table.shape[0]
+    a = [tp, _chk(ctx, "ctx", dev, (R,), _I32), _chk(row_off, "row_off", dev, (R + 1,), _I32),
+         _opt(anc, "anc", dev, (rows,), _I64)]
+    if out is None:
+        out = dict(o=torch.empty((rows, Hq, D), dtype=q.dtype, device=dev),
+                   lse=torch.empty((rows, Hq), dtype=_F32, device=dev))
+    b = [_chk(out["o"], "o", dev, (rows, Hq, D), q.dtype),
+         _opt(out.get("lse"), "lse", dev, (rows, Hq), _F32),
+         _opt(status, "status", dev, (1,), _I32)]
+    if R == 0 or rows == 0:
+        return out
+    if torch.cuda.current_device() == dev.index:
+        nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
+    else:  # the size goes by the device's compute units
+        with torch.cuda.device(dev):
+            nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
+    if nbytes == 0:
+        from . import EINVAL, DsparkError
+        raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
+    ws, wp, wb = _workspace(nbytes, dev, ws)
+    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, table.shape[1], P, qp,
+          qs[0], kp, vp, *st, *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
+    return out
+
+
+def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, prompt_len=None,
+                  rep=None, pres=None, freq=None, bias_id=None, bias=None, mask=None,
+                  mask_idx=None, out=None, status=None):
+    """The target's logits with each request's penalties, biases and grammar masks, in the
+    layout verify() takes: out [R][gamma+1][V], row j = 0..ell[q] following the anchor and
+    x[q][:j] (x [R][gamma]: the drafted tokens).
+    logits: packed [rows][V] with row_off [R+1] (a plan's), or [R][gamma+1][V] without; `out`
+    may be logits itself in the latter form.
+    hist [R][n] with hist_len [R], prompt_len [R]: each request's tokens, prompt first, anchor
+    included; rep divides positive and multiplies other logits of seen ids; pres and freq (times
+    the count) are taken off generated ids; bias_id, bias [R][nbias] (-1: unused; the last
+    entry for an id counts); mask [n][words] int32: bit v % 32 of word v // 32 allows id v, of
+    the mask mask_idx [R][gamma+1] names (-1: none; without mask_idx: mask q * (gamma + 1) + j);
+    other ids become -inf."""
+    dev = _device(logits, "logits")
+    dt = _dt(logits, "logits")
+    xp = _chk(x, "x", dev, (None, None), _I32)
+    R, gamma = x.shape
+    V = logits.shape[-1]
+    if row_off is None:
+        lp = _chk(logits, "logits", dev, (R, gamma + 1, V), logits.dtype)
+        rows, stride = R * (gamma + 1), V
+    else:
+        lp = _chk(logits, "logits", dev, (None, V), logits.dtype, False)
+        st = _strides(logits, 1)
+        if st is None:
+            raise ValueError("rows of logits must be contiguous")
+        rows, stride = logits.shape[0], max(st[0], V)
+    if out is None:
+        out = torch.empty((R, gamma + 1, V), dtype=logits.dtype, device=dev)
+    op = _chk(out, "out", dev, (R, gamma + 1, V), logits.dtype)
+    n_hist = nb = n_mask = words = 0
+    if hist is not None:
+        if hist_len is None:
+            raise ValueError("hist needs hist_len")
+        n_hist = hist.shape[-1]
+    if (bias is None) != (bias_id is None):
+        raise ValueError("bias and bias_id come together")
+    if bias is not None:
+        nb = bias.shape[-1]
+    if mask is not None:
+        n_mask, words = mask.shape[0], mask.shape[-1]
+        if mask_idx is None and n_mask < R * (gamma + 1):
+            raise ValueError("without mask_idx there is a mask for every row")
+    per = (R,)
+    _call(dev, "dspark_target_logits", R, gamma, V, dt, lp, stride, rows,
+          _opt(row_off, "row_off", dev, (R + 1,), _I32), _chk(ell, "ell", dev, per, _I32), xp,
+          _opt(hist, "hist", dev, (R, n_hist), _I32), n_hist,
+          _opt(hist_len, "hist_len", dev, per, _I32),
+          _opt(prompt_len, "prompt_len", dev, per, _I32), _opt(rep, "rep", dev, per, _F32),
+          _opt(pres, "pres", dev, per, _F32), _opt(freq, "freq", dev, per, _F32),
+          _opt(bias_id, "bias_id", dev, (R, nb), _I32), _opt(bias, "bias", dev, (R, nb), _F32), nb,
+          _opt(mask, "mask", dev, (n_mask, words), _I32), n_mask, words,
+          _opt(mask_idx, "mask_idx", dev, (R, gamma + 1), _I32), op,
+          _opt(status, "status", dev, (1,), _I32))
+    return out
+
+
+def cache_commit_workspace_bytes(R) -> int:
+    from . import lib
+    return int(lib().dspark_cache_commit_workspace_bytes(R))
+
+
+def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path=None, done=None,
+                 k_cache=None, v_cache=None, out=None, ws=None, status=None):
+    """After verification: the lengths with the anchor and the n_acc accepted nodes of each
+    request committed ([R] int32; `out` may be ctx itself).  path [R][gamma] (trees): the
+    accepted nodes, ascending; their keys and values move to the places behind the anchor, in
+    the caches ([n_pages][Hkv][page_size][D], or with a leading layer dimension).  done [R]:
+    finished requests (nonzero) give their pages back: free_pages and n_free grow, held and
+    the length become 0."""
+    dev = _device(n_acc, "n_acc")
+    R = n_acc.shape[0]
+    a = [_chk(n_acc, "n_acc", dev, (R,), _I32), _opt(path, "path", dev, (R, None), _I32),
+         _opt(done, "done", dev, (R,), _I32), _chk(ctx, "ctx", dev, (R,), _I32)]
+    if out is None:
+        out = torch.empty(R, dtype=_I32, device=dev)
+    b = [_chk(out, "out", dev, (R,), _I32), _chk(held, "held", dev, (R,), _I32),
+         _chk(table, "table", dev, (R, None), _I32),
+         _chk(free_pages, "free_pages", dev, (None,), _I32),
+         _chk(n_free, "n_free", dev, (1,), _I32)]
+    c = [0, 0, 0, 0, 0, None, None, 0, 0, 0, 0]
+    if path is not None:
+        if k_cache is None or v_cache is None:
+            raise ValueError("a path needs the caches")
+        kp, vp, shape, st = _cache(k_cache, v_cache, dev, 5 if k_cache.dim() == 5 else 4)
+        if len(shape) == 4:
+            shape, st = (1, *shape), [0, *st]
+        if shape[3] != page_size:
+            raise ValueError(f"the caches have pages of {shape[3]} tokens, expected {page_size}")
+        c = [shape[0], shape[2], shape[4], _dt(k_cache, "k_cache"), shape[1], kp, vp, *st]
+    sp = _opt(status, "status", dev, (1,), _I32)
+    if R == 0:
+        return out
+    ws, wp, wb = _workspace(cache_commit_workspace_bytes(R), dev, ws)
+    _call(dev, "dspark_cache_commit", R, 0 if path is None else path.shape[1], page_size,
+          table.shape[1], free_pages.shape[0], *a, *b, *c, sp, wp, wb)
+    return out

@@ -1,0 +1,338 @@
+"""cache_plan, cache_append and cache_commit against their definitions (exact: integers and
+copies), at the sizes, orders and faults where they can go wrong."""
+import numpy as np
+import pytest
+import torch
+
+from tests import target_ref as ref
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def T(x, dtype=I32):
+    return torch.tensor(x, dtype=dtype, device="cuda:0")
+
+
+def case(seed, R, gamma, page, ctx_hi, spare, tree=False, width=None):
+    g = np.random.default_rng(seed)
+    ctx = g.integers(0, ctx_hi + 1, R).tolist()
+    lens = g.integers(0, gamma + 1, R).tolist()
+    held = [ref.cdiv(c, page) for c in ctx]
+    W = max(ref.cdiv(c + gamma + 1, page) for c in ctx) + 1
+    order = g.permutation(sum(held) + spare).tolist()
+    table, at = [], 0
+    for h in held:
+        table.append(order[at:at + h] + [-7] * (W - h))
+        at += h
+    parent = None
+    if tree:
+        parent = [[int(g.integers(0, max(i, 1))) for i in range(width or gamma + 1)] for _ in range(R)]
+    return dict(ctx=ctx, lens=lens, held=held, table=table, free=order[at:] or [0], n_free=spare,
+                parent=parent)
+
+
+def run_plan(c, page, rows, extra=1, ws=None):
+    import draft_sampling_scheduling_amd as ds
+    d = {k: T(c[k]) for k in ("ctx", "lens", "held", "table", "free")}
+    d["n_free"] = T([c["n_free"]])
+    parent = None if c["parent"] is None else T(c["parent"])
+    st = T([0])
+    out = dict(row_off=torch.full((len(c["ctx"]) + 1,), -9, dtype=I32, device="cuda:0"))
+    for k in ("req", "position", "slot"):
+        out[k] = torch.full((rows,), -9, dtype=I32, device="cuda:0")
+    if parent is not None:
+        out["anc"] = torch.full((rows,), -9, dtype=torch.int64, device="cuda:0")
+    for _ in range(2):  # a step planned again changes nothing
+        ds.cache_plan(d["lens"], d["ctx"], d["held"], d["table"], d["free"], d["n_free"], page,
+                      rows=rows, extra=extra, parent=parent, out=out, ws=ws, status=st)
+        if int(st) & ds.FAULT_PAGE:
+            break  # a second try may serve others from what is left
+    table = [list(r) for r in c["table"]]
+    want, bits = ref.plan(c["lens"], c["ctx"], c["held"], table, c["free"], c["n_free"], page, rows,
+                          extra, c["parent"])
+    got = {k: v.tolist() for k, v in out.items()}
+    n = want["row_off"][-1]
+    assert got["row_off"] == want["row_off"]
+    for k in out:
+        if k != "row_off":
+            assert got[k][:n] == want[k], k
+            assert got[k][n:] == [-9] * (rows - n), k  # rows of nobody stay as they were
+    assert d["table"].tolist() == table
+    assert d["held"].tolist() == want["held"] and d["n_free"].tolist() == [want["n_free"]]
+    assert int(st) == bits
+    return want, bits
+
+
+@pytest.mark.parametrize("R,gamma,page,ctx_hi,tree", [
+    (1, 1, 8, 0, False), (1, 64, 8, 3, True), (4, 4, 16, 200, False), (37, 8, 16, 700, True),
+    (257, 3, 64, 5000, False), (512, 16, 16, 8192, True), (1300, 2, 1024, 4000, False),
+    (3000, 1, 8, 60, True)])
+def test_plan(R, gamma, page, ctx_hi, tree):
+    c = case(R + gamma, R, gamma, page, ctx_hi, R * (ref.cdiv(gamma + 1, page) + 1), tree)
+    want, bits = run_plan(c, page, R * (gamma + 1))
+    assert bits == 0 and want["row_off"][-1] == sum(c["lens"]) + R
+
+
+def test_plan_prompts():
+    """Pieces of prompts beside requests that bring nothing (extra = 0)."""
+    c = case(5, 9, 4, 16, 100, 900)
+    c["lens"] = [0, 2000, 1, 0, 777, 0, 4096, 16, 0]
+    c["table"] = [r + [-7] * 300 for r in c["table"]]
+    want, bits = run_plan(c, 16, 7000, extra=0)
+    assert bits == 0 and want["row_off"][-1] == sum(c["lens"])
+
+
+def test_plan_sits_out():
+    c = case(6, 5, 4, 16, 50, 30)
+    c["lens"] = [3, -1, 0, -1, 4]
+    _, bits = run_plan(c, 16, 25)
+    assert bits == 0
+
+
+@pytest.mark.parametrize("spare", [0, 1, 3, 7])
+def test_plan_out_of_pages(spare):
+    """Those whose pages are had are served, those that need none too, the others not."""
+    c = case(7, 40, 12, 8, 90, spare)
+    want, bits = run_plan(c, 8, 40 * 13)
+    assert bits == 8 and 0 <= want["n_free"] <= spare
+    assert want["row_off"][-1] > 0 or spare == 0
+
+
+@pytest.mark.parametrize("rows", [0, 1, 17, 60])
+def test_plan_out_of_rows(rows):
+    c = case(8, 20, 6, 16, 300, 100)
+    want, bits = run_plan(c, 16, rows)
+    assert bits == 4 and want["row_off"][-1] <= rows
+
+
+def test_plan_faults():
+    c = case(9, 12, 6, 16, 300, 60, tree=True)
+    W = len(c["table"][0])
+    c["ctx"][0] = -1                      # refused
+    c["lens"][1] = -5                     # refused
+    c["held"][2] = W + 1                  # refused
+    c["held"][3] = -1                     # refused
+    c["ctx"][4] = W * 16 - 1              # passes its table
+    c["lens"][4] = 6
+    c["lens"][5], c["parent"][5][3] = 6, 3      # a node above itself: counts as 2
+    c["lens"][6], c["parent"][6][1] = 6, -2
+    c["ctx"][7], c["lens"][7], c["held"][7] = 40, 3, 3
+    c["table"][7][:3] = [5, 6, -1]              # its rows' page is unknown: slots -1
+    c["lens"][8] = 2 ** 31 - 1            # no row count: refused
+    _, bits = run_plan(c, 16, 12 * 7)
+    assert bits == 4 | 8 | 16
+
+
+def test_plan_page_ids_past_the_slots():
+    c = case(10, 2, 2, 1024, 100, 4)
+    c["lens"] = [2, 2]
+    c["table"][1][0] = (1 << 21) - 1      # its last slot is 2^31 - 1
+    c["table"][0][0] = 1 << 21            # its slots pass 31 bits
+    c["held"] = [1, 1]
+    want, bits = run_plan(c, 1024, 6)
+    assert bits == 8 and want["slot"][:3] == [-1] * 3 and min(want["slot"][3:]) > 2 ** 31 - 1025
+
+
+def test_plan_widths():
+    """A tree of 65 nodes uses all 64 bits of a mask; one of 66 is refused."""
+    c = case(11, 2, 65, 16, 20, 40, tree=True)
+    c["lens"] = [64, 65]
+    c["parent"] = [[max(i - 1, 0) for i in range(66)] for _ in range(2)]
+    want, bits = run_plan(c, 16, 140)
+    assert bits == 4 and want["row_off"] == [0, 65, 65] and want["anc"][64] == -1
+
+
+def test_plan_n_free_clamped():
+    import draft_sampling_scheduling_amd as ds
+    st = T([0])
+    for bad, left in ((-3, 0), (9, 3)):
+        held, nf, table = T([0]), T([bad]), T([[-1, -1]])
+        p = ds.cache_plan(T([3]), T([0]), held, table, T([4, 5, 6, 7]), nf, 8, rows=4, extra=1,
+                          status=st.zero_())
+        assert int(st) == ds.FAULT_PAGE and nf.tolist() == [left]
+        assert p["row_off"].tolist() == ([0, 0] if bad < 0 else [0, 4])
+        assert table.tolist() == ([[-1, -1]] if bad < 0 else [[7, -1]])
+
+
+# ----------------------------------------------------------------------------------------
+# append
+# ----------------------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,Hq,Hkv,D,page,dtype,layout", [
+    (1, 1, 1, 8, 8, torch.bfloat16, "phtd"), (20, 4, 2, 64, 16, torch.float32, "phtd"),
+    (577, 20, 4, 128, 16, torch.bfloat16, "pthd"), (300, 2, 2, 1024, 32, torch.float32, "pthd"),
+    (1000, 8, 8, 72, 128, torch.bfloat16, "phtd")])
+def test_append(rows, Hq, Hkv, D, page, dtype, layout):
+    import draft_sampling_scheduling_amd as ds
+    g = np.random.default_rng(rows)
+    P = ref.cdiv(rows, page) + 3
+    shape = (P, Hkv, page, D) if layout == "phtd" else (P, page, Hkv, D)
+    kc, vc = (torch.from_numpy(g.standard_normal(shape, np.float32)).to(dtype) for _ in range(2))
+    qkv = torch.from_numpy(g.standard_normal((rows, Hq + 2 * Hkv, D), np.float32)).to(dtype)
+    slot = g.permutation(P * page)[:rows].astype(np.int32)
+    slot[g.random(rows) < 0.1] = -1
+    bad = slot.copy()
+    if rows > 10:
+        bad[3], bad[5], bad[6] = P * page, -2, 2 ** 31 - 1
+    live = rows - rows // 7
+    dk, dv, dq = kc.to("cuda:0"), vc.to("cuda:0"), qkv.to("cuda:0")
+    views = [x if layout == "phtd" else x.transpose(1, 2) for x in (dk, dv)]
+    st = T([0])
+    ds.cache_append(dq[:, Hq:Hq + Hkv], dq[:, Hq + Hkv:], *views, T(bad.tolist()),
+                    n_rows=T([live]), status=st)
+    for c, x in ((kc, qkv[:, Hq:Hq + Hkv]), (vc, qkv[:, Hq + Hkv:])):
+        y = c if layout == "phtd" else c.transpose(1, 2)
+        for i in range(live):
+            if 0 <= bad[i] < P * page:
+                y[bad[i] // page, :, bad[i] % page] = x[i]
+    assert torch.equal(dk.cpu(), kc) and torch.equal(dv.cpu(), vc)
+    assert int(st) == (ds.FAULT_PAGE if rows > 10 else 0)
+    for n in (0, -4, 2 ** 31 - 1):  # a count of rows that is none, or past them
+        ds.cache_append(dq[:, Hq:Hq + Hkv], dq[:, Hq + Hkv:], *views, T([-1] * rows), n_rows=T([n]))
+    assert torch.equal(dk.cpu(), kc)
+
+
+def test_append_refuses():
+    import draft_sampling_scheduling_amd as ds
+    k = torch.zeros(4, 2, 64, device="cuda:0")
+    c = torch.zeros(3, 2, 16, 64, device="cuda:0")
+    s = T([0, 1, 2, 3])
+    ds.cache_append(k, k, c, c.clone(), s)
+    for a in ((k.half(), k, c, c, s), (k, k, c, c.bfloat16(), s), (k, k, c, c, s.long()),
+              (k.bfloat16(), k.bfloat16(), c, c, s)):
+        with pytest.raises(TypeError):
+            ds.cache_append(*a)
+    for a in ((k[:, :1], k, c, c, s), (k, k, c, c[:2], s), (k, k, c, c, s[:3]),
+              (k.transpose(1, 2).contiguous().transpose(1, 2), k, c, c, s),
+              (k, k, c, torch.zeros(3, 16, 2, 64, device="cuda:0").transpose(1, 2), s),
+              (k, k, c, c.cpu(), s), (k, k, c[0], c[0], s)):
+        with pytest.raises(ValueError):
+            ds.cache_append(*a)
+    with pytest.raises(ds.DsparkError):
+        c = torch.zeros(3, 2, 12, 64, device="cuda:0")
+        ds.cache_append(k, k, c, c.clone(), s)
+
+
+# ----------------------------------------------------------------------------------------
+# commit
+# ----------------------------------------------------------------------------------------
+def commit_ref(c, n_acc, path, done, page, caches, free_len, P):
+    """By the definition, on lists and host caches [layers][P][Hkv][page][D]."""
+    LEN, PAGE, TREE = 4, 8, 16
+    bits, ctx_out, held = 0, [], list(c["held"])
+    free, nf = list(c["free"]), c["n_free"]
+    for q in range(len(n_acc)):
+        W = len(c["table"][q])
+        if not 0 <= held[q] <= W:
+            bits |= LEN
+        h = min(max(held[q], 0), W)
+        if done and done[q]:
+            for p in c["table"][q][:h]:
+                if nf < free_len:
+                    free[nf] = p
+                    nf += 1
+                else:
+                    bits |= PAGE
+            held[q] = 0
+            ctx_out.append(0)
+            continue
+        cx = c["ctx"][q]
+        na = min(n_acc[q], len(path[q]) if path else n_acc[q], max(-1, h * page - cx - 1))
+        na = max(na, -1)
+        if na != n_acc[q]:
+            bits |= LEN
+        ctx_out.append(cx + na + 1)
+        if not path:
+            continue
+        moves, last = [], 0
+        for i in range(1, na + 1):
+            p = path[q][i - 1]
+            if p <= last or cx + p >= h * page:
+                bits |= TREE
+                break
+            last = p
+            if p == i:
+                continue
+            ps, pd = (c["table"][q][(cx + k) // page] for k in (p, i))
+            if not (0 <= ps < P and 0 <= pd < P):
+                bits |= PAGE
+                continue
+            moves.append((ps, (cx + p) % page, pd, (cx + i) % page))
+        for x in caches:
+            old = [x[:, a, :, b].clone() for a, b, _, _ in moves]
+            for y, (_, _, a, b) in zip(old, moves):
+                x[:, a, :, b] = y
+    return ctx_out, held, free, nf, bits
+
+
+def run_commit(seed, R, gamma, page, ctx_hi, layers, Hkv, D, dtype, tree, change=None, P_known=None,
+               free_len=None, in_place=False):
+    import draft_sampling_scheduling_amd as ds
+    g = np.random.default_rng(seed)
+    c = case(seed, R, gamma, page, ctx_hi, 3)
+    c["held"] = [ref.cdiv(x + gamma + 1, page) for x in c["ctx"]]
+    P = sum(c["held"]) + 3
+    order, at = g.permutation(P).tolist(), 0
+    for q, h in enumerate(c["held"]):
+        c["table"][q][:h] = order[at:at + h]
+        at += h
+    n_acc = g.integers(-1, gamma + 1, R).tolist()
+    path = [sorted((g.permutation(gamma) + 1).tolist()[:max(k, 0)]) + [0] * (gamma - max(k, 0))
+            for k in n_acc] if tree else None
+    done = (g.random(R) < 0.3).astype(int).tolist()
+    c["free"] = order[at:] + [-5] * (P - 3)
+    free_len = len(c["free"]) if free_len is None else free_len
+    c["free"] = c["free"][:free_len]
+    if change:
+        change(c, n_acc, path, done)
+    caches = [torch.from_numpy(g.standard_normal((layers, P, Hkv, page, D), np.float32)).to(dtype)
+              for _ in range(2)]
+    dc = [x.to("cuda:0") for x in caches]
+    if layers == 1:
+        dc = [x[0] for x in dc]
+    st = T([0])
+    ctx, held, free, nf = T(c["ctx"]), T(c["held"]), T(c["free"]), T([c["n_free"]])
+    known = P if P_known is None else P_known
+    view = [x[..., :known, :, :, :] for x in dc] if tree else [None, None]
+    out = ds.cache_commit(T(n_acc), ctx, held, T(c["table"]), free, nf, page,
+                          path=T(path) if tree else None, done=T(done), k_cache=view[0],
+                          v_cache=view[1], out=ctx if in_place else None, status=st)
+    want = commit_ref(c, n_acc, path, done, page, caches, free_len, known)
+    assert out.tolist() == want[0] and held.tolist() == want[1]
+    assert free.tolist() == want[2] and nf.tolist() == [want[3]] and int(st) == want[4]
+    for a, b in zip(dc, caches):
+        assert torch.equal(a.cpu().view(b.shape), b)
+    return want
+
+
+@pytest.mark.parametrize("R,gamma,page,ctx_hi,layers,Hkv,D,dtype,tree", [
+    (1, 1, 8, 0, 1, 1, 8, torch.float32, True), (4, 4, 16, 200, 2, 2, 64, torch.float32, False),
+    (64, 8, 16, 256, 4, 4, 128, torch.bfloat16, True), (9, 64, 8, 100, 3, 1, 72, torch.bfloat16, True),
+    (3, 33, 64, 70, 1, 8, 256, torch.float32, True), (1500, 2, 16, 30, 1, 1, 64, torch.bfloat16, True)])
+def test_commit(R, gamma, page, ctx_hi, layers, Hkv, D, dtype, tree):
+    want = run_commit(R, R, gamma, page, ctx_hi, layers, Hkv, D, dtype, tree, in_place=R % 2 == 0)
+    assert want[4] == 0
+
+
+def test_commit_faults():
+    def change(c, n_acc, path, done):
+        done[:8] = [0] * 8
+        n_acc[:8] = [9, -4, 6, 6, 6, 3, 8, 2]     # past gamma, below -1
+        path[0] = list(range(1, 9))
+        path[2] = [1, 2, 2, 5, 6, 8, 0, 0]        # does not ascend
+        path[3] = [0, 2, 3, 4, 5, 6, 7, 8]        # node 0 is the anchor
+        path[4] = [2, 4, 5, 6, 7, 900, 0, 0]      # past the pages held
+        path[5] = [3, 5, 8, 0, 0, 0, 0, 0]
+        c["table"][5][c["ctx"][5] // 8] = -1      # an unknown page
+        c["held"][6] = len(c["table"][6]) + 2
+        path[6] = list(range(1, 9))
+        c["held"][7] = 0                          # nothing fits
+        path[7] = [1, 2] + [0] * 6
+
+    want = run_commit(3, 12, 8, 8, 90, 2, 2, 64, torch.bfloat16, True, change)
+    assert want[4] & 4 and want[4] & 8 and want[4] & 16
+
+
+def test_commit_pages_past_the_pool_and_the_list():
+    assert run_commit(4, 10, 6, 8, 60, 1, 2, 64, torch.bfloat16, True, P_known=20)[4] & 8
+    assert run_commit(5, 10, 6, 8, 60, 1, 2, 64, torch.bfloat16, False, free_len=5)[4] & 8
