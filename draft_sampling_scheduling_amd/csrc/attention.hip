@@ -32,7 +32,16 @@ constexpr int kAttThreads = kAttWaves * kWave;
 constexpr int kTok = 32;                     // tokens of a wave's tile
 constexpr int kRound = kAttWaves * kTok;     // tokens of a round
 constexpr int kStages = 2;
+constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+// A row tile whose list is cut (see attention_kernel): its pieces lie with workgroups b - 1 ..
+// b - 2 + count, in slot 0 of each but the first's, which is slot `slot`.
+struct AttJoint {
+  int a, M, head, tile;  // first row and query rows of the request, cache head, row tile
+  int count, slot;       // count 0: nothing to join
+  int pad[2];
+};
 
 struct AttParams {
   int R, rows, Hq, Hkv, G;  // G = Hq / Hkv
@@ -48,7 +57,7 @@ struct AttParams {
   float* lse;
   int32_t* status;
   float* part;   // [grid][2][MR][D + 2]: O, then m, then l of each row
-  int4* joint;   // [grid] what the second kernel joins (see AttJoint)
+  AttJoint* joint;  // [grid] what the second kernel joins
 };
 
 // a request's rows and tokens, as the host of the data should have them, clamped
@@ -168,7 +177,8 @@ struct AttWave {
   int node[MT];             // chain: the lane's node
   // state
   f32x16 o[MT][ND];
-  float m[MT], l[MT];       // m: the largest score so far times scale * log2(e)
+  float m[MT], l[MT];       // m: what o and l are relative to, about the largest score so
+                            // far, times scale * log2(e)
 
   __device__ __forceinline__ AttWave(const AttParams& p_, uint32_t base_)
       : p(p_), lane(threadIdx.x & 63), n(lane & 31), h(lane >> 5), base(base_) {}
@@ -234,10 +244,13 @@ struct AttWave {
 #pragma unroll
       for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[mt][r]);
       mx = half_max(mx);
-      const float mn = fmaxf(m[mt], mx * c2);
-      const float ref = mn == -INFINITY ? 0.0f : mn;
-      if (__ballot(mn > m[mt])) {  // some row's maximum grew: what is summed so far shrinks
-        const float f = __builtin_amdgcn_exp2f(m[mt] - ref);
+      mx *= c2;
+      // O and l are relative to m, which follows the maximum only once that is 2^kSlack past
+      // it: weights of up to 2^kSlack lose nothing in float or bf16, and the rescaling of O,
+      // half a tile's arithmetic, falls away on nearly all tiles
+      if (__ballot(mx > m[mt] + kSlack)) {
+        const float mn = fmaxf(m[mt], mx);
+        const float f = __builtin_amdgcn_exp2f(m[mt] - (mn == -INFINITY ? 0.0f : mn));
         l[mt] *= f;
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt)
@@ -245,6 +258,7 @@ struct AttWave {
           for (int r = 0; r < 16; ++r) o[mt][dt][r] *= f;
         m[mt] = mn;
       }
+      const float ref = m[mt] == -INFINITY ? 0.0f : m[mt];
       float sum = 0.0f;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -434,52 +448,71 @@ struct AttWave {
   }
 };
 
-// One segment of a workgroup's share, as the second kernel finds it: a row tile whose list is
-// cut has its pieces at workgroups first .. first + count - 1, in slot 0 (their first
-// segment), but for the first piece, which may be its workgroup's last (slot 1).
-//   joint[b] = (q, head, row tile, count | slot of the first piece << 30), first = b - 1;
-//   count 0: nothing to join
+// Where the rounds of a head go.  Each row tile of each request has a list of kSetup + rounds
+// units, kSetup of them for what a list costs beside its tokens (the queries, the first
+// tile's wait, the merge of the waves; about 8 us where a round takes 3 us with all CUs
+// streaming), which no tokens stand for; all lists, head after head, are one row of
+// units, cut evenly: workgroup b takes share units, the first `more` workgroups one more.
+// A list that is cut has its pieces in the workspace; the first workgroup that begins inside
+// one says so in joint[b].
+constexpr int kSetup = 3;
+
+struct AttShares {
+  int64_t share, more;
+  __device__ __forceinline__ int64_t begin(int64_t b) const {
+    return b * share + (b < more ? b : more);
+  }
+  __device__ __forceinline__ int64_t owner(int64_t u) const {
+    const int64_t big = more * (share + 1);
+    return u < big ? u / (share + 1) : more + (u - big) / share;
+  }
+};
+
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(kAttThreads, 1) attention_kernel(AttParams p) {
   using L = Tile<T, D>;
   constexpr int MR = 32 * MT, ND = D / 32;
   extern __shared__ uint4 lds[];
   __shared__ int64_t sums[kAttWaves];
-  __shared__ int64_t total_s;
-  __shared__ int start_s;
-  __shared__ int64_t start_off;
+  __shared__ int64_t total_s, start_off;
+  __shared__ int start_s[4];
   const int tid = threadIdx.x, wave = uni(tid >> 6);
   const int b = blockIdx.x;
 
-  // the list of rounds: per head, request after request, row tile after row tile
+  auto list = [&](const AttReq& r) -> int64_t {
+    return (r.ctx + r.n + kRound - 1) / kRound + kSetup;
+  };
   auto units = [&](const AttReq& r) -> int64_t {
-    return (int64_t)((r.n * p.G + MR - 1) / MR) * ((r.ctx + r.n + kRound - 1) / kRound);
+    return r.n > 0 ? (int64_t)((r.n * p.G + MR - 1) / MR) * list(r) : 0;
   };
   const int per = (p.R + kAttThreads - 1) / kAttThreads;
   const int lo = min(p.R, tid * per), hi = min(p.R, lo + per);
   int64_t mine = 0;
-  for (int q = lo; q < hi; ++q) {
-    const AttReq r = att_req(p, q, b == 0);
-    mine += r.n > 0 ? units(r) : 0;
-  }
+  for (int q = lo; q < hi; ++q) mine += units(att_req(p, q, b == 0));
   const int64_t upto = block_scan<kAttThreads>(mine, sums);
   if (tid == kAttThreads - 1) total_s = upto;
+  if (tid == 0) p.joint[b].count = 0;
   __syncthreads();
   const int64_t W = uni(total_s), U = W * p.Hkv;
   const int64_t P = U < gridDim.x ? U : gridDim.x;
-  if (tid == 0) p.joint[b] = make_int4(0, 0, 0, 0);
   if (b >= P) return;
-  const int64_t u0 = U * b / P, u1 = U * (b + 1) / P;
+  AttShares cut;
+  cut.share = U / P;
+  cut.more = U - cut.share * P;
+  const int64_t u0 = cut.begin(b), u1 = cut.begin(b + 1);
   int head = (int)(u0 / W);
   {
-    const int64_t w = u0 % W;
-    if (w >= upto - mine && w < upto) {
-      int64_t at = upto - mine;
+    const int64_t w = u0 - head * W;
+    int64_t at = upto - mine;
+    if (w >= at && w < upto) {
       for (int q = lo; q < hi; ++q) {
         const AttReq r = att_req(p, q, false);
-        const int64_t x = r.n > 0 ? units(r) : 0;
+        const int64_t x = units(r);
         if (w < at + x) {
-          start_s = q;
+          start_s[0] = q;
+          start_s[1] = r.a;
+          start_s[2] = r.n;
+          start_s[3] = r.ctx;
           start_off = w - at;
           break;
         }
@@ -488,166 +521,198 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_kernel(AttParams p) 
     }
   }
   __syncthreads();
-  int q = uni(start_s);
-  int64_t off = uni(start_off);  // rounds of q's list before this workgroup's
+  int q = uni(start_s[0]);
+  AttReq rq = {uni(start_s[1]), uni(start_s[2]), uni(start_s[3])};
+  int64_t off = uni(start_off);  // units of q's lists before this workgroup's
 
   const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
   AttWave<T, D, MT> wv(p, base + wave * kStages * 2 * L::BYTES);
   for (int64_t u = u0; u < u1;) {
-    AttReq rq = att_req(p, q, false);
-    rq.a = uni(rq.a);
-    rq.n = uni(rq.n);
-    rq.ctx = uni(rq.ctx);
-    const int64_t rounds = (rq.ctx + rq.n + kRound - 1) / kRound;
-    const int64_t tiles = (rq.n * p.G + MR - 1) / MR;
-    if (rq.n == 0 || off >= tiles * rounds) {  // on to the next request, or the next head
+    if (off >= units(rq)) {  // on to the next request, or the next head
       off = 0;
       if (++q == p.R) {
         q = 0;
         ++head;
       }
+      rq = att_req(p, q, false);
+      rq = {uni(rq.a), uni(rq.n), uni(rq.ctx)};
       continue;
     }
-    const int mt0 = (int)(off / rounds), r0 = (int)(off % rounds);
-    const int nr = (int)(u1 - u < rounds - r0 ? u1 - u : rounds - r0);
+    const int64_t len = list(rq);
+    const int mt0 = (int)(off / len), at = (int)(off - mt0 * len);
+    const int64_t left = u1 - u;
+    const int n = left < len - at ? (int)left : (int)(len - at);
+    const int r0 = at > kSetup ? at - kSetup : 0;  // rounds r0 .. r0 + nr
+    const int nr = at + n - kSetup - r0, rounds = (int)len - kSetup;
+    const int64_t first_u = u;
+    u += n;
+    off += n;
+    if (nr <= 0) continue;
     wv.segment(rq, q, head, mt0 * MR, r0, nr, wave);
 
-    // the second wave's sums into the first's, through LDS
-    __syncthreads();
+    // The waves' sums, through LDS: each gives the other half of its O, and finishes its own
+    // half.
+    constexpr int HD = ND / 2, kGive = (MT * HD * 16 + 2 * MT) * 64;
     float* x = reinterpret_cast<float*>(lds);
     const int lane = tid & 63;
-    if (wave == 1) {
+    auto give = [&](auto self) {
+      constexpr int W = decltype(self)::value;
+      float* y = x + W * kGive + lane;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt)
+        for (int i = 0; i < HD; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) x[((mt * ND + dt) * 16 + r) * 64 + lane] = wv.o[mt][dt][r];
-        x[(MT * ND * 16 + 2 * mt) * 64 + lane] = wv.m[mt];
-        x[(MT * ND * 16 + 2 * mt + 1) * 64 + lane] = wv.l[mt];
+          for (int r = 0; r < 16; ++r)
+            y[((mt * HD + i) * 16 + r) * 64] = wv.o[mt][(1 - W) * HD + i][r];
+        y[(MT * HD * 16 + 2 * mt) * 64] = wv.m[mt];
+        y[(MT * HD * 16 + 2 * mt + 1) * 64] = wv.l[mt];
       }
-    }
-    __syncthreads();
-    const bool whole = r0 == 0 && nr == rounds;
-    if (wave == 0) {
+    };
+    auto finish = [&](auto self) {
+      constexpr int W = decltype(self)::value;
+      const float* y = x + (1 - W) * kGive + lane;
+      const bool whole = r0 == 0 && nr == rounds;
       const int M = rq.n * p.G;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const float m2 = x[(MT * ND * 16 + 2 * mt) * 64 + lane];
-        const float l2 = x[(MT * ND * 16 + 2 * mt + 1) * 64 + lane];
+        const float m2 = y[(MT * HD * 16 + 2 * mt) * 64], l2 = y[(MT * HD * 16 + 2 * mt + 1) * 64];
         const float mm = fmaxf(wv.m[mt], m2);
         const float ref = mm == -INFINITY ? 0.0f : mm;
-        const float f1 = __builtin_amdgcn_exp2f(wv.m[mt] - ref);
-        const float f2 = __builtin_amdgcn_exp2f(m2 - ref);
+        float f1 = __builtin_amdgcn_exp2f(wv.m[mt] - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
         const float ll = wv.l[mt] * f1 + l2 * f2;
         const int row = 32 * mt + wv.n, mi = mt0 * MR + row;
         if (mi >= M) continue;
-        const int i = mi / p.G, a = head * p.G + mi % p.G;
+        const int64_t at = (int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G;
+        const int slot = first_u == u0 ? 0 : 1;
+        float* part = p.part + ((int64_t)b * 2 + slot) * MR * (D + 2);
         if (whole) {
           const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-          T* out = static_cast<T*>(p.o) + ((int64_t)(rq.a + i) * p.Hq + a) * D;
+          f1 *= inv;
+          f2 *= inv;
+        }
 #pragma unroll
-          for (int dt = 0; dt < ND; ++dt)
+        for (int i = 0; i < HD; ++i)
 #pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-              f32x4 y;
+          for (int r4 = 0; r4 < 4; ++r4) {
+            f32x4 z;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = 4 * r4 + e;
-                y[e] = (wv.o[mt][dt][r] * f1 + x[((mt * ND + dt) * 16 + r) * 64 + lane] * f2) * inv;
-              }
-              T* to = out + 32 * dt + 8 * r4 + 4 * wv.h;
-              if constexpr (L::kBf) {
-                bf16x4 z;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[e] = (__bf16)y[e];
-                *reinterpret_cast<bf16x4*>(to) = z;
-              } else {
-                *reinterpret_cast<f32x4*>(to) = y;
-              }
+            for (int e = 0; e < 4; ++e) {
+              const int r = 4 * r4 + e;
+              z[e] = wv.o[mt][W * HD + i][r] * f1 + y[((mt * HD + i) * 16 + r) * 64] * f2;
             }
-          if (p.lse && wv.h == 0)
-            p.lse[(int64_t)(rq.a + i) * p.Hq + a] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
-        } else {
-          const int slot = u == u0 ? 0 : 1;
-          float* part = p.part + ((int64_t)b * 2 + slot) * MR * (D + 2);
+            const int d = 32 * (W * HD + i) + 8 * r4 + 4 * wv.h;
+            if (!whole) {
+              *reinterpret_cast<f32x4*>(part + row * D + d) = z;
+            } else if constexpr (L::kBf) {
+              bf16x4 zb;
 #pragma unroll
-          for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-            for (int r4 = 0; r4 < 4; ++r4) {
-              f32x4 y;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const int r = 4 * r4 + e;
-                y[e] = wv.o[mt][dt][r] * f1 + x[((mt * ND + dt) * 16 + r) * 64 + lane] * f2;
-              }
-              *reinterpret_cast<f32x4*>(part + row * D + 32 * dt + 8 * r4 + 4 * wv.h) = y;
+              for (int e = 0; e < 4; ++e) zb[e] = (__bf16)z[e];
+              *reinterpret_cast<bf16x4*>(static_cast<T*>(p.o) + at * D + d) = zb;
+            } else {
+              *reinterpret_cast<f32x4*>(static_cast<T*>(p.o) + at * D + d) = z;
             }
-          if (wv.h == 0) {
+          }
+        if (W == 0 && wv.h == 0) {
+          if (!whole) {
             part[MR * D + row] = mm;
             part[MR * (D + 1) + row] = ll;
+          } else if (p.lse) {
+            p.lse[at] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
           }
         }
       }
-    }
-    if (tid == 0 && u == u0 && r0 > 0) {
-      // this workgroup begins inside the row tile's list [s, e): the first to do so says
-      // who holds its pieces
-      const int64_t s = u - r0, e = s + rounds;
-      const int64_t first = ((s + 1) * P - 1) / U, last = (e * P - 1) / U;
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, 1>;
+    __syncthreads();
+    if (wave == 0) give(First{});
+    else give(Second{});
+    __syncthreads();
+    if (wave == 0) finish(First{});
+    else finish(Second{});
+    if (tid == 0 && first_u == u0 && r0 > 0) {  // this workgroup begins inside a list
+      const int64_t s = first_u - r0;           // the list's first round
+      const int64_t first = cut.owner(s), last = cut.owner(s + rounds - 1);
       if (first == b - 1)
-        p.joint[b] = make_int4(q, head, mt0,
-                               (int)(last - first + 1) | (U * first / P >= s ? 0 : 1 << 30));
+        p.joint[b] = {rq.a, rq.n * p.G, head, mt0, (int)(last - first) + 1,
+                      cut.begin(first) >= s - kSetup ? 0 : 1, {0, 0}};
     }
     __syncthreads();  // LDS is the next segment's
-    u += nr;
-    off += nr;
   }
 }
 
-// Joins the pieces of the row tiles that are cut: a wave per row, pieces in order.
+// Joins the pieces of the row tiles that are cut: a wave per row, 16 bytes a lane, so that
+// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, eight loads in
+// flight; sums and maxima run over each lane's pieces and meet at the end, always in the
+// same order.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
-  constexpr int MR = 32 * MT, E = D / kWave;
+  constexpr int MR = 32 * MT, LP = D / 4, NP = kWave / LP, kBatch = 8;
   const int b = blockIdx.x;
-  const int4 jt = p.joint[b];
-  const int count = jt.w & 0x3fffffff;
-  if (count == 0) return;
+  const AttJoint jt = p.joint[b];
+  if (jt.count == 0) return;
   const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
-  const AttReq rq = att_req(p, jt.x, false);
-  const int mi = jt.z * MR + row;
-  if (mi >= rq.n * p.G) return;
-  const float* part0 = p.part + ((int64_t)(b - 1) * 2 + (jt.w >> 30)) * MR * (D + 2);
+  const int mi = jt.tile * MR + row;
+  if (mi >= jt.M) return;
+  const int mine = lane / LP, d = 4 * (lane % LP);
   auto piece = [&](int k) {
-    return k == 0 ? part0 : p.part + (int64_t)(b - 1 + k) * 2 * MR * (D + 2);
+    return p.part + ((int64_t)(b - 1 + k) * 2 + (k == 0 ? jt.slot : 0)) * MR * (D + 2);
   };
-  // the largest maximum, a lane per piece
-  float mx = -INFINITY;
-  for (int k = lane; k < count; k += kWave) mx = fmaxf(mx, piece(k)[MR * D + row]);
-  mx = wave_max(mx);
-  const float ref = mx == -INFINITY ? 0.0f : mx;
-  float acc[E], ll = 0.0f;
+  float m = -INFINITY, l = 0.0f;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = 0; k0 < jt.count; k0 += kBatch * NP) {
+    f32x4 x[kBatch];
+    float pm[kBatch], pl[kBatch];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-#pragma unroll 4
-  for (int k = 0; k < count; ++k) {
-    const float* x = piece(k);
-    const float f = __builtin_amdgcn_exp2f(x[MR * D + row] - ref);
-    ll = fmaf(x[MR * (D + 1) + row], f, ll);
+    for (int u = 0; u < kBatch; ++u) {  // pieces past the last: the last, with no weight
+      const int k = k0 + u * NP + mine;
+      const float* y = piece(k < jt.count ? k : jt.count - 1);
+      x[u] = *reinterpret_cast<const f32x4*>(y + row * D + d);
+      pm[u] = k < jt.count ? y[MR * D + row] : -INFINITY;
+      pl[u] = y[MR * (D + 1) + row];
+    }
+    float mn = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(x[row * D + E * lane + e], f, acc[e]);
+    for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, pm[u]);
+    const float ref = mn == -INFINITY ? 0.0f : mn;
+    float f = __builtin_amdgcn_exp2f(m - ref);
+    l *= f;
+    acc *= f;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      // where a piece has no weight its row stays out (0 * inf is none); its sum is finite, or
+      // NaN where the row's scores are
+      f = __builtin_amdgcn_exp2f(pm[u] - ref);
+      l = fmaf(pl[u], f, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? fmaf(x[u][e], f, acc[e]) : acc[e];
+    }
+    m = mn;
   }
-  const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
-  const int i = mi / p.G, a = jt.y * p.G + mi % p.G;
-  T* out = static_cast<T*>(p.o) + ((int64_t)(rq.a + i) * p.Hq + a) * D + E * lane;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    if constexpr (std::is_same<T, uint16_t>::value)
-      out[e] = __builtin_bit_cast(uint16_t, (__bf16)(acc[e] * inv));
-    else
-      out[e] = acc[e] * inv;
+  for (int w = LP; w < kWave; w *= 2) {  // the lanes that hold the same d
+    const float m2 = __shfl_xor(m, w, kWave), mm = fmaxf(m, m2);
+    const float ref = mm == -INFINITY ? 0.0f : mm;
+    const float f1 = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
+    l = l * f1 + __shfl_xor(l, w, kWave) * f2;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f1 + __shfl_xor(acc[e], w, kWave) * f2;
+    m = mm;
   }
-  if (p.lse && lane == 0) p.lse[(int64_t)(rq.a + i) * p.Hq + a] = (mx + __builtin_amdgcn_logf(ll)) * kLn2;
+  if (mine != 0) return;
+  acc *= l == 0.0f ? 0.0f : 1.0f / l;
+  const int64_t at = (int64_t)(jt.a + mi / p.G) * p.Hq + jt.head * p.G + mi % p.G;
+  T* out = static_cast<T*>(p.o) + at * D + d;
+  if constexpr (std::is_same<T, uint16_t>::value) {
+    bf16x4 z;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = (__bf16)acc[e];
+    *reinterpret_cast<bf16x4*>(out) = z;
+  } else {
+    *reinterpret_cast<f32x4*>(out) = acc;
+  }
+  if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -673,7 +738,7 @@ static int att_grid(int D, dspark_dtype dt) {
 static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
   Carve cv(ws);
   const size_t grid = (size_t)att_grid(D, dt);
-  p.joint = cv.take<int4>(grid);
+  p.joint = cv.take<AttJoint>(grid);
   p.part = cv.take<float>(grid * 2 * 32 * att_mt(R, rows, G, dt) * (D + 2));
   return cv.bytes();
 }

@@ -32,148 +32,209 @@ static PlanWs carve_plan(void* ws, int R) {
   return w;
 }
 
-// Rows and pages of every request: three scans (rows asked for, pages asked for by those
-// whose rows fit, rows granted), each request in its thread's consecutive run.  A request's
-// rows fit in a prefix of the requests that ask for any, and of those its pages are had in a
-// prefix of the ones that need any, so the exclusive sum of the needs is also the count of
-// pages handed out before it.
-__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(
-    int R, int rows, int lg, int max_pages, int free_len, int extra,
-    const int32_t* __restrict__ lens, const int32_t* __restrict__ ctx, int32_t* held,
-    int32_t* n_free, int tree_nodes, int32_t* row_off, PlanWs ws, int32_t* status) {
-  __shared__ int64_t sums[kPlanThreads / kWave];
-  const int per = (R + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(R, (int)threadIdx.x * per), hi = min(R, lo + per);
-  int nf = *n_free;
-  if (nf < 0 || nf > free_len) {
-    if (threadIdx.x == 0) raise_fault(status, DSPARK_FAULT_PAGE);
-    nf = nf < 0 ? 0 : free_len;
+struct PlanArgs {
+  int R, rows, lg, max_pages, free_len, extra, width, tree_nodes;
+  const int32_t *lens, *ctx;
+  int32_t *held, *table;
+  const int32_t* free_pages;
+  int32_t* n_free;
+  const int32_t* parent;
+  int32_t *row_off, *req, *position, *slot;
+  uint64_t* anc;
+  int32_t* status;
+  PlanWs ws;
+};
+
+// Rows and pages of every request, by one workgroup of NT threads, each request in its
+// thread's consecutive run.  One scan of (rows asked for, pages they lack) settles a step in
+// which everybody is served.  Otherwise a request's rows fit in a prefix of the requests that
+// ask for any, and of those its pages are had in a prefix of the ones that need any, so the
+// exclusive sum of the needs is also the count of pages handed out before it.
+template <int NT>
+__device__ __forceinline__ void plan_scan(const PlanArgs& p, int64_t* sums) {
+  const int R = p.R, tid = threadIdx.x;
+  const int per = (R + NT - 1) / NT;
+  const int lo = min(R, tid * per), hi = min(R, lo + per);
+  int nf = *p.n_free;
+  if (nf < 0 || nf > p.free_len) {
+    if (tid == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
+    nf = nf < 0 ? 0 : p.free_len;
   }
   // rows request q asks for (0 where refused) and the pages they lack
   auto ask = [&](int q, bool tell, int& n, int& need) {
-    const int64_t m = (int64_t)lens[q] + extra, c = ctx[q];
-    const int64_t h = held[q];
-    const bool bad = m < 0 || c < 0 || h < 0 || h > max_pages ||
-                     c + m > ((int64_t)max_pages << lg) || m > tree_nodes;
-    if (bad && tell) raise_fault(status, DSPARK_FAULT_LEN);
+    const int64_t m = (int64_t)p.lens[q] + p.extra, c = p.ctx[q];
+    const int64_t h = p.held[q];
+    const bool bad = m < 0 || c < 0 || h < 0 || h > p.max_pages ||
+                     c + m > ((int64_t)p.max_pages << p.lg) || m > p.tree_nodes;
+    if (bad && tell) raise_fault(p.status, DSPARK_FAULT_LEN);
     n = bad ? 0 : (int)m;
-    const int64_t want = n == 0 ? 0 : ((c + n + (1 << lg) - 1) >> lg) - h;
+    const int64_t want = n == 0 ? 0 : ((c + n + (1 << p.lg) - 1) >> p.lg) - h;
     need = want > 0 ? (int)want : 0;
   };
-  int64_t s = 0;
+  int64_t sn = 0, sp = 0;
   for (int q = lo; q < hi; ++q) {
     int n, need;
     ask(q, true, n, need);
-    s += n;
+    sn += n;
+    sp += need;
   }
-  int64_t base_n = block_scan<kPlanThreads>(s, sums) - s;
-  // pages asked for by the requests whose rows fit
-  int64_t run = base_n;
-  s = 0;
+  int64_t base_n = sn, base_p = sp, all_n, all_p;
+  block_scan2<NT>(base_n, base_p, all_n, all_p, sums);
+  base_n -= sn;
+  base_p -= sp;
+  int64_t at = base_n, given = all_p;  // first row of this run; pages handed out in all
+  const bool everybody = all_n <= p.rows && all_p <= nf;
+  if (!everybody) {
+    // pages asked for by the requests whose rows fit
+    int64_t run = base_n, s = 0;
+    for (int q = lo; q < hi; ++q) {
+      int n, need;
+      ask(q, false, n, need);
+      run += n;
+      if (n > 0 && run > p.rows) raise_fault(p.status, DSPARK_FAULT_LEN);
+      s += run <= p.rows ? need : 0;
+    }
+    base_p = block_scan<NT>(s, sums) - s;
+    // rows granted, pages handed out
+    int64_t pages = base_p, got = 0;
+    run = base_n;
+    s = 0;
+    for (int q = lo; q < hi; ++q) {
+      int n, need;
+      ask(q, false, n, need);
+      run += n;
+      need = run <= p.rows ? need : 0;
+      pages += need;
+      const bool lack = need > 0 && pages > nf;
+      if (lack) raise_fault(p.status, DSPARK_FAULT_PAGE);
+      s += run <= p.rows && !lack ? n : 0;
+      got += lack ? 0 : need;
+    }
+    at = s;
+    int64_t unused, all_got = got;
+    block_scan2<NT>(at, all_got, unused, given, sums);
+    at -= s;
+  }
+  int64_t run = base_n, pages = base_p;
   for (int q = lo; q < hi; ++q) {
     int n, need;
     ask(q, false, n, need);
     run += n;
-    if (n > 0 && run > rows) raise_fault(status, DSPARK_FAULT_LEN);
-    s += run <= rows ? need : 0;
-  }
-  int64_t base_p = block_scan<kPlanThreads>(s, sums) - s;
-  // rows granted
-  run = base_n;
-  int64_t pages = base_p;
-  s = 0;
-  for (int q = lo; q < hi; ++q) {
-    int n, need;
-    ask(q, false, n, need);
-    run += n;
-    need = run <= rows ? need : 0;
+    need = run <= p.rows ? need : 0;
     const int64_t before = pages;
     pages += need;
     const bool lack = need > 0 && pages > nf;
-    if (lack) raise_fault(status, DSPARK_FAULT_PAGE);
-    s += run <= rows && !lack ? n : 0;
-    ws.take[q] = lack ? 0 : need;
-    ws.first[q] = (int32_t)(before < nf ? before : 0);
+    p.row_off[q] = (int32_t)at;
+    at += run <= p.rows && !lack ? n : 0;
+    if (q == R - 1) p.row_off[R] = (int32_t)at;
+    const int h = p.held[q];
+    p.ws.held[q] = h;
+    p.ws.take[q] = lack ? 0 : need;
+    p.ws.first[q] = (int32_t)(before < nf ? before : 0);
+    if (!lack && need > 0) p.held[q] = h + need;
   }
-  int64_t at = block_scan<kPlanThreads>(s, sums) - s;
-  run = base_n;
-  pages = base_p;
-  s = 0;  // pages handed out
-  for (int q = lo; q < hi; ++q) {
-    int n, need;
-    ask(q, false, n, need);
-    run += n;
-    need = run <= rows ? need : 0;
-    pages += need;
-    const bool served = run <= rows && !(need > 0 && pages > nf);
-    row_off[q] = (int32_t)at;
-    at += served ? n : 0;
-    const int h = held[q];
-    ws.held[q] = h;
-    if (served && need > 0) {
-      held[q] = h + need;
-      s += need;
-    }
-    if (q == R - 1) row_off[R] = (int32_t)at;
-  }
-  const int64_t out = block_scan<kPlanThreads>(s, sums);
-  if (threadIdx.x == kPlanThreads - 1) {
-    ws.nfree[0] = nf;
-    *n_free = nf - (int32_t)out;
+  if (tid == NT - 1) {
+    p.ws.nfree[0] = nf;
+    *p.n_free = nf - (int32_t)given;
   }
 }
 
-// One workgroup per request and slice of its rows: its new pages into the table, and each
-// row's slot, position and ancestors.  A row's ancestors are a walk up at most 64 parents,
-// read from LDS.
-__global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(
-    int lg, int max_pages, const int32_t* __restrict__ ctx, int32_t* table,
-    const int32_t* __restrict__ free_pages, const int32_t* __restrict__ parent, int width,
-    const int32_t* __restrict__ row_off, PlanWs ws, int32_t* __restrict__ req,
-    int32_t* __restrict__ position, int32_t* __restrict__ slot, uint64_t* __restrict__ anc,
-    int32_t* status) {
+// Row i of request q, whose rows begin at a: slot, position and ancestors (a walk up at most
+// 64 parents through `up`).
+__device__ __forceinline__ void plan_row(const PlanArgs& p, int q, int a, int i, int had,
+                                         const int32_t* top, const int* up) {
+  const int c = p.ctx[q], t = c + i, idx = t >> p.lg;
+  const int page = idx < had ? p.table[(size_t)q * p.max_pages + idx] : top[-(idx - had)];
+  int s = -1;
+  if (page < 0 || page > (0x7fffffff >> p.lg))
+    raise_fault(p.status, DSPARK_FAULT_PAGE);
+  else
+    s = (page << p.lg) + (t & ((1 << p.lg) - 1));
+  int depth = i;
+  if (up) {
+    uint64_t bits = 0;
+    depth = 0;
+    for (int j = i; j > 0; j = up[j]) {
+      bits |= (uint64_t)1 << (j - 1);
+      ++depth;
+    }
+    p.anc[a + i] = bits;
+  }
+  p.slot[a + i] = s;
+  if (p.req) p.req[a + i] = q;
+  if (p.position) p.position[a + i] = c + depth;
+}
+
+// the node above node i of request q
+__device__ __forceinline__ int plan_parent(const PlanArgs& p, int q, int i) {
+  if (i == 0) return 0;
+  const int u = p.parent[(size_t)q * p.width + i];
+  if (u >= 0 && u < i) return u;
+  raise_fault(p.status, DSPARK_FAULT_TREE);
+  return i - 1;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(PlanArgs p) {
+  __shared__ int64_t sums[2 * kPlanThreads / kWave];
+  plan_scan<kPlanThreads>(p, sums);
+}
+
+// One workgroup per request and slice of its rows: its new pages into the table, and its rows.
+__global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(PlanArgs p) {
   __shared__ int up[DSPARK_MAX_TREE_NODES];
   const int q = blockIdx.x;
-  const int a = row_off[q], n = row_off[q + 1] - a;
-  const int had = ws.held[q], take = ws.take[q], c = ctx[q];
+  const int a = p.row_off[q], n = p.row_off[q + 1] - a;
+  const int had = p.ws.held[q], take = p.ws.take[q];
   // the k-th of q's new pages is top[-k]
-  const int32_t* top = free_pages + (ws.nfree[0] - 1 - ws.first[q]);
-  int32_t* row = table + (size_t)q * max_pages;
+  const int32_t* top = p.free_pages + (p.ws.nfree[0] - 1 - p.ws.first[q]);
   if (n == 0) return;
   const int t0 = blockIdx.y * kRowThreads + threadIdx.x, step = gridDim.y * kRowThreads;
-  for (int k = t0; k < take; k += step) row[had + k] = top[-k];
-  if (parent) {
-    for (int i = threadIdx.x; i < n; i += kRowThreads) {
-      int p = i == 0 ? 0 : parent[(size_t)q * width + i];
-      if (i > 0 && (p < 0 || p >= i)) {
-        raise_fault(status, DSPARK_FAULT_TREE);
-        p = i - 1;
-      }
-      up[i] = p;
+  for (int k = t0; k < take; k += step) p.table[(size_t)q * p.max_pages + had + k] = top[-k];
+  if (p.parent) {
+    for (int i = threadIdx.x; i < n; i += kRowThreads) up[i] = plan_parent(p, q, i);
+    __syncthreads();
+  }
+  for (int i = t0; i < n; i += step) plan_row(p, q, a, i, had, top, p.parent ? up : nullptr);
+}
+
+// The whole plan in one workgroup, for steps of few requests and rows: the scan, then a thread
+// per row, which finds its request in the row offsets.
+constexpr int kSmallThreads = 256, kSmallR = 256, kSmallRows = 1024, kSmallNodes = 8192;
+
+__global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(PlanArgs p) {
+  __shared__ int64_t sums[2 * kSmallThreads / kWave];
+  __shared__ int off[kSmallR + 1];
+  __shared__ int up[kSmallNodes];
+  const int tid = threadIdx.x, R = p.R;
+  plan_scan<kSmallThreads>(p, sums);
+  __syncthreads();  // what the scan wrote is read by other threads below
+  for (int q = tid; q <= R; q += kSmallThreads) off[q] = p.row_off[q];
+  __syncthreads();
+  const int nf = p.ws.nfree[0];
+  for (int q = tid; q < R; q += kSmallThreads) {
+    const int take = p.ws.take[q], had = p.ws.held[q];
+    const int32_t* top = p.free_pages + (nf - 1 - p.ws.first[q]);
+    for (int k = 0; k < take; ++k) p.table[(size_t)q * p.max_pages + had + k] = top[-k];
+  }
+  if (p.parent) {
+    for (int k = tid; k < R * p.width; k += kSmallThreads) {
+      const int q = k / p.width, i = k % p.width;
+      if (i < off[q + 1] - off[q]) up[k] = plan_parent(p, q, i);
     }
     __syncthreads();
   }
-  for (int i = t0; i < n; i += step) {
-    const int t = c + i, idx = t >> lg;
-    const int page = idx < had ? row[idx] : top[-(idx - had)];
-    int s = -1;
-    if (page < 0 || page > (0x7fffffff >> lg))
-      raise_fault(status, DSPARK_FAULT_PAGE);
-    else
-      s = (page << lg) + (t & ((1 << lg) - 1));
-    int depth = i;
-    if (parent) {
-      uint64_t bits = 0;
-      depth = 0;
-      for (int j = i; j > 0; j = up[j]) {
-        bits |= (uint64_t)1 << (j - 1);
-        ++depth;
-      }
-      anc[a + i] = bits;
+  const int rows = off[R];
+  for (int row = tid; row < rows; row += kSmallThreads) {
+    int lo = 0, hi = R;  // the last request that begins at or before the row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (off[mid] <= row)
+        lo = mid;
+      else
+        hi = mid;
     }
-    slot[a + i] = s;
-    if (req) req[a + i] = q;
-    if (position) position[a + i] = c + depth;
+    plan_row(p, lo, off[lo], row - off[lo], p.ws.held[lo], p.free_pages + (nf - 1 - p.ws.first[lo]),
+             p.parent ? up + lo * p.width : nullptr);
   }
 }
 
@@ -230,114 +291,126 @@ __device__ __forceinline__ int clamp_acc(int na, int c, int h, int lg, int most)
   return na < -1 ? -1 : na;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) commit_scan_kernel(
-    int R, int most, int lg, int max_pages, int free_len, const int32_t* __restrict__ n_acc,
-    const int32_t* __restrict__ done, const int32_t* ctx, int32_t* ctx_out, int32_t* held,
-    int32_t* n_free, CommitWs ws, int32_t* status) {
-  __shared__ int64_t sums[kPlanThreads / kWave];
-  const int per = (R + kPlanThreads - 1) / kPlanThreads;
-  const int lo = min(R, (int)threadIdx.x * per), hi = min(R, lo + per);
+// entries of the block tables up to which one workgroup gives pages back (it copies about 256
+// of them a microsecond)
+constexpr int kGivePages = 16384;
+
+struct CommitArgs {
+  int R, gamma, most, lg, max_pages, free_len;
+  const int32_t *n_acc, *path, *done, *ctx;
+  int32_t *ctx_out, *held;
+  const int32_t* table;
+  int32_t *free_pages, *n_free;
+  int layers, Hkv, chunks, n_pages;
+  uint4 *k_cache, *v_cache;
+  int64_t layer_stride, page_stride, head_stride, tok_stride;  // in 16-byte pieces
+  int32_t* status;
+  CommitWs ws;
+};
+
+// Lengths of every request and the places of the pages given back, by one workgroup; GIVE:
+// and the pages themselves, a wave per request.
+template <int NT, bool GIVE>
+__device__ __forceinline__ void commit_scan(const CommitArgs& p, int64_t* sums) {
+  const int R = p.R, tid = threadIdx.x;
+  const int per = (R + NT - 1) / NT;
+  const int lo = min(R, tid * per), hi = min(R, lo + per);
   int64_t s = 0;
   for (int q = lo; q < hi; ++q) {
-    int h = held[q];
-    if (h < 0 || h > max_pages) {
-      raise_fault(status, DSPARK_FAULT_LEN);
-      h = h < 0 ? 0 : max_pages;
+    int h = p.held[q];
+    if (h < 0 || h > p.max_pages) {
+      raise_fault(p.status, DSPARK_FAULT_LEN);
+      h = h < 0 ? 0 : p.max_pages;
     }
-    const bool end = done && done[q] != 0;
-    const int c = ctx[q];
-    ws.ctx[q] = c;
-    ws.held[q] = h;
+    const bool end = p.done && p.done[q] != 0;
+    const int c = p.ctx[q], n = p.n_acc[q];
+    p.ws.ctx[q] = c;
+    p.ws.held[q] = h;
     if (end) {
       s += h;
-      ctx_out[q] = 0;
+      p.ctx_out[q] = 0;
     } else {
-      const int na = clamp_acc(n_acc[q], c, h, lg, most);
-      if (na != n_acc[q]) raise_fault(status, DSPARK_FAULT_LEN);
-      ctx_out[q] = c + na + 1;
+      const int na = clamp_acc(n, c, h, p.lg, p.most);
+      if (na != n) raise_fault(p.status, DSPARK_FAULT_LEN);
+      p.ctx_out[q] = c + na + 1;
     }
   }
-  if (!done) return;
-  int nf = *n_free;
-  if (nf < 0 || nf > free_len) {
-    if (threadIdx.x == 0) raise_fault(status, DSPARK_FAULT_PAGE);
-    nf = nf < 0 ? 0 : free_len;
+  if (!p.done) return;
+  int nf = *p.n_free;
+  if (nf < 0 || nf > p.free_len) {
+    if (tid == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
+    nf = nf < 0 ? 0 : p.free_len;
   }
-  const int64_t end = block_scan<kPlanThreads>(s, sums);
+  const int64_t end = block_scan<NT>(s, sums);
   int64_t at = nf + end - s;
   for (int q = lo; q < hi; ++q) {
-    ws.first[q] = (int32_t)(at < free_len ? at : free_len);
-    if (done[q] != 0) {
-      at += ws.held[q];
-      held[q] = 0;
+    p.ws.first[q] = (int32_t)(at < p.free_len ? at : p.free_len);
+    if (p.done[q] != 0) {
+      at += p.ws.held[q];
+      p.held[q] = 0;
     }
   }
-  if (threadIdx.x == kPlanThreads - 1) {
+  if (tid == NT - 1) {
     const int64_t total = nf + end;
-    if (total > free_len) raise_fault(status, DSPARK_FAULT_PAGE);
-    *n_free = (int32_t)(total < free_len ? total : free_len);
+    if (total > p.free_len) raise_fault(p.status, DSPARK_FAULT_PAGE);
+    *p.n_free = (int32_t)(total < p.free_len ? total : p.free_len);
+  }
+  if (GIVE) {
+    __syncthreads();
+    for (int q = tid / kWave; q < R; q += NT / kWave) {
+      if (p.done[q] == 0) continue;
+      const int first = p.ws.first[q], h = p.ws.held[q];
+      for (int k = tid & (kWave - 1); k < h && first + k < p.free_len; k += kWave)
+        p.free_pages[first + k] = p.table[(size_t)q * p.max_pages + k];
+    }
   }
 }
 
-// One workgroup per request and 256 of the 16-byte columns (layer, keys or values, head,
-// piece of D) of its tokens.  A thread owns its column, so the moves of one column are one
-// thread's: a batch of eight tokens is read before any of them is written, and since the path
-// ascends (its i-th node is at least i), no later batch reads a token that an earlier one
-// wrote.  The first slice also gives a finished request's pages back.
-__global__ void __launch_bounds__(256) commit_move_kernel(
-    int gamma, int lg, int max_pages, int free_len, const int32_t* __restrict__ n_acc,
-    const int32_t* __restrict__ path, const int32_t* __restrict__ done,
-    const int32_t* __restrict__ table, int32_t* __restrict__ free_pages, int layers, int Hkv,
-    int chunks, int n_pages, uint4* k_cache, uint4* v_cache, int64_t layer_stride,
-    int64_t page_stride, int64_t head_stride, int64_t tok_stride, CommitWs ws, int32_t* status) {
-  const int q = blockIdx.x;
-  const int c = ws.ctx[q], h = ws.held[q];
-  const int32_t* pages = table + (size_t)q * max_pages;
-  if (done && done[q] != 0) {
-    const int at = ws.first[q];
-    if (blockIdx.y == 0)
-      for (int k = threadIdx.x; k < h && at + k < free_len; k += 256) free_pages[at + k] = pages[k];
-    return;
-  }
-  if (!path || c < 0) return;
-  const int na = clamp_acc(n_acc[q], c, h, lg, gamma);
+// The moves of request q in 256 of the 16-byte columns (layer, keys or values, head, piece of
+// D) of its tokens.  A thread owns its column, so the moves of one column are one thread's: a
+// batch of eight tokens is read before any of them is written, and since the path ascends
+// (its i-th node is at least i), no later batch reads a token that an earlier one wrote.
+__device__ __forceinline__ void commit_move(const CommitArgs& p, int q, int slice, int c, int h) {
+  const int32_t* pages = p.table + (size_t)q * p.max_pages;
+  if (c < 0) return;
+  const int na = clamp_acc(p.n_acc[q], c, h, p.lg, p.gamma);
   if (na < 1) return;
-  const int per_layer = 2 * Hkv * chunks;
-  const int64_t col = (int64_t)blockIdx.y * 256 + threadIdx.x;
-  const bool mine = col < (int64_t)layers * per_layer;
+  const int per_layer = 2 * p.Hkv * p.chunks;
+  const int64_t col = (int64_t)slice * 256 + threadIdx.x;
+  const bool mine = col < (int64_t)p.layers * per_layer;
   int64_t at = 0;
-  uint4* cache = k_cache;
+  uint4* cache = p.k_cache;
   if (mine) {
     const int layer = (int)(col / per_layer);
     int r = (int)(col % per_layer);
-    if (r >= Hkv * chunks) {
-      cache = v_cache;
-      r -= Hkv * chunks;
+    if (r >= p.Hkv * p.chunks) {
+      cache = p.v_cache;
+      r -= p.Hkv * p.chunks;
     }
-    at = layer * layer_stride + (int64_t)(r / chunks) * head_stride + r % chunks;
+    at = layer * p.layer_stride + (int64_t)(r / p.chunks) * p.head_stride + r % p.chunks;
   }
-  const bool tell = blockIdx.y == 0 && threadIdx.x == 0;
-  const int mask = (1 << lg) - 1;
+  const bool tell = slice == 0 && threadIdx.x == 0;
+  const int mask = (1 << p.lg) - 1;
   constexpr int kBatch = 8;
   int last = 0;
   bool stop = false;
   for (int i0 = 1; i0 <= na && !stop; i0 += kBatch) {
-    int64_t from[kBatch], to[kBatch];  // -1: nothing moves
+    int64_t from[kBatch], to[kBatch];  // from -1: nothing moves
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + u;
-      const int p = path[(size_t)q * gamma + (i <= na ? i - 1 : 0)];
-      const bool fine = p > last && (int64_t)c + p < ((int64_t)h << lg);
-      if (i <= na && !stop && !fine && tell) raise_fault(status, DSPARK_FAULT_TREE);
+      const int n = p.path[(size_t)q * p.gamma + (i <= na ? i - 1 : 0)];
+      const bool fine = n > last && (int64_t)c + n < ((int64_t)h << p.lg);
+      if (i <= na && !stop && !fine && tell) raise_fault(p.status, DSPARK_FAULT_TREE);
       stop = stop || i > na || !fine;
-      const int src = stop ? 0 : c + p, dst = stop ? 0 : c + i;
-      last = stop ? last : p;
-      const int ps = pages[src >> lg], pd = pages[dst >> lg];
-      const bool known = ps >= 0 && ps < n_pages && pd >= 0 && pd < n_pages;
-      const bool move = !stop && p != i;
-      if (move && !known && tell) raise_fault(status, DSPARK_FAULT_PAGE);
-      from[u] = move && known && mine ? at + ps * page_stride + (src & mask) * tok_stride : -1;
-      to[u] = at + pd * page_stride + (dst & mask) * tok_stride;
+      const int src = stop ? 0 : c + n, dst = stop ? 0 : c + i;
+      last = stop ? last : n;
+      const int ps = pages[src >> p.lg], pd = pages[dst >> p.lg];
+      const bool known = ps >= 0 && ps < p.n_pages && pd >= 0 && pd < p.n_pages;
+      const bool move = !stop && n != i;
+      if (move && !known && tell) raise_fault(p.status, DSPARK_FAULT_PAGE);
+      from[u] = move && known && mine ? at + ps * p.page_stride + (src & mask) * p.tok_stride : -1;
+      to[u] = at + pd * p.page_stride + (dst & mask) * p.tok_stride;
     }
     uint4 x[kBatch];
 #pragma unroll
@@ -346,6 +419,40 @@ __global__ void __launch_bounds__(256) commit_move_kernel(
     for (int u = 0; u < kBatch; ++u)
       if (from[u] >= 0) cache[to[u]] = x[u];
   }
+}
+
+// One launch, where the lengths go to memory of their own and the pages given back are few:
+// the last workgroup scans and gives, the others move.  A move reads only what the scan leaves
+// alone: ctx, and held of requests that go on.
+__global__ void __launch_bounds__(256) commit_kernel(CommitArgs p, int slices) {
+  __shared__ int64_t sums[256 / kWave];
+  const int b = blockIdx.x;
+  if (b == (int)gridDim.x - 1) {
+    commit_scan<256, true>(p, sums);
+    return;
+  }
+  const int q = b / slices;
+  if (p.done && p.done[q] != 0) return;
+  const int h = p.held[q];
+  commit_move(p, q, b % slices, p.ctx[q], h < 0 ? 0 : (h > p.max_pages ? p.max_pages : h));
+}
+
+// Two launches otherwise: the scan, then the moves from the lengths it kept, and the pages.
+__global__ void __launch_bounds__(kPlanThreads) commit_scan_kernel(CommitArgs p) {
+  __shared__ int64_t sums[kPlanThreads / kWave];
+  commit_scan<kPlanThreads, false>(p, sums);
+}
+
+__global__ void __launch_bounds__(256) commit_move_kernel(CommitArgs p) {
+  const int q = blockIdx.x, h = p.ws.held[q];
+  if (p.done && p.done[q] != 0) {
+    const int at = p.ws.first[q];
+    if (blockIdx.y == 0)
+      for (int k = threadIdx.x; k < h && at + k < p.free_len; k += 256)
+        p.free_pages[at + k] = p.table[(size_t)q * p.max_pages + k];
+    return;
+  }
+  if (p.path) commit_move(p, q, blockIdx.y, p.ws.ctx[q], h);
 }
 
 }  // namespace dspark
@@ -373,18 +480,39 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
     return DSPARK_EINVAL;
   const PlanWs w = carve_plan(ws, R);
   if (ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
-  const int lg = log2_of(page_size);
-  int nodes = 0x7fffffff;
-  if (parent) nodes = width < DSPARK_MAX_TREE_NODES ? width : DSPARK_MAX_TREE_NODES;
-  plan_scan_kernel<<<1, kPlanThreads, 0, stream>>>(R, rows, lg, max_pages, free_len, extra, lens,
-                                                   ctx, held, n_free, nodes, row_off, w,
-                                                   dev_status);
+  PlanArgs p{};
+  p.R = R;
+  p.rows = rows;
+  p.lg = log2_of(page_size);
+  p.max_pages = max_pages;
+  p.free_len = free_len;
+  p.extra = extra;
+  p.width = width;
+  p.tree_nodes = 0x7fffffff;
+  if (parent) p.tree_nodes = width < DSPARK_MAX_TREE_NODES ? width : DSPARK_MAX_TREE_NODES;
+  p.lens = lens;
+  p.ctx = ctx;
+  p.held = held;
+  p.table = table;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.parent = parent;
+  p.row_off = row_off;
+  p.req = req;
+  p.position = position;
+  p.slot = slot;
+  p.anc = anc;
+  p.status = dev_status;
+  p.ws = w;
+  if (R <= kSmallR && rows <= kSmallRows && (!parent || (int64_t)R * width <= kSmallNodes)) {
+    plan_small_kernel<<<1, kSmallThreads, 0, stream>>>(p);
+    return launch_status();
+  }
+  plan_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   // slices of a request's rows: one for steps of drafted tokens, more where few requests
   // bring long prompts
   const int slices = parent ? 1 : 1 + rows / (R < 64 ? 64 * kRowThreads : R * kRowThreads);
-  plan_rows_kernel<<<dim3(R, slices < 64 ? slices : 64), kRowThreads, 0, stream>>>(
-      lg, max_pages, ctx, table, free_pages, parent, width, row_off, w, req, position, slot, anc,
-      dev_status);
+  plan_rows_kernel<<<dim3(R, slices < 64 ? slices : 64), kRowThreads, 0, stream>>>(p);
   return launch_status();
 }
 
@@ -451,13 +579,43 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   const int lg = log2_of(page_size), u = (int)(16 / e), chunks = path ? D / u : 1;
   const int64_t cols = path ? (int64_t)layers * 2 * Hkv * chunks : 1;
   if ((cols + 255) / 256 > 65535) return DSPARK_EINVAL;
-  commit_scan_kernel<<<1, kPlanThreads, 0, stream>>>(R, path ? gamma : 0x7fffffff, lg, max_pages,
-                                                     free_len, n_acc, done, ctx, ctx_out, held,
-                                                     n_free, w, dev_status);
-  if (path || done)
-    commit_move_kernel<<<dim3(R, cols > 0 ? (unsigned)((cols + 255) / 256) : 1), 256, 0, stream>>>(
-        gamma, lg, max_pages, free_len, n_acc, path, done, table, free_pages, layers, Hkv, chunks,
-        n_pages, static_cast<uint4*>(k_cache), static_cast<uint4*>(v_cache), layer_stride / u,
-        page_stride / u, head_stride / u, tok_stride / u, w, dev_status);
+  const int slices = cols > 256 ? (int)((cols + 255) / 256) : 1;
+  CommitArgs p{};
+  p.R = R;
+  p.gamma = gamma;
+  p.most = path ? gamma : 0x7fffffff;
+  p.lg = lg;
+  p.max_pages = max_pages;
+  p.free_len = free_len;
+  p.n_acc = n_acc;
+  p.path = path;
+  p.done = done;
+  p.ctx = ctx;
+  p.ctx_out = ctx_out;
+  p.held = held;
+  p.table = table;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.layers = layers;
+  p.Hkv = Hkv;
+  p.chunks = chunks;
+  p.n_pages = n_pages;
+  p.k_cache = static_cast<uint4*>(k_cache);
+  p.v_cache = static_cast<uint4*>(v_cache);
+  p.layer_stride = layer_stride / u;
+  p.page_stride = page_stride / u;
+  p.head_stride = head_stride / u;
+  p.tok_stride = tok_stride / u;
+  p.status = dev_status;
+  p.ws = w;
+  const bool apart = ctx_out + R <= ctx || ctx + R <= ctx_out;
+  const bool few = R <= 1024 && (!done || (int64_t)R * max_pages <= kGivePages);
+  const int64_t blocks = path ? (int64_t)R * slices : 0;
+  if (few && (!path || (apart && blocks < (1 << 24) - 1))) {
+    commit_kernel<<<(unsigned)blocks + 1, 256, 0, stream>>>(p, slices);
+    return launch_status();
+  }
+  commit_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  if (path || done) commit_move_kernel<<<dim3(R, slices), 256, 0, stream>>>(p);
   return launch_status();
 }

@@ -27,6 +27,39 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums) {
   return base + v;
 }
 
+// the same of two values at once, and their totals; `sums` has 2 * NT / 64 entries
+template <int NT>
+__device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& all_a, int64_t& all_b,
+                                            int64_t* sums) {
+  constexpr int NW = NT / kWave;
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int64_t u = __shfl_up(a, o, kWave), v = __shfl_up(b, o, kWave);
+    if (lane >= o) {
+      a += u;
+      b += v;
+    }
+  }
+  if (lane == kWave - 1) {
+    sums[wave] = a;
+    sums[NW + wave] = b;
+  }
+  __syncthreads();
+  all_a = all_b = 0;
+  int64_t base_a = 0, base_b = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    base_a += w < wave ? sums[w] : 0;
+    base_b += w < wave ? sums[NW + w] : 0;
+    all_a += sums[w];
+    all_b += sums[NW + w];
+  }
+  a += base_a;
+  b += base_b;
+  __syncthreads();
+}
+
 inline bool page_size_ok(int ps) { return ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 inline int log2_of(int p) { return __builtin_ctz((unsigned)p); }
 

@@ -52,8 +52,16 @@ def set_argtypes(L):
 
 
 # ----------------------------------------------------------------------------------------
-# checks and calls
+# checks and calls (a decode step makes many of them, so the passing case costs little: about
+# 0.4 us a tensor; what is wrong with one is found out only once something is)
 # ----------------------------------------------------------------------------------------
+try:
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _device(t, name):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -62,20 +70,33 @@ def _device(t, name):
     return t.device
 
 
-def _chk(t, name, dev, shape, dtype, dense=True):
-    """One tensor argument; returns its address.  A None in `shape` matches any size."""
+def _dims(t, name, n):
+    """Sizes of a tensor of n dimensions."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != n:
+        raise ValueError(f"{name} has {t.dim()} dimensions, expected {n}")
+    return t.shape
+
+
+def _refuse(t, name, dev, shape, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, expected {dev}")
     if t.dtype is not dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    have = t.shape
-    if len(have) != len(shape) or any(w is not None and w != h for h, w in zip(have, shape)):
-        raise ValueError(f"{name} has shape {tuple(have)}, expected {shape}")
-    if dense and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _chk(t, name, dev, shape, dtype):
+    """One tensor argument; returns its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == dev and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dev, shape, dtype)
 
 
 def _opt(t, *a):
@@ -92,50 +113,77 @@ def _dt(t, name):
 
 def _strides(t, last):
     """Strides of the leading dimensions (0 for a dimension of size 1, whose stride is never
-    used) of a tensor whose last `last` dimensions are dense."""
-    n = t.dim() - last
-    dense = 1
-    for k in range(t.dim() - 1, n - 1, -1):
-        if t.shape[k] != 1 and t.stride(k) != dense:
+    used) of a tensor whose last `last` dimensions are dense; None where they are not."""
+    shape, st = t.shape, t.stride()
+    n, dense = len(shape) - last, 1
+    for k in range(len(shape) - 1, n - 1, -1):
+        if st[k] != dense and shape[k] != 1:
             return None
-        dense *= t.shape[k]
-    return [t.stride(k) if t.shape[k] > 1 else 0 for k in range(n)]
+        dense *= shape[k]
+    return [s if m != 1 else 0 for s, m in zip(st[:n], shape)]
+
+
+def _rows(t, name, dev, shape, dtype):
+    """A tensor of rows [rows][heads][D], each dense; returns its address and row stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev:
+        _refuse(t, name, dev, shape, dtype)
+    st = t.stride()
+    if st[2] == 1 and st[1] == shape[2] and shape[0] != 1:
+        return t.data_ptr(), st[0]
+    st = _strides(t, 2)
+    if st is None:
+        raise ValueError(f"{name} must be dense within a row")
+    return t.data_ptr(), st[0]
 
 
 def _cache(k_cache, v_cache, dev, dims):
-    """Shape and strides of a pair of caches (`dims`: 4, or 5 with a leading layer)."""
-    kp = _chk(k_cache, "k_cache", dev, (None,) * dims, k_cache.dtype, False)
-    vp = _chk(v_cache, "v_cache", dev, tuple(k_cache.shape), k_cache.dtype, False)
-    st = _strides(k_cache, 1)
-    if st is None or _strides(v_cache, 1) is None:
-        raise ValueError("the caches' last dimension must be contiguous")
-    if st != _strides(v_cache, 1):
-        raise ValueError("k_cache and v_cache differ in strides")
-    return kp, vp, tuple(k_cache.shape), st
+    """Addresses, shape and strides of a pair of caches (`dims`: 4, or 5 with a leading layer)."""
+    shape = _dims(k_cache, "k_cache", dims)
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if (not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not k_cache.dtype or
+                t.shape != shape):
+            _refuse(t, name, dev, shape, k_cache.dtype)
+    st = k_cache.stride()
+    if 1 in shape or st[-1] != 1 or v_cache.stride() != st:
+        st = _strides(k_cache, 1)
+        if st is None or _strides(v_cache, 1) is None:
+            raise ValueError("the caches' last dimension must be contiguous")
+        if st != _strides(v_cache, 1):
+            raise ValueError("k_cache and v_cache differ in strides")
+    return k_cache.data_ptr(), v_cache.data_ptr(), shape, st[:dims - 1]
 
 
-def _call(dev, fn, *args):
-    """fn(*args, stream) on `dev`; raises on a refusal."""
-    from . import DsparkError, lib
-    f = getattr(lib(), fn)
-    if torch.cuda.current_device() == dev.index:
-        rc = f(*args, torch.cuda.current_stream().cuda_stream)
+_fn = {}
+
+
+def _call(dev, name, *args):
+    """The library's `name`(*args, stream) on `dev`; raises on a refusal."""
+    f = _fn.get(name)
+    if f is None:
+        from . import lib
+        f = _fn[name] = getattr(lib(), name)
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch.cuda.current_stream().cuda_stream)
+            rc = f(*args, _raw_stream(index))
     if rc != 0:
-        raise DsparkError(fn, rc)
+        from . import DsparkError
+        raise DsparkError(name, rc)
 
 
 def _workspace(nbytes, dev, ws):
     if ws is None:
-        ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=dev)
-    else:
-        if ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"ws must be a contiguous tensor on {dev}")
-        if ws.numel() * ws.element_size() < nbytes:
-            raise ValueError("workspace too small")
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+        nbytes = max(nbytes, 256)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        return ws, ws.data_ptr(), nbytes
+    if ws.device != dev or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
+    have = ws.numel() * ws.element_size()
+    if have < nbytes:
+        raise ValueError("workspace too small")
+    return ws, ws.data_ptr(), have
 
 
 def cache_plan_workspace_bytes(R) -> int:
@@ -154,12 +202,14 @@ def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, e
     a caller-supplied `out` may leave "req" and "position" out.  Rows behind row_off[-1] are
     left as they were."""
     dev = _device(lens, "lens")
-    R = lens.shape[0]
-    a = [_chk(lens, "lens", dev, (R,), _I32), _chk(ctx, "ctx", dev, (R,), _I32),
-         _chk(held, "held", dev, (R,), _I32), _chk(table, "table", dev, (R, None), _I32),
-         _chk(free_pages, "free_pages", dev, (None,), _I32),
+    per = R, = _dims(lens, "lens", 1)
+    W, F = _dims(table, "table", 2)[1], _dims(free_pages, "free_pages", 1)[0]
+    width = 0 if parent is None else _dims(parent, "parent", 2)[1]
+    a = [_chk(lens, "lens", dev, per, _I32), _chk(ctx, "ctx", dev, per, _I32),
+         _chk(held, "held", dev, per, _I32), _chk(table, "table", dev, (R, W), _I32),
+         _chk(free_pages, "free_pages", dev, (F,), _I32),
          _chk(n_free, "n_free", dev, (1,), _I32),
-         _opt(parent, "parent", dev, (R, None), _I32)]
+         _opt(parent, "parent", dev, (R, width), _I32)]
     if out is None:
         out = dict(row_off=torch.empty(R + 1, dtype=_I32, device=dev))
         for k in ("req", "position", "slot"):
@@ -176,8 +226,7 @@ def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, e
         out["row_off"].zero_()
         return out
     ws, wp, wb = _workspace(cache_plan_workspace_bytes(R), dev, ws)
-    _call(dev, "dspark_cache_plan", R, rows, page_size, table.shape[1], free_pages.shape[0],
-          extra, *a, 0 if parent is None else parent.shape[1], *b, wp, wb)
+    _call(dev, "dspark_cache_plan", R, rows, page_size, W, F, extra, *a, width, *b, wp, wb)
     return out
 
 
@@ -187,13 +236,11 @@ def cache_append(k, v, k_cache, v_cache, slot, *, n_rows=None, status=None):
     rows at and behind it are skipped (a plan's row_off[-1:])."""
     dev = _device(k, "k")
     kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
-    rows = k.shape[0]
+    rows = _dims(k, "k", 3)[0]
     dt = _dt(k_cache, "k_cache")
-    a, b = (_chk(x, s, dev, (rows, Hkv, D), k_cache.dtype, False) for x, s in ((k, "k"), (v, "v")))
-    ks, vs = _strides(k, 2), _strides(v, 2)
-    if ks is None or vs is None:
-        raise ValueError("k and v must be dense within a row")
-    _call(dev, "dspark_cache_append", rows, Hkv, D, dt, page, P, a, b, ks[0], vs[0],
+    a, ks = _rows(k, "k", dev, (rows, Hkv, D), k_cache.dtype)
+    b, vs = _rows(v, "v", dev, (rows, Hkv, D), k_cache.dtype)
+    _call(dev, "dspark_cache_append", rows, Hkv, D, dt, page, P, a, b, ks, vs,
           _chk(slot, "slot", dev, (rows,), _I32), _opt(n_rows, "n_rows", dev, (1,), _I32), kp, vp,
           *st, _opt(status, "status", dev, (1,), _I32))
 
@@ -214,14 +261,10 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
     dev = _device(q, "q")
     kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
     dt = _dt(q, "q")
-    qp = _chk(q, "q", dev, (None, None, D), k_cache.dtype, False)
-    rows, Hq = q.shape[0], q.shape[1]
-    qs = _strides(q, 2)
-    if qs is None:
-        raise ValueError("q must be dense within a row")
-    tp = _chk(table, "table", dev, (None, None), _I32)
-    R = table.shape[0]
-    a = [tp, _chk(ctx, "ctx", dev, (R,), _I32), _chk(row_off, "row_off", dev, (R + 1,), _I32),
+    rows, Hq, _ = _dims(q, "q", 3)
+    qp, qs = _rows(q, "q", dev, (rows, Hq, D), k_cache.dtype)
+    R, W = _dims(table, "table", 2)
+    a = [_chk(table, "table", dev, (R, W), _I32), _chk(ctx, "ctx", dev, (R,), _I32), _chk(row_off, "row_off", dev, (R + 1,), _I32),
          _opt(anc, "anc", dev, (rows,), _I64)]
     if out is None:
         out = dict(o=torch.empty((rows, Hq, D), dtype=q.dtype, device=dev),
@@ -240,8 +283,7 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
         from . import EINVAL, DsparkError
         raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
     ws, wp, wb = _workspace(nbytes, dev, ws)
-    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, table.shape[1], P, qp,
-          qs[0], kp, vp, *st, *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
+    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st, *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
     return out
 
 
@@ -261,18 +303,18 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
     other ids become -inf."""
     dev = _device(logits, "logits")
     dt = _dt(logits, "logits")
-    xp = _chk(x, "x", dev, (None, None), _I32)
-    R, gamma = x.shape
+    R, gamma = _dims(x, "x", 2)
+    xp = _chk(x, "x", dev, (R, gamma), _I32)
     V = logits.shape[-1]
     if row_off is None:
         lp = _chk(logits, "logits", dev, (R, gamma + 1, V), logits.dtype)
         rows, stride = R * (gamma + 1), V
     else:
-        lp = _chk(logits, "logits", dev, (None, V), logits.dtype, False)
+        rows = _dims(logits, "logits", 2)[0]
         st = _strides(logits, 1)
         if st is None:
             raise ValueError("rows of logits must be contiguous")
-        rows, stride = logits.shape[0], max(st[0], V)
+        lp, stride = logits.data_ptr(), max(st[0], V)
     if out is None:
         out = torch.empty((R, gamma + 1, V), dtype=logits.dtype, device=dev)
     op = _chk(out, "out", dev, (R, gamma + 1, V), logits.dtype)
@@ -317,14 +359,15 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     finished requests (nonzero) give their pages back: free_pages and n_free grow, held and
     the length become 0."""
     dev = _device(n_acc, "n_acc")
-    R = n_acc.shape[0]
-    a = [_chk(n_acc, "n_acc", dev, (R,), _I32), _opt(path, "path", dev, (R, None), _I32),
-         _opt(done, "done", dev, (R,), _I32), _chk(ctx, "ctx", dev, (R,), _I32)]
+    per = R, = _dims(n_acc, "n_acc", 1)
+    W, F = _dims(table, "table", 2)[1], _dims(free_pages, "free_pages", 1)[0]
+    gamma = 0 if path is None else _dims(path, "path", 2)[1]
+    a = [_chk(n_acc, "n_acc", dev, per, _I32), _opt(path, "path", dev, (R, gamma), _I32),
+         _opt(done, "done", dev, per, _I32), _chk(ctx, "ctx", dev, per, _I32)]
     if out is None:
         out = torch.empty(R, dtype=_I32, device=dev)
-    b = [_chk(out, "out", dev, (R,), _I32), _chk(held, "held", dev, (R,), _I32),
-         _chk(table, "table", dev, (R, None), _I32),
-         _chk(free_pages, "free_pages", dev, (None,), _I32),
+    b = [_chk(out, "out", dev, per, _I32), _chk(held, "held", dev, per, _I32),
+         _chk(table, "table", dev, (R, W), _I32), _chk(free_pages, "free_pages", dev, (F,), _I32),
          _chk(n_free, "n_free", dev, (1,), _I32)]
     c = [0, 0, 0, 0, 0, None, None, 0, 0, 0, 0]
     if path is not None:
@@ -340,6 +383,5 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     if R == 0:
         return out
     ws, wp, wb = _workspace(cache_commit_workspace_bytes(R), dev, ws)
-    _call(dev, "dspark_cache_commit", R, 0 if path is None else path.shape[1], page_size,
-          table.shape[1], free_pages.shape[0], *a, *b, *c, sp, wp, wb)
+    _call(dev, "dspark_cache_commit", R, gamma, page_size, W, F, *a, *b, *c, sp, wp, wb)
     return out
