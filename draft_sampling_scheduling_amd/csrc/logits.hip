@@ -72,104 +72,173 @@ struct Raw8<float> {
   }
 };
 
+// inputs that every lane reads alike, through the scalar cache
+template <class V>
+__device__ __forceinline__ V uniform_load(const V* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) V*)p)[i];
+}
+
 template <class T>
 __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams p) {
-  __shared__ __attribute__((aligned(16))) uint32_t seen[kLogSlice];
-  __shared__ __attribute__((aligned(16))) int last_bias[kLogSlice];  // entry + 1, 0 none
+  // one word per id of the slice: first what the history holds of it, then (its words in
+  // registers) which bias entry is its last
+  __shared__ __attribute__((aligned(16))) uint32_t word[kLogSlice];
   const int q = blockIdx.y, v0 = blockIdx.x * kLogSlice, tid = threadIdx.x;
   const bool tell = blockIdx.x == 0 && tid == 0;
 
-  int L = p.ell[q];
+  // Everything that can be asked for at once is: the request's scalars, and the first ids of
+  // its history and biases (clamped to the arrays, not to their lengths, which come with
+  // them).  In a small step the round trips are all there is.
+  int L = uniform_load(p.ell, q);
+  const int64_t row0 = p.row_off ? uniform_load(p.row_off, q) : (int64_t)q * (p.gamma + 1);
+  const bool has_hist = p.hist && p.hist_stride > 0;
+  int hl = has_hist ? uniform_load(p.hist_len, q) : 0;
+  const int pl = has_hist && p.prompt_len ? uniform_load(p.prompt_len, q) : 0;
+  const float rep_in = p.rep ? uniform_load(p.rep, q) : 1.0f;
+  const float pres_in = p.pres ? uniform_load(p.pres, q) : 0.0f;
+  const float freq_in = p.freq ? uniform_load(p.freq, q) : 0.0f;
+  constexpr int kBatch = 4;  // ids in flight per thread
+  const int32_t* hist = p.hist + (int64_t)q * p.hist_stride;
+  int id[kBatch];
+  auto load_ids = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kLogThreads;
+      id[u] = hist[i < p.hist_stride ? i : p.hist_stride - 1];
+    }
+  };
+  if (has_hist) load_ids(tid);
+  const int32_t* bias_id = p.bias_id + (int64_t)q * p.nbias;
+  int first_bias = -1;
+  if (p.nbias > 0) first_bias = bias_id[tid < p.nbias ? tid : p.nbias - 1];
+
   if (L < 0 || L > p.gamma) {
     if (tell) raise_fault(p.status, DSPARK_FAULT_LEN);
     L = L < 0 ? 0 : p.gamma;
   }
-  const int64_t row0 = p.row_off ? p.row_off[q] : (int64_t)q * (p.gamma + 1);
-  auto param = [&](const float* a, float none, bool positive) {
-    const float x = a ? a[q] : none;
+  auto param = [&](float x, float none, bool positive) {
     const bool bad = !(fabsf(x) <= FLT_MAX) || (positive && !(x > 0.0f));
     if (bad && tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
     return bad ? none : x;
   };
-  const float rep = param(p.rep, 1.0f, true), pres = param(p.pres, 0.0f, false);
-  const float freq = param(p.freq, 0.0f, false);
+  const float rep = param(rep_in, 1.0f, true), pres = param(pres_in, 0.0f, false);
+  const float freq = param(freq_in, 0.0f, false);
+  const float inv = 1.0f / rep;  // l / rep as l * inv: off by one more rounding, 2^-24
 
-  // the row pointers, and the first row's logits under way before the history is scanned
+  // A row's operands: its mask's bits of the thread's ids, then its logits.  Loads return in
+  // order, so a row waits for its own only if all of them are issued a row ahead.
+  struct Row {
+    Raw8<T> x[kLogGroups];
+    uint32_t bits[kLogGroups];
+  };
   auto row_ok = [&](int j) { return row0 + j >= 0 && row0 + j < p.rows; };
-  auto load_row = [&](int j, Raw8<T> (&r)[kLogGroups]) {
+  auto load_row = [&](int j, Row& r) {
+#pragma unroll
+    for (int g = 0; g < kLogGroups; ++g) r.bits[g] = 0xFFu;
+    if (!row_ok(j)) return;
+    if (p.mask) {
+      const int64_t at = (int64_t)q * (p.gamma + 1) + j;
+      const int64_t i = p.mask_idx ? uniform_load(p.mask_idx, at) : at;
+      if (i < -1 || i >= p.n_mask) {
+        if (tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
+      } else if (i >= 0) {
+        const uint8_t* allow = reinterpret_cast<const uint8_t*>(p.mask + i * p.mask_stride);
+#pragma unroll
+        for (int g = 0; g < kLogGroups; ++g) {
+          const int v = v0 + g * kLogSpan + tid * 8;
+          if (v < p.V) r.bits[g] = allow[v >> 3];
+        }
+      }
+    }
     const T* src = static_cast<const T*>(p.logits) + (row0 + j) * p.row_stride;
 #pragma unroll
     for (int g = 0; g < kLogGroups; ++g) {
       const int v = v0 + g * kLogSpan + tid * 8;
-      if (v < p.V) r[g].load(src + v);
+      if (v < p.V) r.x[g].load(src + v);
     }
   };
-  Raw8<T> next[kLogGroups];
-  if (row_ok(0)) load_row(0, next);
+  Row next;
+  load_row(0, next);  // under way while the history is scanned
 
-  for (int i = tid; i < kLogSlice; i += kLogThreads) seen[i] = 0;
-  if (p.nbias > 0)
-    for (int i = tid; i < kLogSlice; i += kLogThreads) last_bias[i] = 0;
-  __syncthreads();
-  if (p.hist) {
-    int hl = p.hist_len[q], pl = p.prompt_len ? p.prompt_len[q] : 0;
-    const bool bad = hl < 0 || hl > p.hist_stride || pl < 0 || pl > hl;
-    if (bad && tell) raise_fault(p.status, DSPARK_FAULT_LEN);
-    hl = hl < 0 ? 0 : (hl > p.hist_stride ? p.hist_stride : hl);
-    const int32_t* hist = p.hist + (int64_t)q * p.hist_stride;
-    for (int i = tid; i < hl; i += kLogThreads) {
-      const int id = hist[i];
-      const uint32_t at = (uint32_t)(id - v0);
-      if (id < 0 || id >= p.V) {
-        if (blockIdx.x == 0) raise_fault(p.status, DSPARK_FAULT_TOKEN);
-      } else if (at < kLogSlice) {
-        if (i < pl)
-          atomicOr(&seen[at], kInPrompt);
-        else
-          atomicAdd(&seen[at], 1u);
-      }
-    }
-  }
-  for (int i = tid; i < p.nbias; i += kLogThreads) {
-    const int id = p.bias_id[(int64_t)q * p.nbias + i];
-    const uint32_t at = (uint32_t)(id - v0);
-    if (id < -1 || id >= p.V) {
-      if (blockIdx.x == 0) raise_fault(p.status, DSPARK_FAULT_TOKEN);
-    } else if (id >= 0 && at < kLogSlice) {
-      atomicMax(&last_bias[at], i + 1);
-    }
-  }
-  __syncthreads();
-
+  auto clear = [&]() {
+    for (int i = tid; i < kLogSlice / 4; i += kLogThreads)
+      reinterpret_cast<uint4*>(word)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+  };
   uint32_t w[kLogGroups][8];
   float add[kLogGroups][8];
   bool touched[kLogGroups];
+  clear();
+  if (has_hist) {
+    const bool bad = hl < 0 || hl > p.hist_stride || pl < 0 || pl > hl;
+    if (bad && tell) raise_fault(p.status, DSPARK_FAULT_LEN);
+    hl = hl < 0 ? 0 : (hl > p.hist_stride ? p.hist_stride : hl);
+    for (int i0 = tid; i0 < hl; i0 += kBatch * kLogThreads) {
+      if (i0 != tid) load_ids(i0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int i = i0 + u * kLogThreads;
+        const uint32_t at = (uint32_t)(id[u] - v0);
+        if (i >= hl) continue;
+        if (id[u] < 0 || id[u] >= p.V) {
+          if (blockIdx.x == 0) raise_fault(p.status, DSPARK_FAULT_TOKEN);
+        } else if (at < kLogSlice) {
+          if (i < pl)
+            atomicOr(&word[at], kInPrompt);
+          else
+            atomicAdd(&word[at], 1u);
+        }
+      }
+    }
+  }
+  __syncthreads();
 #pragma unroll
   for (int g = 0; g < kLogGroups; ++g) {
     touched[g] = false;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int at = g * kLogSpan + tid * 8 + e;
-      w[g][e] = seen[at];
-      const int b = p.nbias > 0 ? last_bias[at] : 0;
-      add[g][e] = b > 0 ? p.bias[(int64_t)q * p.nbias + b - 1] : 0.0f;
-      touched[g] = touched[g] || w[g][e] != 0 || b > 0;
+      w[g][e] = word[g * kLogSpan + tid * 8 + e];
+      add[g][e] = 0.0f;
+      touched[g] = touched[g] || w[g][e] != 0;
     }
+  }
+  if (p.nbias > 0) {
+    __syncthreads();
+    clear();
+    for (int i = tid; i < p.nbias; i += kLogThreads) {
+      const int id = i == tid ? first_bias : bias_id[i];
+      const uint32_t at = (uint32_t)(id - v0);
+      if (id < -1 || id >= p.V) {
+        if (blockIdx.x == 0) raise_fault(p.status, DSPARK_FAULT_TOKEN);
+      } else if (id >= 0 && at < kLogSlice) {
+        atomicMax(&word[at], (uint32_t)i + 1);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < kLogGroups; ++g)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t i = word[g * kLogSpan + tid * 8 + e];
+        if (i > 0) {
+          add[g][e] = p.bias[(int64_t)q * p.nbias + i - 1];
+          touched[g] = true;
+        }
+      }
   }
 
   for (int j = 0; j <= L; ++j) {
-    Raw8<T> cur[kLogGroups];
-#pragma unroll
-    for (int g = 0; g < kLogGroups; ++g) cur[g] = next[g];
-    if (j < L && row_ok(j + 1)) load_row(j + 1, next);
+    Row cur = next;
+    if (j < L) load_row(j + 1, next);
     if (j > 0) {  // the token drafted between the last row and this one
-      const int id = p.x[(int64_t)q * p.gamma + j - 1];
+      const int id = uniform_load(p.x, (int64_t)q * p.gamma + j - 1);
       if ((id < 0 || id >= p.V) && tell) raise_fault(p.status, DSPARK_FAULT_TOKEN);
+      const uint32_t in = (uint32_t)(id - v0);
+      if (id >= 0 && id < p.V && in < kLogSlice) {
 #pragma unroll
-      for (int g = 0; g < kLogGroups; ++g) {
-        const uint32_t at = (uint32_t)(id - (v0 + g * kLogSpan + tid * 8));
-        if (id >= 0 && id < p.V && at < 8) {
-          touched[g] = true;
+        for (int g = 0; g < kLogGroups; ++g) {
+          const uint32_t at = in - (uint32_t)(g * kLogSpan + tid * 8);
+          touched[g] = touched[g] || at < 8;
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[g][e] += at == (uint32_t)e ? 1u : 0u;
         }
@@ -179,38 +248,26 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
       if (tell) raise_fault(p.status, DSPARK_FAULT_LEN);
       continue;
     }
-    const uint8_t* allow = nullptr;  // a bit per id
-    if (p.mask) {
-      const int64_t at = (int64_t)q * (p.gamma + 1) + j;
-      const int64_t i = p.mask_idx ? p.mask_idx[at] : at;
-      if (i < -1 || i >= p.n_mask) {
-        if (tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
-      } else if (i >= 0) {
-        allow = reinterpret_cast<const uint8_t*>(p.mask + i * p.mask_stride);
-      }
-    }
     T* dst = static_cast<T*>(p.out) + ((int64_t)q * (p.gamma + 1) + j) * p.V;
 #pragma unroll
     for (int g = 0; g < kLogGroups; ++g) {
       const int v = v0 + g * kLogSpan + tid * 8;
       if (v >= p.V) continue;
-      const uint32_t bits = allow ? allow[v >> 3] : 0xFFu;
+      const uint32_t bits = cur.bits[g];
       if (touched[g] || bits != 0xFFu) {
         float l[8];
-        cur[g].get(l);
+        cur.x[g].get(l);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          if (w[g][e] != 0) {
-            const float c = (float)(w[g][e] & ~kInPrompt);
-            l[e] = l[e] > 0.0f ? l[e] / rep : l[e] * rep;
-            l[e] -= freq * c + (c > 0.0f ? pres : 0.0f);
-          }
-          l[e] += add[g][e];
+          // branch-free: ids that nothing touches are multiplied by 1 and lose 0
+          const float c = (float)(w[g][e] & ~kInPrompt);
+          l[e] *= w[g][e] == 0 ? 1.0f : (l[e] > 0.0f ? inv : rep);
+          l[e] = fmaf(-freq, c, l[e]) - (c > 0.0f ? pres : 0.0f) + add[g][e];
           l[e] = (bits >> e) & 1 ? l[e] : -INFINITY;
         }
-        cur[g].set(l);
+        cur.x[g].set(l);
       }
-      cur[g].store(dst + v);
+      cur.x[g].store(dst + v);
     }
   }
 }
