@@ -652,67 +652,69 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
   const int b = blockIdx.x;
   const AttJoint jt = p.joint[b];
   if (jt.count == 0) return;
-  const int lane = threadIdx.x & 63, row = blockIdx.y * 4 + (threadIdx.x >> 6);
-  const int mi = jt.tile * MR + row;
-  if (mi >= jt.M) return;
+  const int lane = threadIdx.x & 63;
   const int mine = lane / LP, d = 4 * (lane % LP);
   auto piece = [&](int k) {
     return p.part + ((int64_t)(b - 1 + k) * 2 + (k == 0 ? jt.slot : 0)) * MR * (D + 2);
   };
-  float m = -INFINITY, l = 0.0f;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k0 = 0; k0 < jt.count; k0 += kBatch * NP) {
-    f32x4 x[kBatch];
-    float pm[kBatch], pl[kBatch];
+  const int rows = min(MR, jt.M - jt.tile * MR);
+  for (int row = blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += 4 * gridDim.y) {
+    const int mi = jt.tile * MR + row;
+    float m = -INFINITY, l = 0.0f;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k0 = 0; k0 < jt.count; k0 += kBatch * NP) {
+      f32x4 x[kBatch];
+      float pm[kBatch], pl[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {  // pieces past the last: the last, with no weight
-      const int k = k0 + u * NP + mine;
-      const float* y = piece(k < jt.count ? k : jt.count - 1);
-      x[u] = *reinterpret_cast<const f32x4*>(y + row * D + d);
-      pm[u] = k < jt.count ? y[MR * D + row] : -INFINITY;
-      pl[u] = y[MR * (D + 1) + row];
+      for (int u = 0; u < kBatch; ++u) {  // pieces past the last: the last, with no weight
+        const int k = k0 + u * NP + mine;
+        const float* y = piece(k < jt.count ? k : jt.count - 1);
+        x[u] = *reinterpret_cast<const f32x4*>(y + row * D + d);
+        pm[u] = k < jt.count ? y[MR * D + row] : -INFINITY;
+        pl[u] = y[MR * (D + 1) + row];
+      }
+      float mn = m;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, pm[u]);
+      const float ref = mn == -INFINITY ? 0.0f : mn;
+      float f = __builtin_amdgcn_exp2f(m - ref);
+      l *= f;
+      acc *= f;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        // where a piece has no weight its row stays out (0 * inf is none); its sum is finite, or
+        // NaN where the row's scores are
+        f = __builtin_amdgcn_exp2f(pm[u] - ref);
+        l = fmaf(pl[u], f, l);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? fmaf(x[u][e], f, acc[e]) : acc[e];
+      }
+      m = mn;
     }
-    float mn = m;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) mn = fmaxf(mn, pm[u]);
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    float f = __builtin_amdgcn_exp2f(m - ref);
-    l *= f;
-    acc *= f;
+    for (int w = LP; w < kWave; w *= 2) {  // the lanes that hold the same d
+      const float m2 = __shfl_xor(m, w, kWave), mm = fmaxf(m, m2);
+      const float ref = mm == -INFINITY ? 0.0f : mm;
+      const float f1 = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
+      l = l * f1 + __shfl_xor(l, w, kWave) * f2;
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      // where a piece has no weight its row stays out (0 * inf is none); its sum is finite, or
-      // NaN where the row's scores are
-      f = __builtin_amdgcn_exp2f(pm[u] - ref);
-      l = fmaf(pl[u], f, l);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? fmaf(x[u][e], f, acc[e]) : acc[e];
+      for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f1 + __shfl_xor(acc[e], w, kWave) * f2;
+      m = mm;
     }
-    m = mn;
-  }
+    if (mine != 0) continue;
+    acc *= l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t at = (int64_t)(jt.a + mi / p.G) * p.Hq + jt.head * p.G + mi % p.G;
+    T* out = static_cast<T*>(p.o) + at * D + d;
+    if constexpr (std::is_same<T, uint16_t>::value) {
+      bf16x4 z;
 #pragma unroll
-  for (int w = LP; w < kWave; w *= 2) {  // the lanes that hold the same d
-    const float m2 = __shfl_xor(m, w, kWave), mm = fmaxf(m, m2);
-    const float ref = mm == -INFINITY ? 0.0f : mm;
-    const float f1 = __builtin_amdgcn_exp2f(m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
-    l = l * f1 + __shfl_xor(l, w, kWave) * f2;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = acc[e] * f1 + __shfl_xor(acc[e], w, kWave) * f2;
-    m = mm;
+      for (int e = 0; e < 4; ++e) z[e] = (__bf16)acc[e];
+      *reinterpret_cast<bf16x4*>(out) = z;
+    } else {
+      *reinterpret_cast<f32x4*>(out) = acc;
+    }
+    if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
   }
-  if (mine != 0) return;
-  acc *= l == 0.0f ? 0.0f : 1.0f / l;
-  const int64_t at = (int64_t)(jt.a + mi / p.G) * p.Hq + jt.head * p.G + mi % p.G;
-  T* out = static_cast<T*>(p.o) + at * D + d;
-  if constexpr (std::is_same<T, uint16_t>::value) {
-    bf16x4 z;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) z[e] = (__bf16)acc[e];
-    *reinterpret_cast<bf16x4*>(out) = z;
-  } else {
-    *reinterpret_cast<f32x4*>(out) = acc;
-  }
-  if (p.lse && d == 0) p.lse[at] = (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // ---------------------------------------------------------------------------------------
@@ -756,7 +758,10 @@ static int att_launch(const AttParams& p, hipStream_t stream) {
   const int sh = att_lds(D, dt), grid = att_grid(D, dt);
   ensure_dynamic_lds(reinterpret_cast<const void*>(kern), sh, raised);
   kern<<<grid, kAttThreads, sh, stream>>>(p);
-  attention_join_kernel<T, D, MT><<<dim3(grid, 8 * MT), 256, 0, stream>>>(p);
+  // a wave per row of a row tile, as far as the host knows how many rows there are
+  const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
+  const int slices = m < 32 * MT ? (int)(m + 3) / 4 : 8 * MT;
+  attention_join_kernel<T, D, MT><<<dim3(grid, slices), 256, 0, stream>>>(p);
   return launch_status();
 }
 
