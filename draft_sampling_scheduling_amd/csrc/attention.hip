@@ -31,7 +31,6 @@ constexpr int kAttWaves = 2;
 constexpr int kAttThreads = kAttWaves * kWave;
 constexpr int kTok = 32;                     // tokens of a wave's tile
 constexpr int kRound = kAttWaves * kTok;     // tokens of a round
-constexpr int kStages = 2;
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
@@ -122,6 +121,20 @@ struct Tile {
   }
 };
 
+// How a variant (element type, D, row tiles of 32 query rows per wave) sits on a CU.
+//   STAGES 2: a wave's K and V tiles are copied two tiles deep.  STAGES 1: one buffer each; K's
+//   next tile is under way as soon as the scores are taken, V's as soon as O is.  Half the
+//   LDS, twice the workgroups.
+//   PER_CU workgroups are resident, of two waves, so PER_CU / 2 waves share a SIMD: where
+//   registers allow two of them, one's set-up and merge hide behind the other's tiles.
+template <class T, int D, int MT>
+struct Fit {
+  static constexpr bool kBf = std::is_same<T, uint16_t>::value;
+  static constexpr int STAGES = (kBf && D == 64) || (kBf && MT == 2) ? 2 : 1;
+  static constexpr int LDS = kAttWaves * STAGES * 2 * kTok * D * (kBf ? 2 : 4);
+  static constexpr int PER_CU = LDS <= 32 * 1024 ? 4 : 2;
+};
+
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -163,7 +176,7 @@ __device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 *
 template <class T, int D, int MT>
 struct AttWave {
   using L = Tile<T, D>;
-  static constexpr int ND = D / 32;
+  static constexpr int ND = D / 32, STAGES = Fit<T, D, MT>::STAGES;
 
   const AttParams& p;
   int lane, n, h;           // n: lane's column (query row of the tile), h: half-wave
@@ -193,7 +206,7 @@ struct AttWave {
       pg[g] = sload(pages, i);
     }
   }
-  __device__ __forceinline__ void copy_tile(int t0, int (&pg)[4], int s) const {
+  __device__ __forceinline__ void known(int (&pg)[4]) const {
     bool bad = false;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -202,23 +215,26 @@ struct AttWave {
       pg[g] = out ? 0 : pg[g];
     }
     if (bad && lane == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
+  }
+  template <bool V>
+  __device__ __forceinline__ void copy(int t0, const int (&pg)[4], int s) const {
     const int lr = lane / L::CPR, pos = lane % L::CPR;
     const uint32_t row = (uint32_t)(lr * (int)p.tok_b);
-    const uint32_t to = base + s * 2 * L::BYTES;
+    const uint32_t to = base + (2 * s + V) * L::BYTES;
     const int in_page = (1 << p.lg) - 1;
 #pragma unroll
     for (int c = 0; c < L::NC; ++c) {
-      const int64_t off = pg[(c * L::RPC) >> 3] * p.page_b + (int64_t)((t0 + c * L::RPC) & in_page) * p.tok_b;
-      const uint32_t kc = (uint32_t)((pos ^ L::kswz(lr) ^ L::kswz(c * L::RPC)) << 4);
-      const uint32_t vc = (uint32_t)((pos ^ L::vswz(lr) ^ L::vswz(c * L::RPC)) << 4);
-      dma16s(kh + off, row + kc, to + c * 1024);
-      dma16s(vh + off, row + vc, to + L::BYTES + c * 1024);
+      const int64_t off = pg[(c * L::RPC) >> 3] * p.page_b +
+                          (int64_t)((t0 + c * L::RPC) & in_page) * p.tok_b;
+      const int x = V ? L::vswz(lr) ^ L::vswz(c * L::RPC) : L::kswz(lr) ^ L::kswz(c * L::RPC);
+      dma16s((V ? vh : kh) + off, row + (uint32_t)((pos ^ x) << 4), to + c * 1024);
     }
   }
 
   // One tile in stage s: tokens t0 .. t0 + 31.  `edge`: some of them are of the block, or
-  // behind it.
-  __device__ __forceinline__ void tile(int t0, int s, bool edge) {
+  // behind it.  One stage: pg holds the pages of the wave's next tile (`more`: there is one),
+  // which is copied in between.
+  __device__ __forceinline__ void tile(int t0, int s, bool edge, bool more, int (&pg)[4]) {
     const uint32_t ks = base + s * 2 * L::BYTES, vs = ks + L::BYTES;
     f32x16 sc[MT];
 #pragma unroll
@@ -232,10 +248,13 @@ struct AttWave {
         for (int mt = 0; mt < MT; ++mt) mfma_qk<T>(a, qf[mt][st], sc[mt]);
       }
     }
-    bool odd = false;  // the tile's V holds infinities or NaN
-    if (edge) {
-      mask(t0, sc);
-      odd = clean_values(t0, vs);
+    if (edge) mask(t0, sc);
+    if (STAGES == 1) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (more && !edge) {  // (an edge tile may still need K's buffer)
+        known(pg);
+        copy<false>(t0 + kRound, pg, 0);
+      }
     }
     const float c2 = p.scale * kLog2e;
 #pragma unroll
@@ -267,7 +286,13 @@ struct AttWave {
       }
       l[mt] += sum;  // this half-wave's tokens; the halves are added at the end
     }
-    if (odd) odd_values(ks, vs, sc);  // leaves V's tile at 0
+    if (STAGES == 1) {
+      if (more && !edge)
+        vm_wait<L::NC>();
+      else
+        vm_wait<0>();
+    }
+    if (edge && clean_values(t0, vs)) odd_values(ks, vs, sc);  // leaves V's tile at 0
     if constexpr (L::kBf) {
       // O^T += V^T P^T, 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens
       // of it, rounded to bf16 (each weight off by 2^-8 of itself at most, as o is when stored);
@@ -408,7 +433,9 @@ struct AttWave {
     int pg[4];
     if (nt > 0) {
       page_ids(first, pg);
-      copy_tile(first, pg, 0);
+      known(pg);
+      copy<false>(first, pg, 0);
+      copy<true>(first, pg, 0);
       page_ids(first + kRound, pg);  // past the end: the last page's
     }
 #pragma unroll
@@ -431,17 +458,34 @@ struct AttWave {
       for (int dt = 0; dt < ND; ++dt) o[mt][dt] = f32x16{};
     }
     for (int k = 0; k < nt; ++k) {
-      const int t0 = first + k * kRound, s = k & 1;
-      if (k + 1 < nt) {
-        copy_tile(t0 + kRound, pg, s ^ 1);
-        page_ids(t0 + 2 * kRound, pg);
-        vm_wait<2 * L::NC>();
+      const int t0 = first + k * kRound;
+      const bool more = k + 1 < nt, edge = t0 + kTok > ctx;
+      if (STAGES == 2) {
+        if (more) {
+          known(pg);
+          copy<false>(t0 + kRound, pg, ~k & 1);
+          copy<true>(t0 + kRound, pg, ~k & 1);
+          page_ids(t0 + 2 * kRound, pg);
+          vm_wait<2 * L::NC>();
+        } else {
+          vm_wait<0>();
+        }
+        tile(t0, k & 1, edge, more, pg);
+        // the stage is free once its reads have returned
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       } else {
-        vm_wait<0>();
+        vm_wait<L::NC>();  // K's tile; V's is waited for before O
+        tile(t0, 0, edge, more, pg);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if (more) {
+          if (edge) {
+            known(pg);
+            copy<false>(t0 + kRound, pg, 0);
+          }
+          copy<true>(t0 + kRound, pg, 0);
+          page_ids(t0 + 2 * kRound, pg);
+        }
       }
-      tile(t0, s, t0 + kTok > ctx);
-      // the stage is free once its reads have returned
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) l[mt] = half_sum(l[mt]);
@@ -469,7 +513,8 @@ struct AttShares {
 };
 
 template <class T, int D, int MT>
-__global__ void __launch_bounds__(kAttThreads, 1) attention_kernel(AttParams p) {
+__global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
+    attention_kernel(AttParams p) {
   using L = Tile<T, D>;
   constexpr int MR = 32 * MT, ND = D / 32;
   extern __shared__ uint4 lds[];
@@ -526,7 +571,7 @@ __global__ void __launch_bounds__(kAttThreads, 1) attention_kernel(AttParams p) 
   int64_t off = uni(start_off);  // units of q's lists before this workgroup's
 
   const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
-  AttWave<T, D, MT> wv(p, base + wave * kStages * 2 * L::BYTES);
+  AttWave<T, D, MT> wv(p, base + wave * Fit<T, D, MT>::STAGES * 2 * L::BYTES);
   for (int64_t u = u0; u < u1;) {
     if (off >= units(rq)) {  // on to the next request, or the next head
       off = 0;
@@ -728,20 +773,31 @@ static int att_mt(int R, int rows, int G, dspark_dtype dt) {
   return (int64_t)((rows + R - 1) / R) * G <= 32 ? 1 : 2;
 }
 
-static int att_lds(int D, dspark_dtype dt) {
-  return kAttWaves * kStages * 2 * kTok * D * (dt == DSPARK_BF16 ? 2 : 4);
-}
+template <class T_, int D_, int MT_>
+struct Variant {
+  using T = T_;
+  static constexpr int D = D_, MT = MT_;
+  // workgroups: as many as stay resident
+  static int grid() { return device_cus() * Fit<T, D, MT>::PER_CU; }
+};
 
-// workgroups: as many as stay resident (two a CU where LDS holds two)
-static int att_grid(int D, dspark_dtype dt) {
-  return device_cus() * (2 * att_lds(D, dt) <= 160 * 1024 ? 2 : 1);
+// f(variant) of the variant that runs these shapes
+template <class F>
+static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
+  const int mt = att_mt(R, rows, G, dt);
+  if (dt == DSPARK_F32) return D == 64 ? f(Variant<float, 64, 1>{}) : f(Variant<float, 128, 1>{});
+  if (D == 64) return mt == 1 ? f(Variant<uint16_t, 64, 1>{}) : f(Variant<uint16_t, 64, 2>{});
+  return mt == 1 ? f(Variant<uint16_t, 128, 1>{}) : f(Variant<uint16_t, 128, 2>{});
 }
 
 static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
   Carve cv(ws);
-  const size_t grid = (size_t)att_grid(D, dt);
-  p.joint = cv.take<AttJoint>(grid);
-  p.part = cv.take<float>(grid * 2 * 32 * att_mt(R, rows, G, dt) * (D + 2));
+  att_variant(R, rows, G, D, dt, [&](auto v) {
+    const size_t grid = (size_t)v.grid();
+    p.joint = cv.take<AttJoint>(grid);
+    p.part = cv.take<float>(grid * 2 * 32 * v.MT * (v.D + 2));
+    return 0;
+  });
   return cv.bytes();
 }
 
@@ -752,10 +808,9 @@ static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt
 
 template <class T, int D, int MT>
 static int att_launch(const AttParams& p, hipStream_t stream) {
-  constexpr dspark_dtype dt = std::is_same<T, uint16_t>::value ? DSPARK_BF16 : DSPARK_F32;
   static std::atomic<uint64_t> raised;
   auto kern = attention_kernel<T, D, MT>;
-  const int sh = att_lds(D, dt), grid = att_grid(D, dt);
+  const int sh = Fit<T, D, MT>::LDS, grid = Variant<T, D, MT>::grid();
   ensure_dynamic_lds(reinterpret_cast<const void*>(kern), sh, raised);
   kern<<<grid, kAttThreads, sh, stream>>>(p);
   // a wave per row of a row tile, as far as the host knows how many rows there are
@@ -820,11 +875,7 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
   p.lse = lse;
   p.status = dev_status;
   if (ws_bytes < att_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
-  const int mt = att_mt(R, rows, p.G, dt);
-  if (dt == DSPARK_BF16) {
-    if (D == 64)
-      return mt == 1 ? att_launch<uint16_t, 64, 1>(p, stream) : att_launch<uint16_t, 64, 2>(p, stream);
-    return mt == 1 ? att_launch<uint16_t, 128, 1>(p, stream) : att_launch<uint16_t, 128, 2>(p, stream);
-  }
-  return D == 64 ? att_launch<float, 64, 1>(p, stream) : att_launch<float, 128, 1>(p, stream);
+  return att_variant(R, rows, p.G, D, dt, [&](auto v) {
+    return att_launch<typename decltype(v)::T, decltype(v)::D, decltype(v)::MT>(p, stream);
+  });
 }
