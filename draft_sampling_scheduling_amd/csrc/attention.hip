@@ -35,11 +35,12 @@ constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
 // A row tile whose list is cut (see attention_kernel): its pieces lie with workgroups b - 1 ..
-// b - 2 + count, in slot 0 of each but the first's, which is slot `slot`.
+// b - 2 + count.  A piece that begins its list is in its workgroup's slot 1, one that begins
+// inside in slot 0; a workgroup has one of each at most.
 struct AttJoint {
   int a, M, head, tile;  // first row and query rows of the request, cache head, row tile
-  int count, slot;       // count 0: nothing to join
-  int pad[2];
+  int count;             // 0: nothing to join
+  int pad[3];
 };
 
 struct AttParams {
@@ -496,21 +497,28 @@ struct AttWave {
 // units, kSetup of them for what a list costs beside its tokens (the queries, the first
 // tile's wait, the merge of the waves; about 8 us where a round takes 3 us with all CUs
 // streaming), which no tokens stand for; all lists, head after head, are one row of
-// units, cut evenly: workgroup b takes share units, the first `more` workgroups one more.
-// A list that is cut has its pieces in the workspace; the first workgroup that begins inside
-// one says so in joint[b].
-constexpr int kSetup = 3;
+// units, cut evenly: workgroup b begins at unit begin(b).  A cut costs the later piece's
+// set-up and the join, so lists of up to kWhole rounds stay whole (39 against 43 us for 2112
+// lists of 3 to 4 rounds); moving cuts of longer lists to a near end lost more in balance
+// than it saved in joins (105 against 117 us for 184 lists of 30).  A list that is cut has
+// its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
+constexpr int kSetup = 3, kWhole = 4;
 
 struct AttShares {
-  int64_t share, more;
+  int64_t share, more;  // units of a workgroup; the first `more` have one more
   __device__ __forceinline__ int64_t begin(int64_t b) const {
     return b * share + (b < more ? b : more);
   }
-  __device__ __forceinline__ int64_t owner(int64_t u) const {
+  __device__ __forceinline__ int64_t owner(int64_t u) const {  // last b with begin(b) <= u
     const int64_t big = more * (share + 1);
     return u < big ? u / (share + 1) : more + (u - big) / share;
   }
 };
+// where a cut at unit `at` of a list of len units falls
+__device__ __forceinline__ int64_t snapped(int64_t at, int64_t len) {
+  if (len <= kSetup + kWhole) return 2 * at <= len ? 0 : len;
+  return at <= kSetup ? 0 : at;
+}
 
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
@@ -572,26 +580,31 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
 
   const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
   AttWave<T, D, MT> wv(p, base + wave * Fit<T, D, MT>::STAGES * 2 * L::BYTES);
-  for (int64_t u = u0; u < u1;) {
+  int64_t u = u0;  // the unit that `off` stands for
+  bool first = true;
+  while (true) {
     if (off >= units(rq)) {  // on to the next request, or the next head
-      off = 0;
+      off -= units(rq);
       if (++q == p.R) {
         q = 0;
         ++head;
       }
+      if (u >= u1) break;
       rq = att_req(p, q, false);
       rq = {uni(rq.a), uni(rq.n), uni(rq.ctx)};
       continue;
     }
     const int64_t len = list(rq);
-    const int mt0 = (int)(off / len), at = (int)(off - mt0 * len);
-    const int64_t left = u1 - u;
-    const int n = left < len - at ? (int)left : (int)(len - at);
-    const int r0 = at > kSetup ? at - kSetup : 0;  // rounds r0 .. r0 + nr
-    const int nr = at + n - kSetup - r0, rounds = (int)len - kSetup;
-    const int64_t first_u = u;
-    u += n;
-    off += n;
+    const int mt0 = (int)(off / len);
+    const int64_t at = off - mt0 * len, s = u - at;  // the list's units are s .. s + len
+    int64_t from = first ? snapped(at, len) : at;
+    const int64_t to = u1 - s >= len ? len : (u1 - s <= 0 ? 0 : snapped(u1 - s, len));
+    first = false;
+    if (to <= 0) break;
+    u += len - at;
+    off += len - at;
+    from = from > kSetup ? from - kSetup : 0;
+    const int r0 = (int)from, nr = (int)(to - kSetup - from), rounds = (int)len - kSetup;
     if (nr <= 0) continue;
     wv.segment(rq, q, head, mt0 * MR, r0, nr, wave);
 
@@ -629,8 +642,7 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
         const int row = 32 * mt + wv.n, mi = mt0 * MR + row;
         if (mi >= M) continue;
         const int64_t at = (int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G;
-        const int slot = first_u == u0 ? 0 : 1;
-        float* part = p.part + ((int64_t)b * 2 + slot) * MR * (D + 2);
+        float* part = p.part + ((int64_t)b * 2 + (r0 == 0)) * MR * (D + 2);
         if (whole) {
           const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
           f1 *= inv;
@@ -676,38 +688,37 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
     __syncthreads();
     if (wave == 0) finish(First{});
     else finish(Second{});
-    if (tid == 0 && first_u == u0 && r0 > 0) {  // this workgroup begins inside a list
-      const int64_t s = first_u - r0;           // the list's first round
-      const int64_t first = cut.owner(s), last = cut.owner(s + rounds - 1);
-      if (first == b - 1)
-        p.joint[b] = {rq.a, rq.n * p.G, head, mt0, (int)(last - first) + 1,
-                      cut.begin(first) >= s - kSetup ? 0 : 1, {0, 0}};
-    }
+    // this workgroup begins inside a list: the first to do so if the one before it did not
+    if (tid == 0 && r0 > 0 && cut.begin(b - 1) <= s + kSetup)
+      p.joint[b] = {rq.a, rq.n * p.G, head, mt0, (int)(cut.owner(s + len - 1) - b) + 2,
+                    {0, 0, 0}};
+    if (u >= u1) break;
     __syncthreads();  // LDS is the next segment's
   }
 }
 
 // Joins the pieces of the row tiles that are cut: a wave per row, 16 bytes a lane, so that
-// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, eight loads in
-// flight; sums and maxima run over each lane's pieces and meet at the end, always in the
+// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two or twelve
+// such loads in flight; sums and maxima run over each lane's pieces and meet at the end, always in the
 // same order.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
-  constexpr int MR = 32 * MT, LP = D / 4, NP = kWave / LP, kBatch = 8;
+  constexpr int MR = 32 * MT, LP = D / 4, NP = kWave / LP;
   const int b = blockIdx.x;
   const AttJoint jt = p.joint[b];
   if (jt.count == 0) return;
   const int lane = threadIdx.x & 63;
   const int mine = lane / LP, d = 4 * (lane % LP);
   auto piece = [&](int k) {
-    return p.part + ((int64_t)(b - 1 + k) * 2 + (k == 0 ? jt.slot : 0)) * MR * (D + 2);
+    return p.part + ((int64_t)(b - 1 + k) * 2 + (k == 0)) * MR * (D + 2);
   };
   const int rows = min(MR, jt.M - jt.tile * MR);
   for (int row = blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += 4 * gridDim.y) {
     const int mi = jt.tile * MR + row;
     float m = -INFINITY, l = 0.0f;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < jt.count; k0 += kBatch * NP) {
+    auto take = [&](auto batch, int k0) {
+      constexpr int kBatch = decltype(batch)::value;
       f32x4 x[kBatch];
       float pm[kBatch], pl[kBatch];
 #pragma unroll
@@ -735,6 +746,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
         for (int e = 0; e < 4; ++e) acc[e] = f != 0.0f ? fmaf(x[u][e], f, acc[e]) : acc[e];
       }
       m = mn;
+    };
+    if (jt.count <= 2 * NP) {  // as most are: few loads, or those of missing pieces count
+      take(std::integral_constant<int, 2>{}, 0);
+    } else {
+      for (int k0 = 0; k0 < jt.count; k0 += 12 * NP) take(std::integral_constant<int, 12>{}, k0);
     }
 #pragma unroll
     for (int w = LP; w < kWave; w *= 2) {  // the lanes that hold the same d
