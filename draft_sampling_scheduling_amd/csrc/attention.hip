@@ -698,8 +698,8 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
 }
 
 // Joins the pieces of the row tiles that are cut: a wave per row, 16 bytes a lane, so that
-// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two or twelve
-// such loads in flight; sums and maxima run over each lane's pieces and meet at the end, always in the
+// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two, four or
+// twelve such loads in flight; sums and maxima run over each lane's pieces and meet at the end, always in the
 // same order.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
@@ -747,8 +747,11 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
       }
       m = mn;
     };
-    if (jt.count <= 2 * NP) {  // as most are: few loads, or those of missing pieces count
+    // few loads where there are few pieces: those of missing ones take their time too
+    if (jt.count <= 2 * NP) {
       take(std::integral_constant<int, 2>{}, 0);
+    } else if (jt.count <= 4 * NP) {
+      take(std::integral_constant<int, 4>{}, 0);
     } else {
       for (int k0 = 0; k0 < jt.count; k0 += 12 * NP) take(std::integral_constant<int, 12>{}, k0);
     }
