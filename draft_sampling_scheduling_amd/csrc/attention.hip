@@ -869,6 +869,9 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
   if (!q || !k_cache || !v_cache || !table || !ctx || !row_off || !o || !ws || !aligned16(q) ||
       !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(ws))
     return DSPARK_EINVAL;
+  // a row's heads may be read after another's output is written
+  const size_t row_bytes = (size_t)Hq * D * e;
+  if (overlap(q, (size_t)(rows - 1) * q_row * e + row_bytes, o, rows * row_bytes)) return DSPARK_EINVAL;
   AttParams p{};
   p.R = R;
   p.rows = rows;

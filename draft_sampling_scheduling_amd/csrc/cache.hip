@@ -476,7 +476,7 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
   if (R == 0) return DSPARK_OK;
   if (!lens || !ctx || !held || !table || !n_free || !row_off || !ws ||
       (free_len > 0 && !free_pages) || (rows > 0 && (!slot || (parent && !anc))) ||
-      (parent && width < 1))
+      (parent && width < 1) || !aligned16(ws))
     return DSPARK_EINVAL;
   const PlanWs w = carve_plan(ws, R);
   if (ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
@@ -571,8 +571,13 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
       return DSPARK_EINVAL;
   }
   if (R == 0) return DSPARK_OK;
-  if (!n_acc || !ctx || !ctx_out || !held || !table || !ws ||
+  if (!n_acc || !ctx || !ctx_out || !held || !table || !ws || !aligned16(ws) ||
       (done && (!n_free || (free_len > 0 && !free_pages))))
+    return DSPARK_EINVAL;
+  const size_t len_bytes = (size_t)R * sizeof(int32_t);
+  const bool apart = !overlap(ctx_out, len_bytes, ctx, len_bytes);
+  if ((!apart && ctx_out != ctx) || overlap(ctx_out, len_bytes, n_acc, len_bytes) ||
+      overlap(ctx_out, len_bytes, held, len_bytes))
     return DSPARK_EINVAL;
   const CommitWs w = carve_commit(ws, R);
   if (ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
@@ -608,7 +613,6 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   p.tok_stride = tok_stride / u;
   p.status = dev_status;
   p.ws = w;
-  const bool apart = ctx_out + R <= ctx || ctx + R <= ctx_out;
   const bool few = R <= 1024 && (!done || (int64_t)R * max_pages <= kGivePages);
   const int64_t blocks = path ? (int64_t)R * slices : 0;
   if (few && (!path || (apart && blocks < (1 << 24) - 1))) {

@@ -296,7 +296,11 @@ extern "C" int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, co
       (mask && (n_mask < 1 || mask_stride < (V + 31) / 32)))
     return DSPARK_EINVAL;
   // in place only where a row stays where it is
-  if (out == logits && (row_off || row_stride != V)) return DSPARK_EINVAL;
+  const size_t out_bytes = (size_t)R * (gamma + 1) * V * e;
+  const bool in_place = out == logits && !row_off && row_stride == V;
+  if (!in_place && rows > 0 &&
+      overlap(logits, ((size_t)(rows - 1) * row_stride + V) * e, out, out_bytes))
+    return DSPARK_EINVAL;
   LogitsParams p{};
   p.R = R;
   p.gamma = gamma;

@@ -71,4 +71,10 @@ inline bool pages_ok(int page_size, int64_t pages) {
 // element strides whose byte distances keep 16-byte loads aligned
 inline bool stride_ok(int64_t s, size_t esz) { return s >= 0 && (s * (int64_t)esz) % 16 == 0; }
 
+// whether two arrays of so many bytes share any
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return x < y + nb && y < x + na;
+}
+
 }  // namespace dspark

@@ -14,7 +14,8 @@
  * memory, all work enqueued on `stream`, negative returns for calls refused on the host,
  * faults in device data OR-ed into *dev_status (nullable) with every access kept in bounds.
  * No call synchronises or allocates; all may be captured in a graph.  Results do not depend
- * on the order in which workgroups run.
+ * on the order in which workgroups run.  Workspaces are 16-byte aligned, need no preparation
+ * and hold nothing between calls; calls that overlap need one each.
  *
  * Rows.  A step runs `rows` packed rows at most: request q owns rows row_off[q] ..
  * row_off[q+1]-1 (row_off [R+1], on the device); row i of a request is node i of its block:
@@ -108,7 +109,7 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  * Scores, maxima, sums and o are held in float; with bf16 operands the weights exp(s - max)
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row
  * does not see (stale, infinite or NaN) does not reach it.
- * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense.  D in {64, 128};
+ * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.  D in {64, 128};
  * Hq a multiple of Hkv; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
  * aligned.  ctx + n beyond max_pages pages, ctx < 0 or row_off out of order are clamped
  * (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0 (DSPARK_FAULT_PAGE); with
@@ -145,7 +146,8 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  *   one id the last counts; mask [n_mask][mask_stride] uint32 (bit v % 32 of word v / 32
  *   set: allowed; mask_stride >= ceil(V / 32)), mask_idx [R][gamma+1] int32: the row's mask,
  *   -1 none (mask_idx NULL: mask q * (gamma + 1) + j).
- * out may be logits itself where row_off is NULL and row_stride is V.
+ * out may be logits itself where row_off is NULL and row_stride is V, and overlaps it in no
+ * other way.
  * A row whose mask allows nothing is all -inf.
  * Faults: ell outside [0, gamma] (DSPARK_FAULT_LEN, clamped); a row outside [0, rows)
  *   (DSPARK_FAULT_LEN, its out row is left as it was); hist_len outside [0, hist_stride],
@@ -172,7 +174,8 @@ int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *l
  *     elements apart), token ctx[q] + i takes the keys and values that token
  *     ctx[q] + path[q][i-1] had before the call
  *   ctx_out[q] = ctx[q] + n_acc[q] + 1 (the anchor and the accepted nodes; n_acc = -1: the
- *     request had no rows); ctx_out may be ctx
+ *     request had no rows); ctx_out may be ctx, and overlaps ctx, n_acc and held in no
+ *     other way
  *   done [R] int32 (nullable): a request with done != 0 gives its pages back:
  *     free_pages[*n_free ..] takes table[q][0 .. held[q]) in request order, *n_free grows,
  *     held[q] = ctx_out[q] = 0 (its tokens are not moved)

@@ -225,3 +225,36 @@ def test_refusals():
         ds.tree_attention(*ok, ws=torch.empty(256, dtype=torch.uint8, device="cuda:0"))
     none = ds.tree_attention(q[:0], k, v, t, T([40]), T([0, 0]))
     assert none["o"].shape == (0, 4, 64)
+
+
+def test_cache_beyond_32_bits():
+    """Caches of 5 GiB each, their last pages in use: written, read and moved where they are."""
+    import draft_sampling_scheduling_amd as ds
+    g = np.random.default_rng(5)
+    P, Hkv, page, D, n, ctx = 2560, 8, 1024, 128, 5, 1500
+    k, v = (torch.empty(P, Hkv, page, D, dtype=BF, device="cuda:0") for _ in range(2))
+    assert k.numel() * 2 > 2 ** 32
+    table = T([[P - 1, P - 3], [0, P - 2]])
+    rows = torch.from_numpy(g.standard_normal((2, 2, ctx + n, Hkv, D), np.float32)).to(BF)
+    t = np.arange(ctx + n)
+    for q in range(2):
+        slot = table[q].cpu().numpy()[t // page] * page + t % page
+        ds.cache_append(rows[0, q].to("cuda:0"), rows[1, q].to("cuda:0"), k, v, T(slot.tolist()))
+    qs = torch.from_numpy(g.standard_normal((2 * n, 8, D), np.float32)).to(BF)
+    anc = [0, 1, 2, 0b101, 0b1010] * 2  # 1 and 2 under the anchor, 3 under 1, 4 under 2
+    o = ds.tree_attention(qs.to("cuda:0"), k, v, table, T([ctx] * 2), T([0, n, 2 * n]),
+                          anc=T(anc, torch.int64))["o"].double().cpu().numpy()
+    for q in range(2):
+        a = slice(q * n, q * n + n)
+        w = ref.attention(qs[a].double().numpy(), rows[0, q].double().numpy(),
+                          rows[1, q].double().numpy(), ctx, D ** -0.5, ref.sees(n, anc[a]))
+        tol, _ = ref.attention_tol(*w, ctx + n, D, True)
+        assert (np.abs(o[a] - w[0]) <= tol).all()
+    held, free, nf = T([2, 2]), T([0] * 4), T([0])
+    ds.cache_commit(T([2, 2]), T([ctx] * 2), held, table, free, nf, page, path=T([[2, 4]] * 2),
+                    k_cache=k, v_cache=v)
+    for q in range(2):
+        for x, r in ((k, rows[0, q]), (v, rows[1, q])):
+            for i, src in ((1, 2), (2, 4), (3, 3), (0, 0)):
+                at = ctx + i
+                assert torch.equal(x[int(table[q, at // page]), :, at % page].cpu(), r[ctx + src])

@@ -1,0 +1,379 @@
+"""The target-side operators together, as a serving program runs them: whole decode cycles over
+a small two-layer target against its dense form in 64 bits, a tree's accepted path carried
+into the next step, a captured step replayed, and steps on two streams at once."""
+import numpy as np
+import pytest
+import torch
+
+from draft_sampling_scheduling_amd import synth
+from tests import target_ref as ref
+from tests.gpu_util import compare_verify
+
+pytestmark = pytest.mark.gpu
+I32, F32, BF = torch.int32, torch.float32, torch.bfloat16
+
+
+def T(x, dtype=I32):
+    return torch.tensor(np.asarray(x), dtype=dtype, device="cuda:0")
+
+
+class Target:
+    """tokens -> embedding -> two layers of attention with a residual -> logits, in float."""
+
+    def __init__(self, g, V, Hq, Hkv, D, layers=2):
+        E = Hq * D
+        self.V, self.Hq, self.Hkv, self.D, self.layers = V, Hq, Hkv, D, layers
+        self.emb = g.standard_normal((V, E)).astype(np.float32)
+        # keys carry their token's position, so the dense form also pins positions
+        self.pos = g.standard_normal((512, Hkv * D)).astype(np.float32)
+        self.w = [(g.standard_normal((E, (Hq + 2 * Hkv) * D)) / np.sqrt(E)).astype(np.float32)
+                  for _ in range(layers)]
+        self.head = (g.standard_normal((E, V)) / np.sqrt(E)).astype(np.float32)
+        self.dev = {k: torch.from_numpy(np.stack(v) if isinstance(v, list) else v).to("cuda:0")
+                    for k, v in (("emb", self.emb), ("pos", self.pos), ("w", self.w), ("head", self.head))}
+
+    def dense(self, tokens):
+        """[len][V] float64: every token's logits, each seeing itself and all before it."""
+        n, H, K, D = len(tokens), self.Hq, self.Hkv, self.D
+        x = self.emb[tokens].astype(np.float64)
+        for w in self.w:
+            qkv = x @ w.astype(np.float64)
+            q, k, v = np.split(qkv, [H * D, (H + K) * D], 1)
+            k = k + self.pos[:n]
+            o, _, _, _ = ref.attention(q.reshape(n, H, D), k.reshape(n, K, D), v.reshape(n, K, D), 0,
+                                       D ** -0.5, ref.sees(n))
+            x = x + o.reshape(n, H * D)
+        return x @ self.head.astype(np.float64)
+
+    def step(self, ds, tokens, plan, cache, ctx, table, status):
+        """The step's packed rows through the cache; [rows][V] logits."""
+        H, K, D = self.Hq, self.Hkv, self.D
+        x = self.dev["emb"][tokens.long()]
+        n_rows = plan["row_off"][-1:]
+        for i in range(self.layers):
+            qkv = (x @ self.dev["w"][i]).view(-1, H + 2 * K, D)
+            q, k, v = qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:]
+            k += self.dev["pos"][plan["position"].long().clamp(0, 511)].view(-1, K, D)
+            ds.cache_append(k, v, cache[0][i], cache[1][i], plan["slot"], n_rows=n_rows, status=status)
+            a = ds.tree_attention(q, cache[0][i], cache[1][i], table, ctx, plan["row_off"], status=status)
+            x = x + a["o"].view(-1, H * D)
+        return x @ self.dev["head"]
+
+
+def test_decode_cycles(ora):
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V, page, P, W = 6, 4, 512, 8, 60, 12
+    g = np.random.default_rng(11)
+    m = Target(g, V, 4, 2, 64)
+    cfg = synth.scaled(synth.CONFIGS["c1"], R=R, gamma=gamma, V=V, sps_B0=1, sps_B1=40)
+    I = synth.inputs(cfg)
+    W1, W2, w = I["W1"], I["W2"], I["w"]
+    dW2t = T(np.ascontiguousarray(W2.T), F32)
+    sps = synth.sps_table(cfg)
+    cache = [torch.full((m.layers, P, m.Hkv, page, m.D), float("nan"), device="cuda:0") for _ in range(2)]
+    held, ctx, table = T([0] * R), T([0] * R), T(np.full((R, W), -1))
+    free, n_free = T(g.permutation(P)), T([P])
+    status = T([0])
+    rep, pres, freq = 1 + 0.3 * g.random(R), 0.3 * g.random(R), 0.2 * g.random(R)
+    mask = g.integers(0, 2 ** 32, (3, V // 32), dtype=np.uint64).astype(np.uint32)
+    mask |= g.integers(0, 2 ** 32, (3, V // 32), dtype=np.uint64).astype(np.uint32)
+    bias_id, bias = g.integers(-1, V, (R, 3)), g.standard_normal((R, 3)).astype(np.float32)
+
+    def prompt(q):
+        return g.integers(0, V, int(g.integers(1, 30))).tolist()
+
+    text = [prompt(q) for q in range(R)]
+    fresh = list(range(R))
+    for cycle in range(5):
+        if fresh:  # new requests: all but their last token into the cache, the others sit out
+            lens = [len(text[q]) - 1 if q in fresh else 0 for q in range(R)]
+            rows = sum(lens) + 3
+            p = ds.cache_plan(T(lens), ctx, held, table, free, n_free, page, rows=rows, status=status)
+            toks = T(sum((text[q][:-1] for q in fresh), []) + [0] * 3)
+            m.step(ds, toks, p, cache, ctx, table, status)
+            ds.cache_commit(T([k - 1 for k in lens]), ctx, held, table, free, n_free, page, out=ctx,
+                            status=status)
+        assert ctx.tolist() == [len(t) - 1 for t in text] and int(status) == 0
+        x0 = [t[-1] for t in text]
+        U = (1.5 * g.standard_normal((R, gamma, V))).astype(np.float32)
+        h = g.standard_normal((R, gamma, cfg.d)).astype(np.float32)
+        d = ds.draft_markov(T(U, F32), T(h, F32), T(W1, F32), dW2t, T(w, F32), T(x0), 3, cycle)
+        s = ds.schedule(d["c"], T(sps, F32), cfg.sps_B0)
+        if cycle % 2:  # lengths of every kind
+            s["ell"].copy_(T(g.integers(0, gamma + 1, R)))
+        rows = R * (gamma + 1)
+        p = ds.cache_plan(s["ell"], ctx, held, table, free, n_free, page, rows=rows, extra=1,
+                          status=status)
+        live = int(p["row_off"][-1])
+        both = torch.cat([T(x0)[:, None], d["x"]], 1)
+        toks = torch.zeros(rows, dtype=I32, device="cuda:0")
+        node = p["position"][:live] - ctx[p["req"][:live].long()]
+        toks[:live] = both[p["req"][:live].long(), node.long()]
+        lg = m.step(ds, toks, p, cache, ctx, table, status)
+        n = max(len(t) for t in text)
+        hist = np.zeros((R, n), int)
+        for q, t in enumerate(text):
+            hist[q, :len(t)] = t
+        plen = [len(t) // 2 for t in text]
+        idx = g.integers(-1, 3, (R, gamma + 1))
+        f32 = np.float32
+        out = ds.target_logits(lg, s["ell"], d["x"], row_off=p["row_off"], hist=T(hist),
+                               hist_len=T([len(t) for t in text]), prompt_len=T(plen),
+                               rep=T(rep.astype(f32), F32), pres=T(pres.astype(f32), F32),
+                               freq=T(freq.astype(f32), F32), bias_id=T(bias_id), bias=T(bias, F32),
+                               mask=torch.from_numpy(mask.view(np.int32)).to("cuda:0"),
+                               mask_idx=T(idx), status=status)
+        v = ds.verify(out, T(U, F32), dW2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], s["ell"], 3,
+                      cycle, status=status)
+        assert int(status) == 0
+        # the dense form, request by request
+        ell, x = s["ell"].tolist(), d["x"].cpu().numpy()
+        got = out.double().cpu().numpy()
+        target = np.zeros((R, gamma + 1, V))
+        for q in range(R):
+            L = ell[q]
+            full = m.dense(text[q] + x[q, :L].tolist())[len(text[q]) - 1:]
+            ms = [None if k < 0 else (mask[k][np.arange(V) // 32] >> (np.arange(V) % 32)) & 1 == 1
+                  for k in idx[q, :L + 1]]
+            want, _ = ref.logits(full, x[q], text[q], plen[q], rep[q], pres[q], freq[q],
+                                 [(int(a), float(b)) for a, b in zip(bias_id[q], bias[q]) if a >= 0], ms)
+            assert (np.isinf(want) == np.isinf(got[q, :L + 1])).all()
+            # float throughout: sums of up to 512 terms, each off by 512 * 2^-24 of terms that
+            # add up to a few tens in size, through two layers and the head: below 2e-3
+            ok = np.isfinite(want)
+            assert np.abs(want[ok] - got[q, :L + 1][ok]).max() < 2e-3, (cycle, q)
+            target[q, :L + 1] = got[q, :L + 1]
+        o = ora.verify(target.astype(np.float32), U, W2, d["bias_rows"].double().cpu().numpy(), x,
+                       s["ell"].cpu().numpy(), seed=3, cycle=cycle)
+        compare_verify(o, {k: t.cpu().numpy() for k, t in v.items()}, s["ell"].cpu().numpy(),
+                       f"target-cycle-{cycle}")
+        n_acc, y = v["n_acc"].tolist(), v["y"].tolist()
+        for q in range(R):
+            text[q] += y[q][:n_acc[q] + 1]
+        # some end, their pages go to new ones
+        done = [int(cycle > 0 and q % 3 == cycle % 3) for q in range(R)]
+        ds.cache_commit(v["n_acc"], ctx, held, table, free, n_free, page, done=T(done), out=ctx,
+                        status=status)
+        fresh = [q for q in range(R) if done[q]]
+        for q in fresh:
+            text[q] = prompt(q)
+        # every page is somebody's, once
+        pages = free.tolist()[:int(n_free)]
+        for q in range(R):
+            pages += table[q, :int(held[q])].tolist()
+        assert sorted(pages) == list(range(P)), cycle
+        assert ctx.tolist() == [0 if done[q] else len(text[q]) - 1 for q in range(R)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_tree_then_next_step(dtype):
+    """A tree's rows, its accepted path committed, and the next token over what is left."""
+    import draft_sampling_scheduling_amd as ds
+    g = np.random.default_rng(21)
+    R, gamma, Hq, Hkv, D, page = 5, 20, 6, 2, 64, 8
+    ctx0 = [0, 3, 17, 40, 8]
+    n = [21, 9, 1, 14, 21]
+    parent = [[0] + [int(g.integers(0, i)) for i in range(1, gamma + 1)] for _ in range(R)]
+    W = 12
+    table, free = T(np.full((R, W), -1)), T(g.permutation(R * W))
+    held, n_free, status = T([0] * R), T([R * W]), T([0])
+    cache = [torch.full((R * W, Hkv, page, D), float("nan"), dtype=dtype, device="cuda:0") for _ in range(2)]
+
+    def kv(rows):
+        return [torch.from_numpy(g.standard_normal((rows, Hkv, D), np.float32)).to(dtype) for _ in range(2)]
+
+    # contexts
+    p = ds.cache_plan(T(ctx0), T([0] * R), held, table, free, n_free, page, rows=sum(ctx0), status=status)
+    seqs = []
+    a = kv(sum(ctx0))
+    ds.cache_append(a[0].to("cuda:0"), a[1].to("cuda:0"), *cache, p["slot"], status=status)
+    at = 0
+    for c in ctx0:
+        seqs.append([x[at:at + c].double().numpy() for x in a])
+        at += c
+    ctx = T(ctx0)
+    # the trees
+    rows = R * (gamma + 1)
+    p = ds.cache_plan(T([k - 1 for k in n]), ctx, held, table, free, n_free, page, rows=rows, extra=1,
+                      parent=T(parent), status=status)
+    a = kv(rows)
+    ds.cache_append(a[0].to("cuda:0"), a[1].to("cuda:0"), *cache, p["slot"], n_rows=p["row_off"][-1:],
+                    status=status)
+    q = torch.from_numpy(g.standard_normal((rows, Hq, D), np.float32)).to(dtype)
+    got = ds.tree_attention(q.to("cuda:0"), *cache, table, ctx, p["row_off"], anc=p["anc"], status=status)
+    off = np.concatenate([[0], np.cumsum(n)])
+    anc = p["anc"].cpu().numpy()
+
+    def compare(out, lse, qs, k, v, c, see):
+        w = ref.attention(qs.double().numpy(), k, v, c, D ** -0.5, see)
+        to, tl = ref.attention_tol(*w, len(k), D, dtype is BF)
+        assert (np.abs(out.double().cpu().numpy() - w[0]) <= to).all()
+        assert (np.abs(lse.double().cpu().numpy() - w[1]) <= tl).all()
+
+    n_acc, path = [], []
+    for r in range(R):
+        s = slice(off[r], off[r + 1])
+        k, v = (np.concatenate([seqs[r][i], a[i][s].double().numpy()]) for i in range(2))
+        compare(got["o"][s], got["lse"][s], q[s], k, v, ctx0[r], ref.sees(n[r], anc[s]))
+        leaf, way = int(g.integers(0, n[r])), []
+        while leaf:
+            way.append(leaf)
+            leaf = parent[r][leaf]
+        n_acc.append(len(way))
+        path.append(way[::-1] + [0] * (gamma - len(way)))
+        keep = [off[r]] + [off[r] + i for i in way[::-1]]
+        seqs[r] = [np.concatenate([seqs[r][i], a[i][keep].double().numpy()]) for i in range(2)]
+    ds.cache_commit(T(n_acc), ctx, held, table, free, n_free, page, path=T(path), k_cache=cache[0],
+                    v_cache=cache[1], out=ctx, status=status)
+    assert ctx.tolist() == [len(s[0]) for s in seqs]
+    # one more token each
+    p = ds.cache_plan(T([0] * R), ctx, held, table, free, n_free, page, rows=R, extra=1, status=status)
+    a = kv(R)
+    ds.cache_append(a[0].to("cuda:0"), a[1].to("cuda:0"), *cache, p["slot"], status=status)
+    q = torch.from_numpy(g.standard_normal((R, Hq, D), np.float32)).to(dtype)
+    got = ds.tree_attention(q.to("cuda:0"), *cache, table, ctx, p["row_off"], status=status)
+    for r in range(R):
+        k, v = (np.concatenate([seqs[r][i], a[i][r:r + 1].double().numpy()]) for i in range(2))
+        compare(got["o"][r:r + 1], got["lse"][r:r + 1], q[r:r + 1], k, v, len(k) - 1, ref.sees(1))
+    assert int(status) == 0
+
+
+class Step:
+    """One step's buffers; run() plans, appends, attends, shapes the logits and commits."""
+
+    def __init__(self, seed, R=40, gamma=4, Hq=8, Hkv=2, D=64, page=16, V=1000):
+        g = np.random.default_rng(seed)
+        gt = torch.Generator(device="cuda").manual_seed(seed)
+        self.R, self.gamma, self.page, self.rows = R, gamma, page, R * (gamma + 1)
+        self.g, self.V, W = g, V, 20
+        P = R * W
+
+        def rnd(*shape):
+            return torch.randn(*shape, generator=gt, device="cuda").to(BF)
+
+        self.cache0 = [rnd(P, Hkv, page, D) for _ in range(2)]
+        self.cache = [x.clone() for x in self.cache0]
+        self.qkv = rnd(self.rows, Hq + 2 * Hkv, D)
+        self.Hq, self.Hkv = Hq, Hkv
+        self.logits, self.x = rnd(self.rows, V), T(g.integers(0, V, (R, gamma)))
+        self.parent = T([[0] + [int(g.integers(0, i)) for i in range(1, gamma + 1)] for _ in range(R)])
+        self.free = T(g.permutation(P))
+        self.state0 = [torch.zeros(R, dtype=I32, device="cuda"),  # held
+                       torch.full((R, W), -1, dtype=I32, device="cuda"), T([P])]
+        self.state = [x.clone() for x in self.state0]
+        self.ctx, self.lens, self.n_acc = T([0] * R), T([0] * R), T([0] * R)
+        self.path, self.done = T([[0] * gamma] * R), T([0] * R)
+        self.hist, self.hl = T(g.integers(0, V, (R, 30))), T([30] * R)
+        self.pres = torch.ones(R, device="cuda")
+        self.status = T([0])
+        self.change()
+
+    def change(self):
+        g, R, gamma = self.g, self.R, self.gamma
+        self.ctx.copy_(T(g.integers(0, 250, R)))
+        self.lens.copy_(T(g.integers(0, gamma + 1, R)))
+        n = [int(g.integers(0, k + 1)) for k in self.lens.tolist()]
+        self.n_acc.copy_(T(n))
+        self.path.copy_(T([sorted((g.permutation(k) + 1).tolist()[:a]) + [0] * (gamma - a)
+                           for k, a in zip(self.lens.tolist(), n)]))
+        self.done.copy_(T((g.random(R) < 0.2).astype(int)))
+        self.qkv.copy_(torch.randn_like(self.qkv))
+
+    def run(self, ds):
+        for a, b in zip(self.cache + self.state, self.cache0 + self.state0):
+            a.copy_(b)
+        held, table, n_free = self.state
+        free = self.free.clone()
+        p = ds.cache_plan(self.lens, self.ctx, held, table, free, n_free, self.page, rows=self.rows,
+                          extra=1, parent=self.parent, status=self.status,
+                          out=dict(row_off=torch.zeros(self.R + 1, dtype=I32, device="cuda"),
+                                   slot=torch.full((self.rows,), -1, dtype=I32, device="cuda"),
+                                   anc=torch.zeros(self.rows, dtype=torch.int64, device="cuda")))
+        q, k, v = self.qkv.split([self.Hq, self.Hkv, self.Hkv], 1)
+        ds.cache_append(k, v, *self.cache, p["slot"], n_rows=p["row_off"][-1:], status=self.status)
+        out = dict(o=torch.zeros_like(q, memory_format=torch.contiguous_format),
+                   lse=torch.zeros(self.rows, self.Hq, device="cuda"))
+        a = ds.tree_attention(q, *self.cache, table, self.ctx, p["row_off"], anc=p["anc"], out=out,
+                              status=self.status)
+        t = ds.target_logits(self.logits, self.lens, self.x, row_off=p["row_off"], hist=self.hist,
+                             hist_len=self.hl, pres=self.pres, status=self.status,
+                             out=torch.zeros(self.R, self.gamma + 1, self.V, dtype=BF, device="cuda"))
+        c = ds.cache_commit(self.n_acc, self.ctx, held, table, free, n_free, self.page, path=self.path,
+                            done=self.done, k_cache=self.cache[0], v_cache=self.cache[1],
+                            status=self.status)
+        return [p["row_off"], p["slot"], p["anc"], a["o"], a["lse"], t, c, free, *self.state, *self.cache]
+
+
+def snap(outs):
+    torch.cuda.synchronize()
+    return [x.view(torch.int16).clone() if x.dtype == BF else x.clone() for x in outs]
+
+
+def same(a, b):
+    return all(torch.equal(x.nan_to_num() if x.is_floating_point() else x,
+                           y.nan_to_num() if y.is_floating_point() else y) for x, y in zip(a, b))
+
+
+def test_step_graph_replays():
+    import draft_sampling_scheduling_amd as ds
+    s = Step(31)
+    s.run(ds)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        s.run(ds)
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = s.run(ds)
+    for k in range(5):
+        s.change()
+        graph.replay()
+        got = snap(outs)
+        graph.replay()  # a step replayed again gives the same
+        assert same(snap(outs), got), k
+        want = snap(s.run(ds))  # eager work between the replays
+        assert same(got, want), k
+        assert int(s.status) == 0
+
+
+def test_two_streams_at_once():
+    """Two steps at once on two streams, their tensors made on a third, each with workspaces
+    of its own: both as alone."""
+    import draft_sampling_scheduling_amd as ds
+    steps = [Step(41), Step(42, R=24, Hq=10, D=128, V=4104)]
+    want = [snap(s.run(ds)) for s in steps]
+    streams = [torch.cuda.Stream() for _ in steps]
+    torch.cuda.synchronize()
+    for k in range(4):
+        outs = []
+        for s, st in zip(steps, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                outs.append(s.run(ds))
+        for o, w in zip(outs, want):
+            assert same(snap(o), w), k
+
+
+def test_workspaces_given():
+    """A caller's workspace of the stated size serves, whatever it holds; one step's after the
+    other's may be the same."""
+    import draft_sampling_scheduling_amd as ds
+    s = Step(51)
+    want = snap(s.run(ds))
+    att = ds.tree_attention_workspace_bytes(s.R, s.rows, s.Hq, s.Hkv, 64, ds.BF16)
+    for fill in (0, 255, 127):
+        ws = torch.full((max(att, ds.cache_plan_workspace_bytes(s.R)),), fill, dtype=torch.uint8,
+                        device="cuda")
+        for a, b in zip(s.state, s.state0):
+            a.copy_(b)
+        p = ds.cache_plan(s.lens, s.ctx, s.state[0], s.state[1], s.free, s.state[2], s.page, rows=s.rows,
+                          extra=1, parent=s.parent, ws=ws)
+        live = int(p["row_off"][-1])
+        assert torch.equal(p["slot"][:live], want[1][:live])
+        q, k, v = s.qkv.split([s.Hq, s.Hkv, s.Hkv], 1)
+        for a, b in zip(s.cache, s.cache0):
+            a.copy_(b)
+        ds.cache_append(k, v, *s.cache, p["slot"], n_rows=p["row_off"][-1:])
+        a = ds.tree_attention(q, *s.cache, s.state[1], s.ctx, p["row_off"], anc=p["anc"], ws=ws)
+        assert torch.equal(a["o"][:live].view(torch.int16), want[3][:live])

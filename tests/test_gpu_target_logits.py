@@ -116,6 +116,26 @@ def test_headline_vocabulary():
     check(8, 3, 8, 151936, BF, n_hist=2000, nb=20)
 
 
+def test_beyond_32_bits():
+    """5 GB of logits: the last requests as they come out alone."""
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V = 520, 16, 151936
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    lg = torch.randn(R, gamma + 1, V, device="cuda", generator=gen)
+    assert lg.numel() * 4 > 2 ** 32
+    x = torch.randint(0, V, (R, gamma), device="cuda", dtype=I32, generator=gen)
+    ell = torch.full((R,), gamma, device="cuda", dtype=I32)
+    one = torch.ones(R, device="cuda")
+    out = ds.target_logits(lg, ell, x, pres=one, freq=one)
+    for s in (slice(0, 1), slice(R - 2, R)):
+        alone = ds.target_logits(lg[s].contiguous(), ell[s], x[s], pres=one[s], freq=one[s])
+        assert torch.equal(out[s], alone)
+    q = R - 1
+    assert float(out[q, gamma, x[q, 0].long()]) < float(lg[q, gamma, x[q, 0].long()]) - 1.5
+    ds.target_logits(lg, ell, x, pres=one, freq=one, out=lg)
+    assert torch.equal(out, lg)
+
+
 def test_infinities_and_nan():
     def edit(lg):
         f = lg.view(-1)

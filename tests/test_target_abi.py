@@ -57,7 +57,7 @@ def test_plan_refusals(ds):
     for bad in (dict(R=-1), dict(rows=-1), dict(page=12), dict(page=4), dict(page=2048),
                 dict(W=0), dict(W=1 << 27), dict(free_len=-1), dict(extra=2), dict(lens=None),
                 dict(free=None), dict(parent=P(), width=5), dict(parent=P(), anc=P(), width=0),
-                dict(slot=None), dict(wsp=None)):
+                dict(slot=None), dict(wsp=None), dict(wsp=P(0x1002))):
         assert call(**bad) == ds.EINVAL, bad
     assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
     assert call(R=0) == ds.OK
@@ -80,7 +80,7 @@ def test_attention_refusals(ds):
     ws = ds.tree_attention_workspace_bytes(4, 20, 8, 2, 64, ds.BF16)
 
     def call(R=4, rows=20, Hq=8, Hkv=2, D=64, dt=ds.BF16, page=16, W=10, n=40, q=P(), q_row=512,
-             k=P(), st=1024, tok=64, table=P(), scale=0.125, o=P(), wsp=P(), ws_bytes=ws):
+             k=P(), st=1024, tok=64, table=P(), scale=0.125, o=P(0x100000), wsp=P(), ws_bytes=ws):
         return ds.lib().dspark_tree_attention(R, rows, Hq, Hkv, D, dt, page, W, n, q, q_row, k, P(),
                                               2048, st, tok, table, P(), P(), None, scale, o, None,
                                               None, wsp, ws_bytes, None)
@@ -89,7 +89,9 @@ def test_attention_refusals(ds):
                 dict(W=0), dict(n=0), dict(q=None), dict(q=P(0x1002)), dict(q_row=511),
                 dict(k=None), dict(st=1), dict(tok=-64), dict(table=None), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
-                dict(o=None), dict(wsp=None), dict(rows=-1), dict(rows=1 << 28, Hq=8)):
+                dict(o=None), dict(wsp=None), dict(wsp=P(0x1008)), dict(rows=-1),
+                dict(o=P()), dict(o=P(0x1000 + 19 * 1024)),  # over q
+                dict(rows=1 << 28, Hq=8)):
         assert call(**bad) == ds.EINVAL, bad
     assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
     assert call(R=0) == ds.OK and call(rows=0) == ds.OK
@@ -106,7 +108,8 @@ def test_logits_refusals(ds):
                 dict(dt=2), dict(lg=None), dict(lg=P(0x1004)), dict(stride=1016),
                 dict(stride=1025), dict(rows=-1), dict(ell=None), dict(hist=P()), dict(nb=-1),
                 dict(nb=2), dict(mask=P(), n_mask=0, words=32), dict(mask=P(), n_mask=1, words=31),
-                dict(out=None), dict(out=P())):  # in place with packed rows
+                dict(out=None), dict(out=P()),  # in place with packed rows
+                dict(off=None, out=P(0x1800)), dict(lg=P(0x10000))):  # over each other
         assert call(**bad) == ds.EINVAL, bad
     assert call(off=None, out=P(), stride=1032) == ds.EINVAL  # in place, rows spaced
     assert call(R=0) == ds.OK
@@ -116,15 +119,17 @@ def test_commit_refusals(ds):
     ws = ds.cache_commit_workspace_bytes(4)
 
     def call(R=4, gamma=4, page=16, W=10, n_acc=P(), path=P(), done=None, n_free=P(), free=P(),
-             layers=1, Hkv=2, D=64, dt=ds.BF16, n=40, k=P(), st=1024, ws_bytes=ws, free_len=8):
-        return ds.lib().dspark_cache_commit(R, gamma, page, W, free_len, n_acc, path, done, P(),
-                                            P(), P(), P(), free, n_free, layers, Hkv, D, dt, n, k,
+             layers=1, Hkv=2, D=64, dt=ds.BF16, n=40, k=P(), st=1024, ws_bytes=ws, free_len=8,
+             ctx=P(0x2000), out=P(0x2000), held=P(0x3000)):
+        return ds.lib().dspark_cache_commit(R, gamma, page, W, free_len, n_acc, path, done, ctx,
+                                            out, held, P(), free, n_free, layers, Hkv, D, dt, n, k,
                                             P(), 0, 2048, st, 64, None, P(), ws_bytes, None)
 
     for bad in (dict(R=-1), dict(gamma=0), dict(gamma=65), dict(page=20), dict(W=0),
                 dict(n_acc=None), dict(done=P(), n_free=None), dict(done=P(), free=None),
                 dict(layers=-1), dict(Hkv=0), dict(D=12), dict(dt=5), dict(n=0), dict(k=None),
-                dict(k=P(0x1001)), dict(st=1022), dict(free_len=-1)):
+                dict(k=P(0x1001)), dict(st=1022), dict(free_len=-1),
+                dict(out=P(0x2004)), dict(out=P(0x1000)), dict(out=P(0x3008))):
         assert call(**bad) == ds.EINVAL, bad
     assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
     assert call(R=0) == ds.OK
