@@ -504,6 +504,11 @@ struct AttWave {
 // its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
 constexpr int kSetup = 3, kWhole = 4;
 
+// a / b, both at least 0; a 64-bit division is some hundred instructions
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 struct AttShares {
   int64_t share, more;  // units of a workgroup; the first `more` have one more
   __device__ __forceinline__ int64_t begin(int64_t b) const {
@@ -511,7 +516,7 @@ struct AttShares {
   }
   __device__ __forceinline__ int64_t owner(int64_t u) const {  // last b with begin(b) <= u
     const int64_t big = more * (share + 1);
-    return u < big ? u / (share + 1) : more + (u - big) / share;
+    return u < big ? quotient(u, share + 1) : more + quotient(u - big, share);
   }
 };
 // where a cut at unit `at` of a list of len units falls
@@ -541,7 +546,12 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
   const int per = (p.R + kAttThreads - 1) / kAttThreads;
   const int lo = min(p.R, tid * per), hi = min(p.R, lo + per);
   int64_t mine = 0;
-  for (int q = lo; q < hi; ++q) mine += units(att_req(p, q, b == 0));
+  AttReq mine0 = {0, 0, 0};  // request lo
+  for (int q = lo; q < hi; ++q) {
+    const AttReq r = att_req(p, q, b == 0);
+    if (q == lo) mine0 = r;
+    mine += units(r);
+  }
   const int64_t upto = block_scan<kAttThreads>(mine, sums);
   if (tid == kAttThreads - 1) total_s = upto;
   if (tid == 0) p.joint[b].count = 0;
@@ -550,16 +560,16 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
   const int64_t P = U < gridDim.x ? U : gridDim.x;
   if (b >= P) return;
   AttShares cut;
-  cut.share = U / P;
+  cut.share = quotient(U, P);
   cut.more = U - cut.share * P;
   const int64_t u0 = cut.begin(b), u1 = cut.begin(b + 1);
-  int head = (int)(u0 / W);
+  int head = (int)quotient(u0, W);
   {
     const int64_t w = u0 - head * W;
     int64_t at = upto - mine;
     if (w >= at && w < upto) {
       for (int q = lo; q < hi; ++q) {
-        const AttReq r = att_req(p, q, false);
+        const AttReq r = q == lo ? mine0 : att_req(p, q, false);
         const int64_t x = units(r);
         if (w < at + x) {
           start_s[0] = q;
@@ -595,7 +605,7 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
       continue;
     }
     const int64_t len = list(rq);
-    const int mt0 = (int)(off / len);
+    const int mt0 = (int)quotient(off, len);
     const int64_t at = off - mt0 * len, s = u - at;  // the list's units are s .. s + len
     int64_t from = first ? snapped(at, len) : at;
     const int64_t to = u1 - s >= len ? len : (u1 - s <= 0 ? 0 : snapped(u1 - s, len));
@@ -832,6 +842,8 @@ static int att_launch(const AttParams& p, hipStream_t stream) {
   const int sh = Fit<T, D, MT>::LDS, grid = Variant<T, D, MT>::grid();
   ensure_dynamic_lds(reinterpret_cast<const void*>(kern), sh, raised);
   kern<<<grid, kAttThreads, sh, stream>>>(p);
+  // where no request can have more than kWhole rounds, no list is cut
+  if (((int64_t)p.max_pages << p.lg) <= kWhole * kRound) return launch_status();
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
   const int slices = m < 32 * MT ? (int)(m + 3) / 4 : 8 * MT;

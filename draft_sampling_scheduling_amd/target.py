@@ -153,15 +153,21 @@ def _cache(k_cache, v_cache, dev, dims):
     return k_cache.data_ptr(), v_cache.data_ptr(), shape, st[:dims - 1]
 
 
-_fn = {}
+_fns = {}
+
+
+def _fn(name):
+    """The library's function."""
+    f = _fns.get(name)
+    if f is None:
+        from . import lib
+        f = _fns[name] = getattr(lib(), name)
+    return f
 
 
 def _call(dev, name, *args):
     """The library's `name`(*args, stream) on `dev`; raises on a refusal."""
-    f = _fn.get(name)
-    if f is None:
-        from . import lib
-        f = _fn[name] = getattr(lib(), name)
+    f = _fn(name)
     index = dev.index
     if torch.cuda.current_device() == index:
         rc = f(*args, _raw_stream(index))
@@ -187,8 +193,7 @@ def _workspace(nbytes, dev, ws):
 
 
 def cache_plan_workspace_bytes(R) -> int:
-    from . import lib
-    return int(lib().dspark_cache_plan_workspace_bytes(R))
+    return _fn("dspark_cache_plan_workspace_bytes")(R)
 
 
 def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, extra=0,
@@ -246,8 +251,7 @@ def cache_append(k, v, k_cache, v_cache, slot, *, n_rows=None, status=None):
 
 
 def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt) -> int:
-    from . import lib
-    return int(lib().dspark_tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt))
+    return _fn("dspark_tree_attention_workspace_bytes")(R, rows, Hq, Hkv, D, dt)
 
 
 def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=None, out=None,
@@ -346,8 +350,7 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
 
 
 def cache_commit_workspace_bytes(R) -> int:
-    from . import lib
-    return int(lib().dspark_cache_commit_workspace_bytes(R))
+    return _fn("dspark_cache_commit_workspace_bytes")(R)
 
 
 def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path=None, done=None,
