@@ -709,8 +709,8 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
 
 // Joins the pieces of the row tiles that are cut: a wave per row, 16 bytes a lane, so that
 // D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two, four or
-// twelve such loads in flight; sums and maxima run over each lane's pieces and meet at the end, always in the
-// same order.
+// twelve such loads in flight; sums and maxima run over each lane's pieces and meet at the
+// end, always in the same order.
 template <class T, int D, int MT>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
   constexpr int MR = 32 * MT, LP = D / 4, NP = kWave / LP;
@@ -871,7 +871,7 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
                                      void* o, float* lse, int32_t* dev_status, void* ws,
                                      size_t ws_bytes, hipStream_t stream) {
   if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || max_pages < 1 || !pages_ok(page_size, n_pages) ||
-      !pages_ok(page_size, max_pages) || !(scale > 0.0f) || scale > FLT_MAX)
+      !table_ok(page_size, max_pages) || !(scale > 0.0f) || scale > FLT_MAX)
     return DSPARK_EINVAL;
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;
   if (!stride_ok(q_row, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||

@@ -471,7 +471,7 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
                                  int32_t* slot, uint64_t* anc, int32_t* dev_status, void* ws,
                                  size_t ws_bytes, hipStream_t stream) {
   if (R < 0 || rows < 0 || max_pages < 1 || free_len < 0 || extra < 0 || extra > 1 ||
-      !pages_ok(page_size, max_pages))
+      !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
   if (R == 0) return DSPARK_OK;
   if (!lens || !ctx || !held || !table || !n_free || !row_off || !ws ||
@@ -558,7 +558,7 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
                                    int64_t layer_stride, int64_t page_stride,
                                    int64_t head_stride, int64_t tok_stride, int32_t* dev_status,
                                    void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (R < 0 || max_pages < 1 || free_len < 0 || !pages_ok(page_size, max_pages))
+  if (R < 0 || max_pages < 1 || free_len < 0 || !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
   size_t e = 4;
   if (path) {

@@ -63,7 +63,12 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& all
 inline bool page_size_ok(int ps) { return ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 inline int log2_of(int p) { return __builtin_ctz((unsigned)p); }
 
-// a cache of n_pages pages whose tokens and slots fit 31 bits
+// a block table whose tokens leave room to count beyond them in 32 bits
+inline bool table_ok(int page_size, int64_t pages) {
+  return page_size_ok(page_size) && pages >= 1 && pages * page_size <= ((int64_t)1 << 30);
+}
+
+// a cache of n_pages pages whose slots fit 31 bits
 inline bool pages_ok(int page_size, int64_t pages) {
   return page_size_ok(page_size) && pages >= 1 && pages * page_size < ((int64_t)1 << 31);
 }

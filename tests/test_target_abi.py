@@ -55,7 +55,7 @@ def test_plan_refusals(ds):
                                           None, wsp, ws_bytes, None)
 
     for bad in (dict(R=-1), dict(rows=-1), dict(page=12), dict(page=4), dict(page=2048),
-                dict(W=0), dict(W=1 << 27), dict(free_len=-1), dict(extra=2), dict(lens=None),
+                dict(W=0), dict(W=(1 << 26) + 1), dict(free_len=-1), dict(extra=2), dict(lens=None),
                 dict(free=None), dict(parent=P(), width=5), dict(parent=P(), anc=P(), width=0),
                 dict(slot=None), dict(wsp=None), dict(wsp=P(0x1002))):
         assert call(**bad) == ds.EINVAL, bad
@@ -86,7 +86,7 @@ def test_attention_refusals(ds):
                                               None, wsp, ws_bytes, None)
 
     for bad in (dict(Hq=9), dict(Hkv=0), dict(D=80), dict(D=256), dict(dt=2), dict(page=10),
-                dict(W=0), dict(n=0), dict(q=None), dict(q=P(0x1002)), dict(q_row=511),
+                dict(W=0), dict(W=(1 << 26) + 1), dict(n=0), dict(q=None), dict(q=P(0x1002)), dict(q_row=511),
                 dict(k=None), dict(st=1), dict(tok=-64), dict(table=None), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
                 dict(o=None), dict(wsp=None), dict(wsp=P(0x1008)), dict(rows=-1),
