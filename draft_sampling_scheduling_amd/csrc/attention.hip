@@ -27,10 +27,12 @@
 
 namespace dspark {
 
-constexpr int kAttWaves = 2;
-constexpr int kAttThreads = kAttWaves * kWave;
-constexpr int kTok = 32;                     // tokens of a wave's tile
-constexpr int kRound = kAttWaves * kTok;     // tokens of a round
+#ifndef ATT_S
+#define ATT_S(NR, D) (NR == 2 ? 2 : 4)
+#define ATT_P(NR, D) (NR == 2 ? 4 : 2)
+#endif
+constexpr int kTok = 32;  // tokens of a tile
+constexpr int kRows = 32;  // query rows of a wave
 constexpr float kSlack = 8.0f;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
 
@@ -122,18 +124,27 @@ struct Tile {
   }
 };
 
-// How a variant (element type, D, row tiles of 32 query rows per wave) sits on a CU.
-//   STAGES 2: a wave's K and V tiles are copied two tiles deep.  STAGES 1: one buffer each; K's
-//   next tile is under way as soon as the scores are taken, V's as soon as O is.  Half the
-//   LDS, twice the workgroups.
-//   PER_CU workgroups are resident, of two waves, so PER_CU / 2 waves share a SIMD: where
-//   registers allow two of them, one's set-up and merge hide behind the other's tiles.
-template <class T, int D, int MT>
+// How a variant (element type, D, NR: waves over query rows) sits on a CU.
+//   NR 1, up to 32 query rows: the two waves of a workgroup take 32 tokens each, have their
+//   tiles to themselves (no barrier), and merge at the end.  STAGES 2: K and V are copied two
+//   tiles deep.  STAGES 1: one buffer each; K's next tile is under way as soon as the scores
+//   are taken, V's as soon as O is: half the LDS, twice the workgroups.
+//   NR 2 or 4, up to 64 or 128 rows: every wave has 32 rows of its own, and all share each
+//   tile of 32 tokens, copied STAGES - 1 ahead by all of them, with a barrier per tile; the
+//   cache is read once for all rows.
+//   PER_CU workgroups are resident; where registers allow two waves a SIMD, one's set-up,
+//   exponentials and merge hide behind the other's tiles.
+template <class T, int D, int NR>
 struct Fit {
   static constexpr bool kBf = std::is_same<T, uint16_t>::value;
-  static constexpr int STAGES = (kBf && D == 64) || (kBf && MT == 2) ? 2 : 1;
-  static constexpr int LDS = kAttWaves * STAGES * 2 * kTok * D * (kBf ? 2 : 4);
-  static constexpr int PER_CU = LDS <= 32 * 1024 ? 4 : 2;
+  static constexpr int WAVES = NR == 1 ? 2 : NR;
+  static constexpr int THREADS = WAVES * kWave;
+  static constexpr int ROUND = NR == 1 ? 2 * kTok : kTok;  // tokens of a round
+  static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
+  static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : ATT_S(NR, D);
+  static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
+  static constexpr int PER_CU = NR == 1 ? (LDS <= 32 * 1024 ? 4 : 2) : ATT_P(NR, D);
+  static constexpr int PER_SIMD = PER_CU * WAVES / 4;
 };
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -174,141 +185,140 @@ __device__ __forceinline__ void mfma_qk(u32x4 a, u32x4 b, f32x16& acc) {
 // token of accumulator register r of half-wave h, within a tile; also d within 32 for O^T
 __device__ __forceinline__ int reg_row(int r, int h) { return 8 * (r >> 2) + 4 * h + (r & 3); }
 
-template <class T, int D, int MT>
+// What one wave holds: 32 query rows, and its running m, l and O of them.
+template <class T, int D, int NR>
 struct AttWave {
   using L = Tile<T, D>;
-  static constexpr int ND = D / 32, STAGES = Fit<T, D, MT>::STAGES;
+  using F = Fit<T, D, NR>;
+  static constexpr int ND = D / 32;
+  // rows of a tile that this wave copies, from row `mine` on, and groups of 8 of them
+  static constexpr int CROWS = kTok / NR, CG = CROWS / 8, NC = L::NC / NR;
 
   const AttParams& p;
-  int lane, n, h;           // n: lane's column (query row of the tile), h: half-wave
-  uint32_t base;            // this wave's LDS
+  int lane, n, h, wave;     // n: lane's column (query row of the wave's 32), h: half-wave
+  int mine;                 // first row of a tile that this wave copies
+  uint32_t base;            // LDS of its stages
   // segment
   const char *kh, *vh;      // cache bases of the head
   const int32_t* pages;     // the request's block table
   int ctx, len, last_page;  // committed tokens, tokens in all, page of the last token
-  u32x4 qf[MT][L::KSTEPS];
-  uint64_t see[MT];         // tree: nodes (bit j - 1) the lane's row sees
-  int node[MT];             // chain: the lane's node
+  u32x4 qf[L::KSTEPS];
+  uint64_t see;             // tree: nodes (bit j - 1) the lane's row sees
+  int node;                 // chain: the lane's node
   // state
-  f32x16 o[MT][ND];
-  float m[MT], l[MT];       // m: what o and l are relative to, about the largest score so
+  f32x16 o[ND];
+  float m, l;               // m: what o and l are relative to, about the largest score so
                             // far, times scale * log2(e)
 
-  __device__ __forceinline__ AttWave(const AttParams& p_, uint32_t base_)
-      : p(p_), lane(threadIdx.x & 63), n(lane & 31), h(lane >> 5), base(base_) {}
+  __device__ __forceinline__ AttWave(const AttParams& p_, int wave_, uint32_t lds)
+      : p(p_), lane(threadIdx.x & 63), n(lane & 31), h(lane >> 5), wave(wave_),
+        mine(NR == 1 ? 0 : wave_ * CROWS),
+        base(NR == 1 ? lds + wave_ * F::STAGES * F::TILE : lds) {}
 
-  // The copies of tile t0's K and V rows into stage s.  A copy's rows (at most 8, aligned)
-  // share a page.  Rows past the last token read inside its page; nothing reads past it.
-  __device__ __forceinline__ void page_ids(int t0, int (&pg)[4]) const {
+  // Pages of the wave's rows of tile t0, a page per 8 of them (aligned, so they share one);
+  // past the last token, its page.
+  __device__ __forceinline__ void page_ids(int t0, int (&pg)[CG]) const {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      int i = (t0 + 8 * g) >> p.lg;
+    for (int g = 0; g < CG; ++g) {
+      int i = (t0 + mine + 8 * g) >> p.lg;
       i = i < last_page ? i : last_page;
       pg[g] = sload(pages, i);
     }
   }
-  __device__ __forceinline__ void known(int (&pg)[4]) const {
+  __device__ __forceinline__ void known(int (&pg)[CG]) const {
     bool bad = false;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < CG; ++g) {
       const bool out = pg[g] < 0 || pg[g] >= p.n_pages;
       bad = bad || out;
       pg[g] = out ? 0 : pg[g];
     }
     if (bad && lane == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
   }
+  // The copies of the wave's rows of tile t0's K or V into stage s.  Rows past the last token
+  // read inside its page, and are never used.
   template <bool V>
-  __device__ __forceinline__ void copy(int t0, const int (&pg)[4], int s) const {
+  __device__ __forceinline__ void copy(int t0, const int (&pg)[CG], int s) const {
     const int lr = lane / L::CPR, pos = lane % L::CPR;
     const uint32_t row = (uint32_t)(lr * (int)p.tok_b);
-    const uint32_t to = base + (2 * s + V) * L::BYTES;
+    const uint32_t to = base + s * F::TILE + V * L::BYTES + mine * L::RB;
     const int in_page = (1 << p.lg) - 1;
+    const int xl = V ? L::vswz(lr) ^ L::vswz(mine) : L::kswz(lr) ^ L::kswz(mine);
 #pragma unroll
-    for (int c = 0; c < L::NC; ++c) {
+    for (int c = 0; c < NC; ++c) {
       const int64_t off = pg[(c * L::RPC) >> 3] * p.page_b +
-                          (int64_t)((t0 + c * L::RPC) & in_page) * p.tok_b;
-      const int x = V ? L::vswz(lr) ^ L::vswz(c * L::RPC) : L::kswz(lr) ^ L::kswz(c * L::RPC);
+                          (int64_t)((t0 + mine + c * L::RPC) & in_page) * p.tok_b;
+      const int x = xl ^ (V ? L::vswz(c * L::RPC) : L::kswz(c * L::RPC));
       dma16s((V ? vh : kh) + off, row + (uint32_t)((pos ^ x) << 4), to + c * 1024);
     }
   }
 
-  // One tile in stage s: tokens t0 .. t0 + 31.  `edge`: some of them are of the block, or
-  // behind it.  One stage: pg holds the pages of the wave's next tile (`more`: there is one),
-  // which is copied in between.
-  __device__ __forceinline__ void tile(int t0, int s, bool edge, bool more, int (&pg)[4]) {
-    const uint32_t ks = base + s * 2 * L::BYTES, vs = ks + L::BYTES;
-    f32x16 sc[MT];
+  // S^T of a tile
+  __device__ __forceinline__ void scores(uint32_t ks, f32x16& sc) const {
+    const uint32_t krow = here(ks + n * L::RB), kx = here((uint32_t)(h ^ L::kswz(n)) << 4);
+    sc = f32x16{};
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) sc[mt] = f32x16{};
-    {
-      const uint32_t krow = here(ks + n * L::RB), kx = here((uint32_t)(h ^ L::kswz(n)) << 4);
+    for (int st = 0; st < L::KSTEPS; ++st)
+      mfma_qk<T>(lds_get<u32x4>(krow + (kx ^ (uint32_t)(st << 5))), qf[st], sc);
+  }
+
+  // scores of tokens that the lane's row does not see: -inf
+  __device__ __forceinline__ void mask(int t0, f32x16& sc) const {
+    const bool tree = p.anc != nullptr;
 #pragma unroll
-      for (int st = 0; st < L::KSTEPS; ++st) {
-        const u32x4 a = lds_get<u32x4>(krow + (kx ^ (uint32_t)(st << 5)));
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) mfma_qk<T>(a, qf[mt][st], sc[mt]);
-      }
+    for (int r = 0; r < 16; ++r) {
+      const int j = t0 + reg_row(r, h) - ctx;
+      const bool below = tree ? j <= 64 && ((see >> ((j - 1) & 63)) & 1) : j <= node;
+      const bool ok = (j <= 0 || below) && j < len - ctx;
+      sc[r] = ok ? sc[r] : -INFINITY;
     }
-    if (edge) mask(t0, sc);
-    if (STAGES == 1) {
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      if (more && !edge) {  // (an edge tile may still need K's buffer)
-        known(pg);
-        copy<false>(t0 + kRound, pg, 0);
-      }
-    }
+  }
+
+  // the scores' weights, m, l and O's scale
+  __device__ __forceinline__ void weigh(f32x16& sc) {
     const float c2 = p.scale * kLog2e;
+    float mx = sc[0];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float mx = sc[mt][0];
+    for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[r]);
+    mx = half_max(mx) * c2;
+    // O and l are relative to m, which follows the maximum only once that is 2^kSlack past it:
+    // weights of up to 2^kSlack lose nothing in float or bf16, and the rescaling of O, half a
+    // tile's arithmetic, falls away on nearly all tiles
+    if (__ballot(mx > m + kSlack)) {
+      const float mn = fmaxf(m, mx);
+      const float f = __builtin_amdgcn_exp2f(m - (mn == -INFINITY ? 0.0f : mn));
+      l *= f;
 #pragma unroll
-      for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[mt][r]);
-      mx = half_max(mx);
-      mx *= c2;
-      // O and l are relative to m, which follows the maximum only once that is 2^kSlack past
-      // it: weights of up to 2^kSlack lose nothing in float or bf16, and the rescaling of O,
-      // half a tile's arithmetic, falls away on nearly all tiles
-      if (__ballot(mx > m[mt] + kSlack)) {
-        const float mn = fmaxf(m[mt], mx);
-        const float f = __builtin_amdgcn_exp2f(m[mt] - (mn == -INFINITY ? 0.0f : mn));
-        l[mt] *= f;
+      for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) o[mt][dt][r] *= f;
-        m[mt] = mn;
-      }
-      const float ref = m[mt] == -INFINITY ? 0.0f : m[mt];
-      float sum = 0.0f;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        sc[mt][r] = __builtin_amdgcn_exp2f(fmaf(sc[mt][r], c2, -ref));
-        sum += sc[mt][r];
-      }
-      l[mt] += sum;  // this half-wave's tokens; the halves are added at the end
+        for (int r = 0; r < 16; ++r) o[dt][r] *= f;
+      m = mn;
     }
-    if (STAGES == 1) {
-      if (more && !edge)
-        vm_wait<L::NC>();
-      else
-        vm_wait<0>();
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      sc[r] = __builtin_amdgcn_exp2f(fmaf(sc[r], c2, -ref));
+      sum += sc[r];
     }
-    if (edge && clean_values(t0, vs)) odd_values(ks, vs, sc);  // leaves V's tile at 0
+    l += sum;  // this half-wave's tokens; the halves are added at the end
+  }
+
+  // O^T += V^T P^T
+  __device__ __forceinline__ void values(uint32_t vs, const f32x16& sc) {
     if constexpr (L::kBf) {
-      // O^T += V^T P^T, 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens
-      // of it, rounded to bf16 (each weight off by 2^-8 of itself at most, as o is when stored);
-      // V's fragment is two transposing reads of 4 tokens x 16 d.  Rows 8 apart share a
-      // swizzle, so a lane has one address per 32 d and the rest are immediates.
+      // 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens of it, rounded to
+      // bf16 (each weight off by 2^-8 of itself at most, as o is when stored); V's fragment is
+      // two transposing reads of 4 tokens x 16 d.  Rows 8 apart share a swizzle, so a lane has
+      // one address per 32 d and the rest are immediates.
       const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
       const uint32_t vrow = here(vs + r0 * L::RB + (j & 1) * 8);
       const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ L::vswz(r0)) << 4);
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        bf16x8 pb[MT];
+        bf16x8 pb;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) pb[mt][e] = (__bf16)sc[mt][8 * st + e];
+        for (int e = 0; e < 8; ++e) pb[e] = (__bf16)sc[8 * st + e];
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
           union {
@@ -320,9 +330,7 @@ struct AttWave {
           for (int b = 0; b < 2; ++b)
             a.half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                 (DSPARK_LDS s16x4*)(uintptr_t)(at + 8 * (2 * st + b) * L::RB));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.all, pb[mt], o[mt][dt], 0, 0, 0);
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.all, pb, o[dt], 0, 0, 0);
         }
       }
     } else {
@@ -334,29 +342,13 @@ struct AttWave {
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
           const float a = lds_get<float>(vrow + (vx ^ (uint32_t)(dt << 7)) + reg_row(r, 0) * L::RB);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-            o[mt][dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, sc[mt][r], o[mt][dt], 0, 0, 0);
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, sc[r], o[dt], 0, 0, 0);
         }
     }
   }
 
-  // scores of tokens that the lane's row does not see: -inf
-  __device__ __forceinline__ void mask(int t0, f32x16 (&sc)[MT]) const {
-    const bool tree = p.anc != nullptr;
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int j = t0 + reg_row(r, h) - ctx;
-        const bool below = tree ? j <= 64 && ((see[mt] >> ((j - 1) & 63)) & 1) : j <= node[mt];
-        const bool ok = (j <= 0 || below) && j < len - ctx;
-        sc[mt][r] = ok ? sc[mt][r] : -INFINITY;
-      }
-  }
-
   // V rows behind the last token become 0 (they may hold anything, and 0 * NaN is none);
-  // whether the rows left hold infinities or NaN
+  // whether the rows left hold infinities or NaN.  Waves that share a tile all do it alike.
   __device__ __forceinline__ bool clean_values(int t0, uint32_t vs) const {
     bool bad = false;
 #pragma unroll 1
@@ -376,17 +368,22 @@ struct AttWave {
 
   // The product with a V tile that holds infinities or NaN: a weight of 0 leaves a token out
   // (a matrix product would make 0 * inf of it).  The weights go through the K tile's LDS,
-  // which the scores no longer need; the tile is 0 afterwards.
-  __device__ __forceinline__ void odd_values(uint32_t ks, uint32_t vs, const f32x16 (&sc)[MT]) {
+  // which the scores no longer need, a wave at a time; the V tile is 0 afterwards, so that
+  // values() adds nothing.
+  __device__ __forceinline__ void odd_values(uint32_t ks, uint32_t vs, const f32x16& sc) {
+#pragma unroll 1
+    for (int w = 0; w < NR; ++w) {
+      if (NR > 1) {
+        stage_barrier();  // every wave has its scores, and is done with the weights before
+        if (w != wave) continue;
+      }
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-      for (int r = 0; r < 16; ++r) lds_put<float>(ks + (reg_row(r, h) * 32 + n) * 4, sc[mt][r]);
+      for (int r = 0; r < 16; ++r) lds_put<float>(ks + (reg_row(r, h) * 32 + n) * 4, sc[r]);
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll 1
       for (int t = 0; t < kTok; ++t) {
-        const float w = lds_get<float>(ks + (t * 32 + n) * 4);
-        if (w == 0.0f) continue;
+        const float wt = lds_get<float>(ks + (t * 32 + n) * 4);
+        if (wt == 0.0f) continue;
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
 #pragma unroll
@@ -399,97 +396,171 @@ struct AttWave {
               x = bf16_to_f32(lds_get<uint16_t>(at));
             else
               x = lds_get<float>(at);
-            o[mt][dt][r] = fmaf(w, x, o[mt][dt][r]);
+            o[dt][r] = fmaf(wt, x, o[dt][r]);
           }
           asm volatile("" ::: "memory");
         }
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
+    if (NR > 1) stage_barrier();
 #pragma unroll 1
     for (int i = lane; i < L::NC * kWave; i += kWave) lds_put<u32x4>(vs + i * 16, u32x4{0, 0, 0, 0});
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
 
-  // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
-  __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr,
-                                          int wave) {
-    const int M = rq.n * p.G;
+  // the queries and what they see; rows m0 .. m0 + 31 of the request's M
+  __device__ __forceinline__ void begin(const AttReq& rq, int q, int head, int m0, int M) {
     ctx = rq.ctx;
     pages = p.table + (int64_t)q * p.max_pages;
     kh = static_cast<const char*>(p.k) + head * p.head_b;
     vh = static_cast<const char*>(p.v) + head * p.head_b;
     len = rq.ctx + rq.n;
     last_page = (len - 1) >> p.lg;
-    // a chain's row tile sees no node after its last row's
-    int most = len;
-    if (!p.anc) {
-      const int last = m0 + 32 * MT - 1 < M - 1 ? m0 + 32 * MT - 1 : M - 1;
-      most = rq.ctx + last / p.G + 1;
+    m = -INFINITY;
+    l = 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) o[dt] = f32x16{};
+  }
+  __device__ __forceinline__ void queries(const AttReq& rq, int head, int m0, int M) {
+    const int mi = m0 + n;
+    const bool live = mi < M;
+    const int i = live ? mi / p.G : 0, g = live ? mi % p.G : 0;
+    const char* src = static_cast<const char*>(p.q) +
+                      ((int64_t)(rq.a + i) * p.q_row + (int64_t)(head * p.G + g) * D) * L::kE;
+#pragma unroll
+    for (int st = 0; st < L::KSTEPS; ++st) {
+      qf[st] = u32x4{0, 0, 0, 0};
+      if (live) qf[st] = *reinterpret_cast<const u32x4*>(src + (2 * st + h) * 16);
     }
-    const int first = r0 * kRound + wave * kTok;
-    int end = (r0 + nr) * kRound;
-    end = end < most ? end : most;
-    const int nt = first < end ? (end - first + kRound - 1) / kRound : 0;
-    int pg[4];
+    node = i;
+    see = p.anc ? p.anc[rq.a + i] : 0;
+  }
+
+  // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
+  __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr) {
+    const int M = rq.n * p.G;
+    begin(rq, q, head, m0, M);
+    // a chain's row tile sees no node after its last row's
+    int end = len;
+    if (!p.anc) {
+      const int last = m0 + NR * kRows - 1 < M - 1 ? m0 + NR * kRows - 1 : M - 1;
+      end = rq.ctx + last / p.G + 1;
+    }
+    end = end < (r0 + nr) * F::ROUND ? end : (r0 + nr) * F::ROUND;
+    const int first = r0 * F::ROUND + (NR == 1 ? wave * kTok : 0);
+    const int nt = first < end ? (end - first + F::ROUND - 1) / F::ROUND : 0;
+    if constexpr (NR == 1)
+      tokens_apart(rq, head, m0, M, first, nt);
+    else
+      rows_apart(rq, head, m0 + wave * kRows, M, first, nt);
+    l = half_sum(l);
+  }
+
+  // NR 1: this wave's tiles, kRound tokens apart, in its own LDS
+  __device__ __forceinline__ void tokens_apart(const AttReq& rq, int head, int m0, int M, int first,
+                                               int nt) {
+    int pg[CG];
     if (nt > 0) {
       page_ids(first, pg);
       known(pg);
       copy<false>(first, pg, 0);
       copy<true>(first, pg, 0);
-      page_ids(first + kRound, pg);  // past the end: the last page's
+      page_ids(first + F::ROUND, pg);  // past the end: the last page's
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int mi = m0 + 32 * mt + n;
-      const bool live = mi < M;
-      const int i = live ? mi / p.G : 0, g = live ? mi % p.G : 0;
-      const char* src = static_cast<const char*>(p.q) +
-                        ((int64_t)(rq.a + i) * p.q_row + (int64_t)(head * p.G + g) * D) * L::kE;
-#pragma unroll
-      for (int st = 0; st < L::KSTEPS; ++st) {
-        qf[mt][st] = u32x4{0, 0, 0, 0};
-        if (live) qf[mt][st] = *reinterpret_cast<const u32x4*>(src + (2 * st + h) * 16);
-      }
-      node[mt] = i;
-      see[mt] = p.anc ? p.anc[rq.a + i] : 0;
-      m[mt] = -INFINITY;
-      l[mt] = 0.0f;
-#pragma unroll
-      for (int dt = 0; dt < ND; ++dt) o[mt][dt] = f32x16{};
-    }
+    queries(rq, head, m0, M);
     for (int k = 0; k < nt; ++k) {
-      const int t0 = first + k * kRound;
+      const int t0 = first + k * F::ROUND, t1 = t0 + F::ROUND;
       const bool more = k + 1 < nt, edge = t0 + kTok > ctx;
-      if (STAGES == 2) {
-        if (more) {
-          known(pg);
-          copy<false>(t0 + kRound, pg, ~k & 1);
-          copy<true>(t0 + kRound, pg, ~k & 1);
-          page_ids(t0 + 2 * kRound, pg);
-          vm_wait<2 * L::NC>();
-        } else {
-          vm_wait<0>();
-        }
-        tile(t0, k & 1, edge, more, pg);
-        // the stage is free once its reads have returned
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int s = F::STAGES == 2 ? k & 1 : 0;
+      const uint32_t ks = base + s * F::TILE, vs = ks + L::BYTES;
+      if (F::STAGES == 1) {
+        vm_wait<NC>();  // K's tile; V's is waited for before O
+      } else if (more) {
+        known(pg);
+        copy<false>(t1, pg, s ^ 1);
+        copy<true>(t1, pg, s ^ 1);
+        page_ids(t1 + F::ROUND, pg);
+        vm_wait<2 * NC>();
       } else {
-        vm_wait<L::NC>();  // K's tile; V's is waited for before O
-        tile(t0, 0, edge, more, pg);
+        vm_wait<0>();
+      }
+      f32x16 sc;
+      scores(ks, sc);
+      if (edge) mask(t0, sc);
+      if (F::STAGES == 1) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        if (more) {
-          if (edge) {
-            known(pg);
-            copy<false>(t0 + kRound, pg, 0);
-          }
-          copy<true>(t0 + kRound, pg, 0);
-          page_ids(t0 + 2 * kRound, pg);
+        if (more && !edge) {  // (an edge tile may still need K's buffer)
+          known(pg);
+          copy<false>(t1, pg, 0);
         }
       }
+      weigh(sc);
+      if (F::STAGES == 1) {
+        if (more && !edge)
+          vm_wait<NC>();
+        else
+          vm_wait<0>();
+      }
+      if (edge && clean_values(t0, vs)) odd_values(ks, vs, sc);
+      values(vs, sc);
+      // the stage is free once its reads have returned
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      if (F::STAGES == 1 && more) {
+        if (edge) {
+          known(pg);
+          copy<false>(t1, pg, 0);
+        }
+        copy<true>(t1, pg, 0);
+        page_ids(t1 + F::ROUND, pg);
+      }
     }
+  }
+
+  // NR > 1: tiles that all waves share
+  __device__ __forceinline__ void rows_apart(const AttReq& rq, int head, int m0, int M, int first,
+                                             int nt) {
+    constexpr int AHEAD = F::STAGES - 1;
+    int pg[CG];
+    page_ids(first, pg);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) l[mt] = half_sum(l[mt]);
+    for (int a = 0; a < AHEAD; ++a) {
+      if (a < nt) {
+        known(pg);
+        copy<false>(first + a * kTok, pg, a);
+        copy<true>(first + a * kTok, pg, a);
+      }
+      page_ids(first + (a + 1) * kTok, pg);
+    }
+    queries(rq, head, m0, M);
+    const bool live = m0 < M;
+    int s = 0, s_next = AHEAD;
+    for (int k = 0; k < nt; ++k) {
+      const int t0 = first + k * kTok;
+      if (k + AHEAD - 1 < nt)  // this wave's copies of the tile; later ones stay under way
+        vm_wait<(AHEAD - 1) * 2 * NC>();
+      else
+        vm_wait<0>();
+      stage_barrier();  // the whole tile is there, and every wave is done with the one before
+      if (k + AHEAD < nt) {
+        known(pg);
+        copy<false>(t0 + AHEAD * kTok, pg, s_next);
+        copy<true>(t0 + AHEAD * kTok, pg, s_next);
+        page_ids(t0 + (AHEAD + 1) * kTok, pg);
+      }
+      const uint32_t ks = base + s * F::TILE, vs = ks + L::BYTES;
+      f32x16 sc = f32x16{};
+      if (live) {
+        scores(ks, sc);
+        if (t0 + kTok > ctx) mask(t0, sc);
+        weigh(sc);
+      }
+      if (t0 + kTok > ctx && clean_values(t0, vs)) odd_values(ks, vs, sc);
+      if (live) values(vs, sc);
+      s = s + 1 == F::STAGES ? 0 : s + 1;
+      s_next = s_next + 1 == F::STAGES ? 0 : s_next + 1;
+    }
+    stage_barrier();  // the next segment's copies overwrite the stages
   }
 };
 
@@ -525,13 +596,13 @@ __device__ __forceinline__ int64_t snapped(int64_t at, int64_t len) {
   return at <= kSetup ? 0 : at;
 }
 
-template <class T, int D, int MT>
-__global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
+template <class T, int D, int NR>
+__global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_SIMD))
     attention_kernel(AttParams p) {
-  using L = Tile<T, D>;
-  constexpr int MR = 32 * MT, ND = D / 32;
+  using F = Fit<T, D, NR>;
+  constexpr int MR = kRows * NR, ND = D / 32, kRound = F::ROUND, kAttThreads = F::THREADS;
   extern __shared__ uint4 lds[];
-  __shared__ int64_t sums[kAttWaves];
+  __shared__ int64_t sums[F::WAVES];
   __shared__ int64_t total_s, start_off;
   __shared__ int start_s[4];
   const int tid = threadIdx.x, wave = uni(tid >> 6);
@@ -589,7 +660,7 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
   int64_t off = uni(start_off);  // units of q's lists before this workgroup's
 
   const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
-  AttWave<T, D, MT> wv(p, base + wave * Fit<T, D, MT>::STAGES * 2 * L::BYTES);
+  AttWave<T, D, NR> wv(p, wave, base);
   int64_t u = u0;  // the unit that `off` stands for
   bool first = true;
   while (true) {
@@ -616,43 +687,77 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
     from = from > kSetup ? from - kSetup : 0;
     const int r0 = (int)from, nr = (int)(to - kSetup - from), rounds = (int)len - kSetup;
     if (nr <= 0) continue;
-    wv.segment(rq, q, head, mt0 * MR, r0, nr, wave);
+    wv.segment(rq, q, head, mt0 * MR, r0, nr);
 
-    // The waves' sums, through LDS: each gives the other half of its O, and finishes its own
-    // half.
-    constexpr int HD = ND / 2, kGive = (MT * HD * 16 + 2 * MT) * 64;
-    float* x = reinterpret_cast<float*>(lds);
-    const int lane = tid & 63;
-    auto give = [&](auto self) {
-      constexpr int W = decltype(self)::value;
-      float* y = x + W * kGive + lane;
+    const bool whole = r0 == 0 && nr == rounds;
+    const int M = rq.n * p.G, lane = tid & 63;
+    float* part = p.part + ((int64_t)b * 2 + (r0 == 0)) * MR * (D + 2);
+    // a row's O (d .. d + 3), and its m and l, to the output or the workspace
+    auto put = [&](int row, int d, f32x4 z) {
+      if (!whole) {
+        *reinterpret_cast<f32x4*>(part + row * D + d) = z;
+        return;
+      }
+      const int mi = mt0 * MR + row;
+      T* out = static_cast<T*>(p.o) +
+               ((int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G) * D + d;
+      if constexpr (F::kBf) {
+        bf16x4 zb;
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
+        for (int e = 0; e < 4; ++e) zb[e] = (__bf16)z[e];
+        *reinterpret_cast<bf16x4*>(out) = zb;
+      } else {
+        *reinterpret_cast<f32x4*>(out) = z;
+      }
+    };
+    auto put_sums = [&](int row, float m, float l) {
+      const int mi = mt0 * MR + row;
+      if (!whole) {
+        part[MR * D + row] = m;
+        part[MR * (D + 1) + row] = l;
+      } else if (p.lse) {
+        p.lse[(int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G] =
+            (m + __builtin_amdgcn_logf(l)) * kLn2;
+      }
+    };
+    if constexpr (NR > 1) {
+      const int row = kRows * wave + wv.n;
+      if (mt0 * MR + row < M) {
+        const float f = !whole ? 1.0f : (wv.l == 0.0f ? 0.0f : 1.0f / wv.l);
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+          for (int r4 = 0; r4 < 4; ++r4) {
+            f32x4 z;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[e] = wv.o[dt][4 * r4 + e] * f;
+            put(row, 32 * dt + 8 * r4 + 4 * wv.h, z);
+          }
+        if (wv.h == 0) put_sums(row, wv.m, wv.l);
+      }
+    } else {
+      // The waves' sums, through LDS: each gives the other half of its O, and finishes its own
+      // half.
+      constexpr int HD = ND / 2, kGive = (HD * 16 + 2) * 64;
+      float* x = reinterpret_cast<float*>(lds);
+      auto give = [&](auto self) {
+        constexpr int W = decltype(self)::value;
+        float* y = x + W * kGive + lane;
 #pragma unroll
         for (int i = 0; i < HD; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            y[((mt * HD + i) * 16 + r) * 64] = wv.o[mt][(1 - W) * HD + i][r];
-        y[(MT * HD * 16 + 2 * mt) * 64] = wv.m[mt];
-        y[(MT * HD * 16 + 2 * mt + 1) * 64] = wv.l[mt];
-      }
-    };
-    auto finish = [&](auto self) {
-      constexpr int W = decltype(self)::value;
-      const float* y = x + (1 - W) * kGive + lane;
-      const bool whole = r0 == 0 && nr == rounds;
-      const int M = rq.n * p.G;
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const float m2 = y[(MT * HD * 16 + 2 * mt) * 64], l2 = y[(MT * HD * 16 + 2 * mt + 1) * 64];
-        const float mm = fmaxf(wv.m[mt], m2);
-        const float ref = mm == -INFINITY ? 0.0f : mm;
-        float f1 = __builtin_amdgcn_exp2f(wv.m[mt] - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
-        const float ll = wv.l[mt] * f1 + l2 * f2;
-        const int row = 32 * mt + wv.n, mi = mt0 * MR + row;
-        if (mi >= M) continue;
-        const int64_t at = (int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G;
-        float* part = p.part + ((int64_t)b * 2 + (r0 == 0)) * MR * (D + 2);
+          for (int r = 0; r < 16; ++r) y[(i * 16 + r) * 64] = wv.o[(1 - W) * HD + i][r];
+        y[HD * 16 * 64] = wv.m;
+        y[(HD * 16 + 1) * 64] = wv.l;
+      };
+      auto finish = [&](auto self) {
+        constexpr int W = decltype(self)::value;
+        const float* y = x + (1 - W) * kGive + lane;
+        const float m2 = y[HD * 16 * 64], l2 = y[(HD * 16 + 1) * 64];
+        const float mm = fmaxf(wv.m, m2), ref = mm == -INFINITY ? 0.0f : mm;
+        float f1 = __builtin_amdgcn_exp2f(wv.m - ref), f2 = __builtin_amdgcn_exp2f(m2 - ref);
+        const float ll = wv.l * f1 + l2 * f2;
+        if (mt0 * MR + wv.n >= M) return;
         if (whole) {
           const float inv = ll == 0.0f ? 0.0f : 1.0f / ll;
           f1 *= inv;
@@ -666,38 +771,21 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int r = 4 * r4 + e;
-              z[e] = wv.o[mt][W * HD + i][r] * f1 + y[((mt * HD + i) * 16 + r) * 64] * f2;
+              z[e] = wv.o[W * HD + i][r] * f1 + y[(i * 16 + r) * 64] * f2;
             }
-            const int d = 32 * (W * HD + i) + 8 * r4 + 4 * wv.h;
-            if (!whole) {
-              *reinterpret_cast<f32x4*>(part + row * D + d) = z;
-            } else if constexpr (L::kBf) {
-              bf16x4 zb;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) zb[e] = (__bf16)z[e];
-              *reinterpret_cast<bf16x4*>(static_cast<T*>(p.o) + at * D + d) = zb;
-            } else {
-              *reinterpret_cast<f32x4*>(static_cast<T*>(p.o) + at * D + d) = z;
-            }
+            put(wv.n, 32 * (W * HD + i) + 8 * r4 + 4 * wv.h, z);
           }
-        if (W == 0 && wv.h == 0) {
-          if (!whole) {
-            part[MR * D + row] = mm;
-            part[MR * (D + 1) + row] = ll;
-          } else if (p.lse) {
-            p.lse[at] = (mm + __builtin_amdgcn_logf(ll)) * kLn2;
-          }
-        }
-      }
-    };
-    using First = std::integral_constant<int, 0>;
-    using Second = std::integral_constant<int, 1>;
-    __syncthreads();
-    if (wave == 0) give(First{});
-    else give(Second{});
-    __syncthreads();
-    if (wave == 0) finish(First{});
-    else finish(Second{});
+        if (W == 0 && wv.h == 0) put_sums(wv.n, mm, ll);
+      };
+      using First = std::integral_constant<int, 0>;
+      using Second = std::integral_constant<int, 1>;
+      __syncthreads();
+      if (wave == 0) give(First{});
+      else give(Second{});
+      __syncthreads();
+      if (wave == 0) finish(First{});
+      else finish(Second{});
+    }
     // this workgroup begins inside a list: the first to do so if the one before it did not
     if (tid == 0 && r0 > 0 && cut.begin(b - 1) <= s + kSetup)
       p.joint[b] = {rq.a, rq.n * p.G, head, mt0, (int)(cut.owner(s + len - 1) - b) + 2,
@@ -711,9 +799,9 @@ __global__ void __launch_bounds__(kAttThreads, (Fit<T, D, MT>::PER_CU / 2))
 // D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two, four or
 // twelve such loads in flight; sums and maxima run over each lane's pieces and meet at the
 // end, always in the same order.
-template <class T, int D, int MT>
+template <class T, int D, int NR>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
-  constexpr int MR = 32 * MT, LP = D / 4, NP = kWave / LP;
+  constexpr int MR = kRows * NR, LP = D / 4, NP = kWave / LP;
   const int b = blockIdx.x;
   const AttJoint jt = p.joint[b];
   if (jt.count == 0) return;
@@ -794,29 +882,28 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
 // ---------------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------------
-// Row tiles of 32 query rows where a request's rows need no more (rows / R of them times
-// heads to a cache head, the bound the host knows), else of 64: a cache tile is then read for
-// twice the rows.
-static int att_mt(int R, int rows, int G, dspark_dtype dt) {
-  if (dt == DSPARK_F32) return 1;
-  return (int64_t)((rows + R - 1) / R) * G <= 32 ? 1 : 2;
-}
-
-template <class T_, int D_, int MT_>
+template <class T_, int D_, int NR_>
 struct Variant {
   using T = T_;
-  static constexpr int D = D_, MT = MT_;
+  static constexpr int D = D_, NR = NR_;
   // workgroups: as many as stay resident
-  static int grid() { return device_cus() * Fit<T, D, MT>::PER_CU; }
+  static int grid() { return device_cus() * Fit<T, D, NR>::PER_CU; }
 };
 
-// f(variant) of the variant that runs these shapes
+// f(variant) of the variant that runs these shapes: as many waves over query rows as a
+// request's rows (rows / R, the bound the host knows, times heads to a cache head) fill, so
+// that the cache is read once for all of them.  Float has only the first: its products are
+// sixteen times as slow, and bound it before the cache does.
 template <class F>
 static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
-  const int mt = att_mt(R, rows, G, dt);
   if (dt == DSPARK_F32) return D == 64 ? f(Variant<float, 64, 1>{}) : f(Variant<float, 128, 1>{});
-  if (D == 64) return mt == 1 ? f(Variant<uint16_t, 64, 1>{}) : f(Variant<uint16_t, 64, 2>{});
-  return mt == 1 ? f(Variant<uint16_t, 128, 1>{}) : f(Variant<uint16_t, 128, 2>{});
+  const int64_t m = (int64_t)((rows + R - 1) / R) * G;
+  if (D == 64) {
+    if (m <= 32) return f(Variant<uint16_t, 64, 1>{});
+    return m <= 64 ? f(Variant<uint16_t, 64, 2>{}) : f(Variant<uint16_t, 64, 4>{});
+  }
+  if (m <= 32) return f(Variant<uint16_t, 128, 1>{});
+  return m <= 64 ? f(Variant<uint16_t, 128, 2>{}) : f(Variant<uint16_t, 128, 4>{});
 }
 
 static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
@@ -824,7 +911,7 @@ static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, d
   att_variant(R, rows, G, D, dt, [&](auto v) {
     const size_t grid = (size_t)v.grid();
     p.joint = cv.take<AttJoint>(grid);
-    p.part = cv.take<float>(grid * 2 * 32 * v.MT * (v.D + 2));
+    p.part = cv.take<float>(grid * 2 * kRows * v.NR * (v.D + 2));
     return 0;
   });
   return cv.bytes();
@@ -835,19 +922,20 @@ static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt
          (dt == DSPARK_F32 || dt == DSPARK_BF16) && (int64_t)rows * Hq < ((int64_t)1 << 31);
 }
 
-template <class T, int D, int MT>
+template <class T, int D, int NR>
 static int att_launch(const AttParams& p, hipStream_t stream) {
+  using F = Fit<T, D, NR>;
   static std::atomic<uint64_t> raised;
-  auto kern = attention_kernel<T, D, MT>;
-  const int sh = Fit<T, D, MT>::LDS, grid = Variant<T, D, MT>::grid();
-  ensure_dynamic_lds(reinterpret_cast<const void*>(kern), sh, raised);
-  kern<<<grid, kAttThreads, sh, stream>>>(p);
+  auto kern = attention_kernel<T, D, NR>;
+  const int grid = Variant<T, D, NR>::grid();
+  ensure_dynamic_lds(reinterpret_cast<const void*>(kern), F::LDS, raised);
+  kern<<<grid, F::THREADS, F::LDS, stream>>>(p);
   // where no request can have more than kWhole rounds, no list is cut
-  if (((int64_t)p.max_pages << p.lg) <= kWhole * kRound) return launch_status();
+  if (((int64_t)p.max_pages << p.lg) <= kWhole * F::ROUND) return launch_status();
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
-  const int slices = m < 32 * MT ? (int)(m + 3) / 4 : 8 * MT;
-  attention_join_kernel<T, D, MT><<<dim3(grid, slices), 256, 0, stream>>>(p);
+  const int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
+  attention_join_kernel<T, D, NR><<<dim3(grid, slices), 256, 0, stream>>>(p);
   return launch_status();
 }
 
@@ -910,6 +998,6 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
   p.status = dev_status;
   if (ws_bytes < att_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
   return att_variant(R, rows, p.G, D, dt, [&](auto v) {
-    return att_launch<typename decltype(v)::T, decltype(v)::D, decltype(v)::MT>(p, stream);
+    return att_launch<typename decltype(v)::T, decltype(v)::D, decltype(v)::NR>(p, stream);
   });
 }
