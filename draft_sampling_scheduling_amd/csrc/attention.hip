@@ -27,10 +27,6 @@
 
 namespace dspark {
 
-#ifndef ATT_S
-#define ATT_S(NR, D) (NR == 2 ? 2 : 4)
-#define ATT_P(NR, D) (NR == 2 ? 4 : 2)
-#endif
 constexpr int kTok = 32;  // tokens of a tile
 constexpr int kRows = 32;  // query rows of a wave
 constexpr float kSlack = 8.0f;
@@ -130,8 +126,9 @@ struct Tile {
 //   tiles deep.  STAGES 1: one buffer each; K's next tile is under way as soon as the scores
 //   are taken, V's as soon as O is: half the LDS, twice the workgroups.
 //   NR 2 or 4, up to 64 or 128 rows: every wave has 32 rows of its own, and all share each
-//   tile of 32 tokens, copied STAGES - 1 ahead by all of them, with a barrier per tile; the
-//   cache is read once for all rows.
+//   tile of 32 tokens, copied one ahead by all of them, with a barrier per tile; the cache is
+//   read once for all rows.  More stages made four waves slower (196 against 187 us for 128
+//   rows), and two with fewer workgroups in their place (50 to 53 against 48 us for 64 trees).
 //   PER_CU workgroups are resident; where registers allow two waves a SIMD, one's set-up,
 //   exponentials and merge hide behind the other's tiles.
 template <class T, int D, int NR>
@@ -141,9 +138,9 @@ struct Fit {
   static constexpr int THREADS = WAVES * kWave;
   static constexpr int ROUND = NR == 1 ? 2 * kTok : kTok;  // tokens of a round
   static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
-  static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : ATT_S(NR, D);
+  static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : 2;
   static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
-  static constexpr int PER_CU = NR == 1 ? (LDS <= 32 * 1024 ? 4 : 2) : ATT_P(NR, D);
+  static constexpr int PER_CU = NR == 1 ? (LDS <= 32 * 1024 ? 4 : 2) : 8 / NR;
   static constexpr int PER_SIMD = PER_CU * WAVES / 4;
 };
 
@@ -569,9 +566,10 @@ struct AttWave {
 // tile's wait, the merge of the waves; about 8 us where a round takes 3 us with all CUs
 // streaming), which no tokens stand for; all lists, head after head, are one row of
 // units, cut evenly: workgroup b begins at unit begin(b).  A cut costs the later piece's
-// set-up and the join, so lists of up to kWhole rounds stay whole (39 against 43 us for 2112
-// lists of 3 to 4 rounds); moving cuts of longer lists to a near end lost more in balance
-// than it saved in joins (105 against 117 us for 184 lists of 30).  A list that is cut has
+// set-up and the join, so short lists stay whole (39 against 43 us for 2112 lists of 3 to
+// 4 rounds of 64 tokens), but not where a share is hardly more than one (at shares of 9 units,
+// lists of 8 rounds kept whole cost 52 against 48 us); moving cuts of longer lists to a near
+// end lost more in balance than it saved in joins (105 against 117 us for 184 lists of 30).  A list that is cut has
 // its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
 constexpr int kSetup = 3, kWhole = 4;
 
@@ -582,6 +580,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 struct AttShares {
   int64_t share, more;  // units of a workgroup; the first `more` have one more
+  int whole;            // rounds up to which a list stays whole
   __device__ __forceinline__ int64_t begin(int64_t b) const {
     return b * share + (b < more ? b : more);
   }
@@ -589,12 +588,12 @@ struct AttShares {
     const int64_t big = more * (share + 1);
     return u < big ? quotient(u, share + 1) : more + quotient(u - big, share);
   }
+  // where a cut at unit `at` of a list of len units falls
+  __device__ __forceinline__ int64_t snapped(int64_t at, int64_t len) const {
+    if (len <= kSetup + whole) return 2 * at <= len ? 0 : len;
+    return at <= kSetup ? 0 : at;
+  }
 };
-// where a cut at unit `at` of a list of len units falls
-__device__ __forceinline__ int64_t snapped(int64_t at, int64_t len) {
-  if (len <= kSetup + kWhole) return 2 * at <= len ? 0 : len;
-  return at <= kSetup ? 0 : at;
-}
 
 template <class T, int D, int NR>
 __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_SIMD))
@@ -633,6 +632,9 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
   AttShares cut;
   cut.share = quotient(U, P);
   cut.more = U - cut.share * P;
+  // kWhole rounds, and up to 256 tokens where a share is several such lists
+  constexpr int kMost = 256 / kRound > kWhole ? 256 / kRound : kWhole;
+  cut.whole = cut.share >= 2 * kMost ? kMost : (cut.share >= 2 * kWhole ? (int)cut.share / 2 : kWhole);
   const int64_t u0 = cut.begin(b), u1 = cut.begin(b + 1);
   int head = (int)quotient(u0, W);
   {
@@ -678,8 +680,8 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
     const int64_t len = list(rq);
     const int mt0 = (int)quotient(off, len);
     const int64_t at = off - mt0 * len, s = u - at;  // the list's units are s .. s + len
-    int64_t from = first ? snapped(at, len) : at;
-    const int64_t to = u1 - s >= len ? len : (u1 - s <= 0 ? 0 : snapped(u1 - s, len));
+    int64_t from = first ? cut.snapped(at, len) : at;
+    const int64_t to = u1 - s >= len ? len : (u1 - s <= 0 ? 0 : cut.snapped(u1 - s, len));
     first = false;
     if (to <= 0) break;
     u += len - at;
