@@ -798,10 +798,11 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
 }
 
 // Joins the pieces of the row tiles that are cut: a wave per row, 16 bytes a lane, so that
-// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time, two, four or
-// twelve such loads in flight; sums and maxima run over each lane's pieces and meet at the
-// end, always in the same order.
-template <class T, int D, int NR>
+// D / 4 lanes hold a piece's row and the wave takes 256 / D pieces at a time; sums and maxima
+// run over each lane's pieces and meet at the end, always in the same order.
+// DEEP: lists of many pieces, twelve loads in flight where few lists leave the chip to few
+// waves; otherwise four at most, in registers for twice the waves.
+template <class T, int D, int NR, bool DEEP>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
   constexpr int MR = kRows * NR, LP = D / 4, NP = kWave / LP;
   const int b = blockIdx.x;
@@ -848,12 +849,14 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
       m = mn;
     };
     // few loads where there are few pieces: those of missing ones take their time too
+    constexpr int kMost = DEEP ? 12 : 4;
     if (jt.count <= 2 * NP) {
       take(std::integral_constant<int, 2>{}, 0);
-    } else if (jt.count <= 4 * NP) {
+    } else if (DEEP && jt.count <= 4 * NP) {
       take(std::integral_constant<int, 4>{}, 0);
     } else {
-      for (int k0 = 0; k0 < jt.count; k0 += 12 * NP) take(std::integral_constant<int, 12>{}, k0);
+      for (int k0 = 0; k0 < jt.count; k0 += kMost * NP)
+        take(std::integral_constant<int, kMost>{}, k0);
     }
 #pragma unroll
     for (int w = LP; w < kWave; w *= 2) {  // the lanes that hold the same d
@@ -937,7 +940,11 @@ static int att_launch(const AttParams& p, hipStream_t stream) {
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
   const int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
-  attention_join_kernel<T, D, NR><<<dim3(grid, slices), 256, 0, stream>>>(p);
+  const dim3 blocks(grid, slices);
+  if (grid / p.R / p.Hkv >= 16)  // pieces of a list, were there one row tile a request
+    attention_join_kernel<T, D, NR, true><<<blocks, 256, 0, stream>>>(p);
+  else
+    attention_join_kernel<T, D, NR, false><<<blocks, 256, 0, stream>>>(p);
   return launch_status();
 }
 
