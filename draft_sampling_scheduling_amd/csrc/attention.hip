@@ -897,8 +897,12 @@ struct Variant {
 
 // f(variant) of the variant that runs these shapes: as many waves over query rows as a
 // request's rows (rows / R, the bound the host knows, times heads to a cache head) fill, so
-// that the cache is read once for all of them.  Float has only the first: its products are
-// sixteen times as slow, and bound it before the cache does.
+// that the cache is read once for all of them.  33 to 64 rows at D = 128 run four waves too,
+// two of them only copying: half the workgroups cut half the lists (430 against 442 us for 256
+// requests of 512 to 4096 tokens, 29 against 36 us for one of 16000, 153 against 161 us for
+// 64 of 500 to 4000; 49 against 47 us for 64 of 100 to 2048); at D = 64, with half the bytes
+// under way, that costs more than it saves (90 against 77 us).  Float has only the first
+// variant: its products are sixteen times as slow, and bound it before the cache does.
 template <class F>
 static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
   if (dt == DSPARK_F32) return D == 64 ? f(Variant<float, 64, 1>{}) : f(Variant<float, 128, 1>{});
@@ -907,8 +911,7 @@ static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
     if (m <= 32) return f(Variant<uint16_t, 64, 1>{});
     return m <= 64 ? f(Variant<uint16_t, 64, 2>{}) : f(Variant<uint16_t, 64, 4>{});
   }
-  if (m <= 32) return f(Variant<uint16_t, 128, 1>{});
-  return m <= 64 ? f(Variant<uint16_t, 128, 2>{}) : f(Variant<uint16_t, 128, 4>{});
+  return m <= 32 ? f(Variant<uint16_t, 128, 1>{}) : f(Variant<uint16_t, 128, 4>{});
 }
 
 static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
