@@ -114,6 +114,9 @@ def test_long(dtype):
     """One request over many workgroups, and requests of very different lengths."""
     check(1, [20000], [3], 2, 1, 128, 16, dtype)
     check(2, [9001, 3, 0, 4100, 64], [2, 1, 5, 1, 1], 4, 2, 64, 32, dtype)
+    check(6, [7000, 40], [3, 1], 24, 1, 128, 16, dtype)   # 72 query rows to a head
+    check(7, [7000, 40], [3, 5], 11, 1, 64, 16, dtype)    # 55
+    check(8, [2500, 900, 3], [6, 4, 7], 40, 2, 64, 8, dtype, tree=True)  # 140: two row tiles
 
 
 def test_many_requests():
@@ -131,16 +134,18 @@ def test_large_scores(dtype):
 @pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
 @pytest.mark.parametrize("D", [64, 128])
-def test_unseen_nodes_hold_anything(bad, D, dtype):
+@pytest.mark.parametrize("Hq", [6, 14, 24])
+def test_unseen_nodes_hold_anything(Hq, bad, D, dtype):
     """Keys and values of nodes that a row does not see: infinite or NaN, they reach only the
-    rows that see them."""
+    rows that see them (18, 42 and 72 query rows to a cache head)."""
     import draft_sampling_scheduling_amd as ds
     n, ctx = 6, 45
     anc = [0, 0b1, 0b10, 0b101, 0b1001, 0b10010]  # node 2, and 5 under it, hold it
     sick = [2, 5]
     g = np.random.default_rng(9)
     c = ref.Cache(9, [ctx], [n], 2, D, 16, dtype)
-    q = torch.from_numpy(g.standard_normal((n, 6, D), np.float32)).to(dtype)
+    q = torch.from_numpy(g.standard_normal((n, Hq, D), np.float32)).to(dtype)
+
     def go():
         return ds.tree_attention(q.to("cuda:0"), c.dev(c.k), c.dev(c.v),
                                  torch.from_numpy(c.table).to("cuda:0"), T([ctx]), T([0, n]),
