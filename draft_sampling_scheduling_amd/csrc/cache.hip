@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(256) commit_move_kernel(CommitArgs p) {
 using namespace dspark;
 
 extern "C" size_t dspark_cache_plan_workspace_bytes(int R) {
-  return R < 1 ? 0 : carve_plan(nullptr, R).bytes;
+  return R < 1 || R > kMaxRequests ? 0 : carve_plan(nullptr, R).bytes;
 }
 
 extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, int free_len,
@@ -470,7 +470,8 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
                                  int32_t* row_off, int32_t* req, int32_t* position,
                                  int32_t* slot, uint64_t* anc, int32_t* dev_status, void* ws,
                                  size_t ws_bytes, hipStream_t stream) {
-  if (R < 0 || rows < 0 || max_pages < 1 || free_len < 0 || extra < 0 || extra > 1 ||
+  if (R < 0 || R > kMaxRequests || rows < 0 || max_pages < 1 || free_len < 0 || extra < 0 ||
+      extra > 1 ||
       !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
   if (R == 0) return DSPARK_OK;
@@ -546,7 +547,7 @@ extern "C" int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, in
 }
 
 extern "C" size_t dspark_cache_commit_workspace_bytes(int R) {
-  return R < 1 ? 0 : carve_commit(nullptr, R).bytes;
+  return R < 1 || R > kMaxRequests ? 0 : carve_commit(nullptr, R).bytes;
 }
 
 extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free_len,
@@ -558,7 +559,8 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
                                    int64_t layer_stride, int64_t page_stride,
                                    int64_t head_stride, int64_t tok_stride, int32_t* dev_status,
                                    void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (R < 0 || max_pages < 1 || free_len < 0 || !table_ok(page_size, max_pages))
+  if (R < 0 || R > kMaxRequests || max_pages < 1 || free_len < 0 ||
+      !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
   size_t e = 4;
   if (path) {

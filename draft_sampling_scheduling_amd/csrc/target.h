@@ -60,6 +60,8 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& all
   __syncthreads();
 }
 
+constexpr int kMaxRequests = 1 << 20;
+
 inline bool page_size_ok(int ps) { return ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 inline int log2_of(int p) { return __builtin_ctz((unsigned)p); }
 

@@ -28,7 +28,7 @@
  * [page][token][head][D] both serve.  Token t of request q is row t % page_size of page
  * table[q][t / page_size]; table is [R][max_pages] int32.  ctx[q] tokens of request q are
  * committed; the block's node i is token ctx[q] + i.  n_pages * page_size < 2^31 and
- * max_pages * page_size <= 2^30.
+ * max_pages * page_size <= 2^30.  R <= 2^20 (dspark_target_logits: 65535).
  */
 #ifndef DSPARK_TARGET_H
 #define DSPARK_TARGET_H

@@ -54,7 +54,7 @@ def test_plan_refusals(ds):
                                           free, P(), parent, width, P(), None, None, slot, anc,
                                           None, wsp, ws_bytes, None)
 
-    for bad in (dict(R=-1), dict(rows=-1), dict(page=12), dict(page=4), dict(page=2048),
+    for bad in (dict(R=-1), dict(R=(1 << 20) + 1), dict(rows=-1), dict(page=12), dict(page=4), dict(page=2048),
                 dict(W=0), dict(W=(1 << 26) + 1), dict(free_len=-1), dict(extra=2), dict(lens=None),
                 dict(free=None), dict(parent=P(), width=5), dict(parent=P(), anc=P(), width=0),
                 dict(slot=None), dict(wsp=None), dict(wsp=P(0x1002))):
@@ -85,7 +85,7 @@ def test_attention_refusals(ds):
                                               2048, st, tok, table, P(), P(), None, scale, o, None,
                                               None, wsp, ws_bytes, None)
 
-    for bad in (dict(Hq=9), dict(Hkv=0), dict(D=80), dict(D=256), dict(dt=2), dict(page=10),
+    for bad in (dict(R=(1 << 20) + 1), dict(Hq=9), dict(Hkv=0), dict(D=80), dict(D=256), dict(dt=2), dict(page=10),
                 dict(W=0), dict(W=(1 << 26) + 1), dict(n=0), dict(q=None), dict(q=P(0x1002)), dict(q_row=511),
                 dict(k=None), dict(st=1), dict(tok=-64), dict(table=None), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")),
@@ -125,7 +125,7 @@ def test_commit_refusals(ds):
                                             out, held, P(), free, n_free, layers, Hkv, D, dt, n, k,
                                             P(), 0, 2048, st, 64, None, P(), ws_bytes, None)
 
-    for bad in (dict(R=-1), dict(gamma=0), dict(gamma=65), dict(page=20), dict(W=0),
+    for bad in (dict(R=-1), dict(R=(1 << 20) + 1), dict(gamma=0), dict(gamma=65), dict(page=20), dict(W=0),
                 dict(n_acc=None), dict(done=P(), n_free=None), dict(done=P(), free=None),
                 dict(layers=-1), dict(Hkv=0), dict(D=12), dict(dt=5), dict(n=0), dict(k=None),
                 dict(k=P(0x1001)), dict(st=1022), dict(free_len=-1),
