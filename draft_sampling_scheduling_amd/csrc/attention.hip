@@ -140,8 +140,9 @@ struct Fit {
   static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
   static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : 2;
   static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
-  static constexpr int PER_CU = NR == 1 ? (LDS <= 32 * 1024 ? 4 : 2) : 8 / NR;
-  static constexpr int PER_SIMD = PER_CU * WAVES / 4;
+  // two waves a SIMD, but for float rows of 128, whose one wave takes its registers
+  static constexpr int PER_SIMD = !kBf && D == 128 ? 1 : 2;
+  static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
 };
 
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
@@ -902,7 +903,9 @@ struct Variant {
 // requests of 512 to 4096 tokens, 29 against 36 us for one of 16000, 153 against 161 us for
 // 64 of 500 to 4000; 49 against 47 us for 64 of 100 to 2048); at D = 64, with half the bytes
 // under way, that costs more than it saves (90 against 77 us).  Float has only the first
-// variant: its products are sixteen times as slow, and bound it before the cache does.
+// variant: its products, sixteen times as slow, bound it, and rows that are not there cost it
+// as much as others (22 requests of up to 56 rows: 180 us so, 212 us with two waves over
+// rows; 16 of 128 rows: 144 against 123 us).
 template <class F>
 static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
   if (dt == DSPARK_F32) return D == 64 ? f(Variant<float, 64, 1>{}) : f(Variant<float, 128, 1>{});
