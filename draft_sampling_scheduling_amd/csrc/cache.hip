@@ -18,6 +18,7 @@ struct PlanWs {
   int32_t* take;   // [R] pages handed out to q
   int32_t* first;  // [R] index of q's first page among those handed out
   int32_t* nfree;  // [1] free pages before the call
+  int32_t* off;    // [R + 1] the row offsets again, or null
   size_t bytes;
 };
 
@@ -50,8 +51,9 @@ struct PlanArgs {
 // which everybody is served.  Otherwise a request's rows fit in a prefix of the requests that
 // ask for any, and of those its pages are had in a prefix of the ones that need any, so the
 // exclusive sum of the needs is also the count of pages handed out before it.
+// `to`: where the rows' kernel, or part, finds what it needs.
 template <int NT>
-__device__ __forceinline__ void plan_scan(const PlanArgs& p, int64_t* sums) {
+__device__ __forceinline__ void plan_scan(const PlanArgs& p, const PlanWs& to, int64_t* sums) {
   const int R = p.R, tid = threadIdx.x;
   const int per = (R + NT - 1) / NT;
   const int lo = min(R, tid * per), hi = min(R, lo + per);
@@ -125,16 +127,20 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& p, int64_t* sums) {
     pages += need;
     const bool lack = need > 0 && pages > nf;
     p.row_off[q] = (int32_t)at;
+    if (to.off) to.off[q] = (int32_t)at;
     at += run <= p.rows && !lack ? n : 0;
-    if (q == R - 1) p.row_off[R] = (int32_t)at;
+    if (q == R - 1) {
+      p.row_off[R] = (int32_t)at;
+      if (to.off) to.off[R] = (int32_t)at;
+    }
     const int h = p.held[q];
-    p.ws.held[q] = h;
-    p.ws.take[q] = lack ? 0 : need;
-    p.ws.first[q] = (int32_t)(before < nf ? before : 0);
+    to.held[q] = h;
+    to.take[q] = lack ? 0 : need;
+    to.first[q] = (int32_t)(before < nf ? before : 0);
     if (!lack && need > 0) p.held[q] = h + need;
   }
   if (tid == NT - 1) {
-    p.ws.nfree[0] = nf;
+    to.nfree[0] = nf;
     *p.n_free = nf - (int32_t)given;
   }
 }
@@ -176,7 +182,7 @@ __device__ __forceinline__ int plan_parent(const PlanArgs& p, int q, int i) {
 
 __global__ void __launch_bounds__(kPlanThreads) plan_scan_kernel(PlanArgs p) {
   __shared__ int64_t sums[2 * kPlanThreads / kWave];
-  plan_scan<kPlanThreads>(p, sums);
+  plan_scan<kPlanThreads>(p, p.ws, sums);
 }
 
 // One workgroup per request and slice of its rows: its new pages into the table, and its rows.
@@ -203,18 +209,15 @@ constexpr int kSmallThreads = 256, kSmallR = 256, kSmallRows = 1024, kSmallNodes
 
 __global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(PlanArgs p) {
   __shared__ int64_t sums[2 * kSmallThreads / kWave];
-  __shared__ int off[kSmallR + 1];
+  __shared__ int held[kSmallR], take[kSmallR], first[kSmallR], off[kSmallR + 1], nfree[1];
   __shared__ int up[kSmallNodes];
   const int tid = threadIdx.x, R = p.R;
-  plan_scan<kSmallThreads>(p, sums);
-  __syncthreads();  // what the scan wrote is read by other threads below
-  for (int q = tid; q <= R; q += kSmallThreads) off[q] = p.row_off[q];
+  plan_scan<kSmallThreads>(p, PlanWs{held, take, first, nfree, off, 0}, sums);
   __syncthreads();
-  const int nf = p.ws.nfree[0];
+  const int nf = nfree[0];
   for (int q = tid; q < R; q += kSmallThreads) {
-    const int take = p.ws.take[q], had = p.ws.held[q];
-    const int32_t* top = p.free_pages + (nf - 1 - p.ws.first[q]);
-    for (int k = 0; k < take; ++k) p.table[(size_t)q * p.max_pages + had + k] = top[-k];
+    const int32_t* top = p.free_pages + (nf - 1 - first[q]);
+    for (int k = 0; k < take[q]; ++k) p.table[(size_t)q * p.max_pages + held[q] + k] = top[-k];
   }
   if (p.parent) {
     for (int k = tid; k < R * p.width; k += kSmallThreads) {
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(PlanArgs p) {
       else
         hi = mid;
     }
-    plan_row(p, lo, off[lo], row - off[lo], p.ws.held[lo], p.free_pages + (nf - 1 - p.ws.first[lo]),
+    plan_row(p, lo, off[lo], row - off[lo], held[lo], p.free_pages + (nf - 1 - first[lo]),
              p.parent ? up + lo * p.width : nullptr);
   }
 }
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(256) append_kernel(
 // commit
 // ---------------------------------------------------------------------------------------
 struct CommitWs {
-  int32_t* ctx;    // [R] lengths before the call
+  int32_t* ctx;    // [R] lengths before the call (null: not kept)
   int32_t* held;   // [R] pages held before the call
   int32_t* first;  // [R] place of q's first page on the free list
   size_t bytes;
@@ -293,7 +296,7 @@ __device__ __forceinline__ int clamp_acc(int na, int c, int h, int lg, int most)
 
 // entries of the block tables up to which one workgroup gives pages back (it copies about 256
 // of them a microsecond)
-constexpr int kGivePages = 16384;
+constexpr int kGivePages = 16384, kCommitR = 1024;
 
 struct CommitArgs {
   int R, gamma, most, lg, max_pages, free_len;
@@ -308,10 +311,10 @@ struct CommitArgs {
   CommitWs ws;
 };
 
-// Lengths of every request and the places of the pages given back, by one workgroup; GIVE:
-// and the pages themselves, a wave per request.
+// Lengths of every request and the places of the pages given back, by one workgroup, kept in
+// `to`; GIVE: and the pages themselves, a wave per request.
 template <int NT, bool GIVE>
-__device__ __forceinline__ void commit_scan(const CommitArgs& p, int64_t* sums) {
+__device__ __forceinline__ void commit_scan(const CommitArgs& p, const CommitWs& to, int64_t* sums) {
   const int R = p.R, tid = threadIdx.x;
   const int per = (R + NT - 1) / NT;
   const int lo = min(R, tid * per), hi = min(R, lo + per);
@@ -324,8 +327,8 @@ __device__ __forceinline__ void commit_scan(const CommitArgs& p, int64_t* sums) 
     }
     const bool end = p.done && p.done[q] != 0;
     const int c = p.ctx[q], n = p.n_acc[q];
-    p.ws.ctx[q] = c;
-    p.ws.held[q] = h;
+    if (to.ctx) to.ctx[q] = c;
+    to.held[q] = h;
     if (end) {
       s += h;
       p.ctx_out[q] = 0;
@@ -344,9 +347,9 @@ __device__ __forceinline__ void commit_scan(const CommitArgs& p, int64_t* sums) 
   const int64_t end = block_scan<NT>(s, sums);
   int64_t at = nf + end - s;
   for (int q = lo; q < hi; ++q) {
-    p.ws.first[q] = (int32_t)(at < p.free_len ? at : p.free_len);
+    to.first[q] = (int32_t)(at < p.free_len ? at : p.free_len);
     if (p.done[q] != 0) {
-      at += p.ws.held[q];
+      at += to.held[q];
       p.held[q] = 0;
     }
   }
@@ -359,7 +362,7 @@ __device__ __forceinline__ void commit_scan(const CommitArgs& p, int64_t* sums) 
     __syncthreads();
     for (int q = tid / kWave; q < R; q += NT / kWave) {
       if (p.done[q] == 0) continue;
-      const int first = p.ws.first[q], h = p.ws.held[q];
+      const int first = to.first[q], h = to.held[q];
       for (int k = tid & (kWave - 1); k < h && first + k < p.free_len; k += kWave)
         p.free_pages[first + k] = p.table[(size_t)q * p.max_pages + k];
     }
@@ -426,9 +429,10 @@ __device__ __forceinline__ void commit_move(const CommitArgs& p, int q, int slic
 // alone: ctx, and held of requests that go on.
 __global__ void __launch_bounds__(256) commit_kernel(CommitArgs p, int slices) {
   __shared__ int64_t sums[256 / kWave];
+  __shared__ int held[kCommitR], first[kCommitR];
   const int b = blockIdx.x;
   if (b == (int)gridDim.x - 1) {
-    commit_scan<256, true>(p, sums);
+    commit_scan<256, true>(p, CommitWs{nullptr, held, first, 0}, sums);
     return;
   }
   const int q = b / slices;
@@ -440,7 +444,7 @@ __global__ void __launch_bounds__(256) commit_kernel(CommitArgs p, int slices) {
 // Two launches otherwise: the scan, then the moves from the lengths it kept, and the pages.
 __global__ void __launch_bounds__(kPlanThreads) commit_scan_kernel(CommitArgs p) {
   __shared__ int64_t sums[kPlanThreads / kWave];
-  commit_scan<kPlanThreads, false>(p, sums);
+  commit_scan<kPlanThreads, false>(p, p.ws, sums);
 }
 
 __global__ void __launch_bounds__(256) commit_move_kernel(CommitArgs p) {
@@ -459,8 +463,14 @@ __global__ void __launch_bounds__(256) commit_move_kernel(CommitArgs p) {
 
 using namespace dspark;
 
-extern "C" size_t dspark_cache_plan_workspace_bytes(int R) {
-  return R < 1 || R > kMaxRequests ? 0 : carve_plan(nullptr, R).bytes;
+// whether one workgroup makes the whole plan
+static bool plan_small(int R, int rows, int width) {
+  return R <= kSmallR && rows <= kSmallRows && (int64_t)R * width <= kSmallNodes;
+}
+
+extern "C" size_t dspark_cache_plan_workspace_bytes(int R, int rows, int width) {
+  if (R < 1 || R > kMaxRequests || plan_small(R, rows, width)) return 0;
+  return carve_plan(nullptr, R).bytes;
 }
 
 extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, int free_len,
@@ -475,12 +485,13 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
       !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
   if (R == 0) return DSPARK_OK;
-  if (!lens || !ctx || !held || !table || !n_free || !row_off || !ws ||
+  const bool small = plan_small(R, rows, parent ? width : 0);
+  if (!lens || !ctx || !held || !table || !n_free || !row_off || (!small && !ws) ||
       (free_len > 0 && !free_pages) || (rows > 0 && (!slot || (parent && !anc))) ||
       (parent && width < 1) || !aligned16(ws))
     return DSPARK_EINVAL;
   const PlanWs w = carve_plan(ws, R);
-  if (ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
+  if (!small && ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
   PlanArgs p{};
   p.R = R;
   p.rows = rows;
@@ -505,7 +516,7 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
   p.anc = anc;
   p.status = dev_status;
   p.ws = w;
-  if (R <= kSmallR && rows <= kSmallRows && (!parent || (int64_t)R * width <= kSmallNodes)) {
+  if (small) {
     plan_small_kernel<<<1, kSmallThreads, 0, stream>>>(p);
     return launch_status();
   }
@@ -546,8 +557,15 @@ extern "C" int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, in
   return launch_status();
 }
 
-extern "C" size_t dspark_cache_commit_workspace_bytes(int R) {
-  return R < 1 || R > kMaxRequests ? 0 : carve_commit(nullptr, R).bytes;
+// whether one launch commits: few pages to give back, and lengths apart from those that the
+// moves read
+static bool commit_small(int R, int64_t pages, bool moves_in_place) {
+  return R <= kCommitR && pages <= kGivePages && !moves_in_place;
+}
+
+extern "C" size_t dspark_cache_commit_workspace_bytes(int R, int max_pages, int moves_in_place) {
+  if (R < 1 || R > kMaxRequests || commit_small(R, (int64_t)R * max_pages, moves_in_place)) return 0;
+  return carve_commit(nullptr, R).bytes;
 }
 
 extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free_len,
@@ -573,7 +591,7 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
       return DSPARK_EINVAL;
   }
   if (R == 0) return DSPARK_OK;
-  if (!n_acc || !ctx || !ctx_out || !held || !table || !ws || !aligned16(ws) ||
+  if (!n_acc || !ctx || !ctx_out || !held || !table || !aligned16(ws) ||
       (done && (!n_free || (free_len > 0 && !free_pages))))
     return DSPARK_EINVAL;
   const size_t len_bytes = (size_t)R * sizeof(int32_t);
@@ -581,8 +599,10 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   if ((!apart && ctx_out != ctx) || overlap(ctx_out, len_bytes, n_acc, len_bytes) ||
       overlap(ctx_out, len_bytes, held, len_bytes))
     return DSPARK_EINVAL;
+  const bool small = commit_small(R, done ? (int64_t)R * max_pages : 0, path && !apart);
   const CommitWs w = carve_commit(ws, R);
-  if (ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
+  if (!small && !ws) return DSPARK_EINVAL;
+  if (!small && ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
   const int lg = log2_of(page_size), u = (int)(16 / e), chunks = path ? D / u : 1;
   const int64_t cols = path ? (int64_t)layers * 2 * Hkv * chunks : 1;
   if ((cols + 255) / 256 > 65535) return DSPARK_EINVAL;
@@ -615,9 +635,9 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   p.tok_stride = tok_stride / u;
   p.status = dev_status;
   p.ws = w;
-  const bool few = R <= 1024 && (!done || (int64_t)R * max_pages <= kGivePages);
   const int64_t blocks = path ? (int64_t)R * slices : 0;
-  if (few && (!path || (apart && blocks < (1 << 24) - 1))) {
+  if (blocks >= (1 << 24) - 1) return DSPARK_EINVAL;  // a grid holds 2^32 threads
+  if (small) {
     commit_kernel<<<(unsigned)blocks + 1, 256, 0, stream>>>(p, slices);
     return launch_status();
   }

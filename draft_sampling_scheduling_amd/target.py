@@ -31,7 +31,7 @@ _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat1
 def set_argtypes(L):
     """ctypes signatures of the library's target-side entry points."""
     i, i64, sz, vp, f = C.c_int, C.c_int64, C.c_size_t, C.c_void_p, C.c_float
-    L.dspark_cache_plan_workspace_bytes.argtypes = [i]
+    L.dspark_cache_plan_workspace_bytes.argtypes = [i] * 3
     L.dspark_cache_plan_workspace_bytes.restype = sz
     L.dspark_cache_plan.argtypes = ([i] * 6 + [vp] * 7 + [i] + [vp] * 7 + [sz, vp])
     L.dspark_cache_append.argtypes = ([i] * 6 + [vp] * 2 + [i64] * 2 + [vp] * 4 + [i64] * 3 +
@@ -42,7 +42,7 @@ def set_argtypes(L):
                                         [f] + [vp] * 4 + [sz, vp])
     L.dspark_target_logits.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 4 + [i] + [vp] * 7 +
                                        [i, vp, i, i] + [vp] * 4)
-    L.dspark_cache_commit_workspace_bytes.argtypes = [i]
+    L.dspark_cache_commit_workspace_bytes.argtypes = [i] * 3
     L.dspark_cache_commit_workspace_bytes.restype = sz
     L.dspark_cache_commit.argtypes = ([i] * 5 + [vp] * 9 + [i] * 5 + [vp] * 2 + [i64] * 4 +
                                       [vp] * 2 + [sz, vp])
@@ -70,6 +70,7 @@ def _device(t, name):
     return t.device
 
 
+# (get_device(): a tensor's device index, -1 on the host, at half the cost of its device)
 def _dims(t, name, n):
     """Sizes of a tensor of n dimensions."""
     if not isinstance(t, torch.Tensor):
@@ -94,7 +95,7 @@ def _refuse(t, name, dev, shape, dtype):
 def _chk(t, name, dev, shape, dtype):
     """One tensor argument; returns its address."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
-            t.device == dev and t.is_contiguous()):
+            t.get_device() == dev.index and t.is_contiguous()):
         return t.data_ptr()
     _refuse(t, name, dev, shape, dtype)
 
@@ -125,7 +126,8 @@ def _strides(t, last):
 
 def _rows(t, name, dev, shape, dtype):
     """A tensor of rows [rows][heads][D], each dense; returns its address and row stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.device != dev:
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or
+            t.get_device() != dev.index):
         _refuse(t, name, dev, shape, dtype)
     st = t.stride()
     if st[2] == 1 and st[1] == shape[2] and shape[0] != 1:
@@ -140,8 +142,8 @@ def _cache(k_cache, v_cache, dev, dims):
     """Addresses, shape and strides of a pair of caches (`dims`: 4, or 5 with a leading layer)."""
     shape = _dims(k_cache, "k_cache", dims)
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if (not isinstance(t, torch.Tensor) or t.device != dev or t.dtype is not k_cache.dtype or
-                t.shape != shape):
+        if (not isinstance(t, torch.Tensor) or t.get_device() != dev.index or
+                t.dtype is not k_cache.dtype or t.shape != shape):
             _refuse(t, name, dev, shape, k_cache.dtype)
     st = k_cache.stride()
     if 1 in shape or st[-1] != 1 or v_cache.stride() != st:
@@ -181,7 +183,8 @@ def _call(dev, name, *args):
 
 def _workspace(nbytes, dev, ws):
     if ws is None:
-        nbytes = max(nbytes, 256)
+        if nbytes == 0:
+            return None, None, 0
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         return ws, ws.data_ptr(), nbytes
     if ws.device != dev or not ws.is_contiguous():
@@ -192,8 +195,8 @@ def _workspace(nbytes, dev, ws):
     return ws, ws.data_ptr(), have
 
 
-def cache_plan_workspace_bytes(R) -> int:
-    return _fn("dspark_cache_plan_workspace_bytes")(R)
+def cache_plan_workspace_bytes(R, rows, width=0) -> int:
+    return _fn("dspark_cache_plan_workspace_bytes")(R, rows, width)
 
 
 def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, extra=0,
@@ -230,7 +233,7 @@ def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, e
     if R == 0:
         out["row_off"].zero_()
         return out
-    ws, wp, wb = _workspace(cache_plan_workspace_bytes(R), dev, ws)
+    ws, wp, wb = _workspace(cache_plan_workspace_bytes(R, rows, width), dev, ws)
     _call(dev, "dspark_cache_plan", R, rows, page_size, W, F, extra, *a, width, *b, wp, wb)
     return out
 
@@ -349,8 +352,8 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
     return out
 
 
-def cache_commit_workspace_bytes(R) -> int:
-    return _fn("dspark_cache_commit_workspace_bytes")(R)
+def cache_commit_workspace_bytes(R, max_pages, moves_in_place=False) -> int:
+    return _fn("dspark_cache_commit_workspace_bytes")(R, max_pages, moves_in_place)
 
 
 def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path=None, done=None,
@@ -385,6 +388,7 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     sp = _opt(status, "status", dev, (1,), _I32)
     if R == 0:
         return out
-    ws, wp, wb = _workspace(cache_commit_workspace_bytes(R), dev, ws)
+    ws, wp, wb = _workspace(
+        cache_commit_workspace_bytes(R, W, path is not None and a[3] == b[0]), dev, ws)
     _call(dev, "dspark_cache_commit", R, gamma, page_size, W, F, *a, *b, *c, sp, wp, wb)
     return out

@@ -73,9 +73,10 @@ enum { DSPARK_MAX_TREE_NODES = 65 };
  * (DSPARK_FAULT_PAGE); *n_free outside [0, free_len] is clamped (DSPARK_FAULT_PAGE).
  * Outputs: row_off [R+1]; req, position, slot [rows] int32 (req and position nullable);
  * anc [rows] uint64.  Rows at and behind row_off[R] are left as they were.
- * Workspace: ws_bytes >= dspark_cache_plan_workspace_bytes(R).
+ * Workspace: ws_bytes >= dspark_cache_plan_workspace_bytes(R, rows, width), width 0 for
+ * chains; where that is 0 (small steps), ws may be NULL.
  * ------------------------------------------------------------------------------------ */
-size_t dspark_cache_plan_workspace_bytes(int R);
+size_t dspark_cache_plan_workspace_bytes(int R, int rows, int width);
 
 int dspark_cache_plan(int R, int rows, int page_size, int max_pages, int free_len, int extra,
                       const int32_t *lens, const int32_t *ctx, int32_t *held, int32_t *table,
@@ -186,9 +187,10 @@ int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *l
  * entries of it, is moved no further (DSPARK_FAULT_TREE); a page id outside [0, n_pages)
  * moves nothing (DSPARK_FAULT_PAGE); pages past free_len are dropped (DSPARK_FAULT_PAGE).
  * gamma <= 64.  D % 8 == 0, D <= 1024; the cache arguments are read only with a path.
- * Workspace: ws_bytes >= dspark_cache_commit_workspace_bytes(R).
+ * Workspace: ws_bytes >= dspark_cache_commit_workspace_bytes(R, max_pages, moves_in_place),
+ * the last nonzero with a path and ctx_out == ctx; where that is 0, ws may be NULL.
  * ------------------------------------------------------------------------------------ */
-size_t dspark_cache_commit_workspace_bytes(int R);
+size_t dspark_cache_commit_workspace_bytes(int R, int max_pages, int moves_in_place);
 
 int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free_len,
                         const int32_t *n_acc, const int32_t *path, const int32_t *done,

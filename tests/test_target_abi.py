@@ -33,10 +33,16 @@ def test_exports_every_declared_symbol(ds):
 
 
 def test_workspace_sizes(ds):
-    assert ds.cache_plan_workspace_bytes(0) == 0
-    assert ds.cache_plan_workspace_bytes(256) >= 3 * 4 * 256
-    assert ds.cache_commit_workspace_bytes(-1) == 0
-    assert ds.cache_commit_workspace_bytes(7) >= 3 * 4 * 7
+    assert ds.cache_plan_workspace_bytes(0, 5000) == 0
+    assert ds.cache_plan_workspace_bytes(256, 1024) == 0          # small: needs none
+    assert ds.cache_plan_workspace_bytes(256, 1025) >= 3 * 4 * 256
+    assert ds.cache_plan_workspace_bytes(257, 300) >= 3 * 4 * 257
+    assert ds.cache_plan_workspace_bytes(200, 1000, 65) >= 3 * 4 * 200
+    assert ds.cache_commit_workspace_bytes(-1, 10) == 0
+    assert ds.cache_commit_workspace_bytes(7, 100) == 0
+    assert ds.cache_commit_workspace_bytes(7, 100, True) >= 3 * 4 * 7
+    assert ds.cache_commit_workspace_bytes(1025, 1) >= 3 * 4 * 1025
+    assert ds.cache_commit_workspace_bytes(512, 33) >= 3 * 4 * 512
     assert ds.tree_attention_workspace_bytes(4, 20, 8, 2, 64, ds.BF16) > 0
     assert ds.tree_attention_workspace_bytes(0, 20, 8, 2, 64, ds.BF16) == 0
     for bad in (dict(Hq=7), dict(Hkv=0), dict(D=96), dict(dt=2), dict(rows=-1)):
@@ -46,9 +52,9 @@ def test_workspace_sizes(ds):
 
 
 def test_plan_refusals(ds):
-    ws = ds.cache_plan_workspace_bytes(4)
+    ws = ds.cache_plan_workspace_bytes(4, 2000)
 
-    def call(R=4, rows=20, page=16, W=10, free_len=8, extra=1, lens=P(), free=P(), parent=None,
+    def call(R=4, rows=2000, page=16, W=10, free_len=8, extra=1, lens=P(), free=P(), parent=None,
              width=0, slot=P(), anc=None, wsp=P(), ws_bytes=ws):
         return ds.lib().dspark_cache_plan(R, rows, page, W, free_len, extra, lens, P(), P(), P(),
                                           free, P(), parent, width, P(), None, None, slot, anc,
@@ -57,7 +63,8 @@ def test_plan_refusals(ds):
     for bad in (dict(R=-1), dict(R=(1 << 20) + 1), dict(rows=-1), dict(page=12), dict(page=4), dict(page=2048),
                 dict(W=0), dict(W=(1 << 26) + 1), dict(free_len=-1), dict(extra=2), dict(lens=None),
                 dict(free=None), dict(parent=P(), width=5), dict(parent=P(), anc=P(), width=0),
-                dict(slot=None), dict(wsp=None), dict(wsp=P(0x1002))):
+                dict(slot=None), dict(wsp=None), dict(wsp=P(0x1002)),
+                dict(rows=20, lens=None, wsp=None)):
         assert call(**bad) == ds.EINVAL, bad
     assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
     assert call(R=0) == ds.OK
@@ -116,7 +123,7 @@ def test_logits_refusals(ds):
 
 
 def test_commit_refusals(ds):
-    ws = ds.cache_commit_workspace_bytes(4)
+    ws = ds.cache_commit_workspace_bytes(4, 10, True)
 
     def call(R=4, gamma=4, page=16, W=10, n_acc=P(), path=P(), done=None, n_free=P(), free=P(),
              layers=1, Hkv=2, D=64, dt=ds.BF16, n=40, k=P(), st=1024, ws_bytes=ws, free_len=8,
