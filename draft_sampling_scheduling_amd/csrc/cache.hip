@@ -6,6 +6,8 @@
 // append copies two short rows per token.  What counts is the number of launches and of
 // dependent trips to memory, so each scan over the requests is one workgroup's, and all that
 // follows from it is one flat kernel.
+#include <atomic>
+
 #include "target.h"
 
 namespace dspark {
@@ -203,42 +205,122 @@ __global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(PlanArgs p) {
   for (int i = t0; i < n; i += step) plan_row(p, q, a, i, had, top, p.parent ? up : nullptr);
 }
 
-// The whole plan in one workgroup, for steps of few requests and rows: the scan, then a thread
-// per row, which finds its request in the row offsets.
-constexpr int kSmallThreads = 256, kSmallR = 256, kSmallRows = 1024, kSmallNodes = 8192;
+// The whole plan in one workgroup, for steps of not too many requests and rows: the scan; then
+// a thread per request takes its tree from the anchor down (a node's mask is its parent's and
+// its own bit) and names its rows' request; then a thread per row, four rows at a time (of
+// chains, which may be whole prompts, it finds the request in the row offsets).
+template <int NT_, int R_, int ROWS_, int NODES_>
+struct PlanSize {
+  static constexpr int NT = NT_, R = R_, ROWS = ROWS_, NODES = NODES_;
+  static bool fits(int r, int rows, int width) {
+    return r <= R && rows <= ROWS && (int64_t)r * width <= NODES;
+  }
+  struct Lds {
+    uint64_t bits[NODES];  // masks of the nodes, [R][width]
+    int64_t sums[2 * NT / kWave];
+    int held[R], take[R], first[R], off[R + 1], nfree[1], ctx[R];
+    uint16_t req[ROWS];  // request of each row (trees)
+    uint8_t up[NODES];
+  };
+};
+using SmallPlan = PlanSize<256, 256, 1024, 4096>;
+using MidPlan = PlanSize<1024, 1024, 16384, 10240>;
 
-__global__ void __launch_bounds__(kSmallThreads) plan_small_kernel(PlanArgs p) {
-  __shared__ int64_t sums[2 * kSmallThreads / kWave];
-  __shared__ int held[kSmallR], take[kSmallR], first[kSmallR], off[kSmallR + 1], nfree[1];
-  __shared__ int up[kSmallNodes];
-  const int tid = threadIdx.x, R = p.R;
-  plan_scan<kSmallThreads>(p, PlanWs{held, take, first, nfree, off, 0}, sums);
+template <class S>
+__global__ void __launch_bounds__(S::NT) plan_small_kernel(PlanArgs p) {
+  constexpr int NT = S::NT, kBatch = 4;
+  extern __shared__ uint64_t plan_lds[];
+  auto& m = *reinterpret_cast<typename S::Lds*>(plan_lds);
+  const int tid = threadIdx.x, R = p.R, lg = p.lg;
+  if (p.parent) {  // (checked against the rows once those are known)
+    constexpr int kLoads = 12;
+    const int nodes = R * p.width;
+    for (int k0 = tid; k0 < nodes; k0 += kLoads * NT) {
+      int x[kLoads];
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int k = k0 + u * NT;
+        x[u] = p.parent[k < nodes ? k : nodes - 1];
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        const int k = k0 + u * NT;
+        if (k < nodes) m.up[k] = (uint8_t)(x[u] >= 0 && x[u] < k % p.width ? x[u] : 255);
+      }
+    }
+  }
+  plan_scan<NT>(p, PlanWs{m.held, m.take, m.first, m.nfree, m.off, 0}, m.sums);
   __syncthreads();
-  const int nf = nfree[0];
-  for (int q = tid; q < R; q += kSmallThreads) {
-    const int32_t* top = p.free_pages + (nf - 1 - first[q]);
-    for (int k = 0; k < take[q]; ++k) p.table[(size_t)q * p.max_pages + held[q] + k] = top[-k];
-  }
-  if (p.parent) {
-    for (int k = tid; k < R * p.width; k += kSmallThreads) {
-      const int q = k / p.width, i = k % p.width;
-      if (i < off[q + 1] - off[q]) up[k] = plan_parent(p, q, i);
+  const int nf = m.nfree[0];
+  for (int q = tid; q < R; q += NT) {
+    m.ctx[q] = p.ctx[q];
+    const int32_t* top = p.free_pages + (nf - 1 - m.first[q]);
+    for (int k = 0; k < m.take[q]; ++k) p.table[(size_t)q * p.max_pages + m.held[q] + k] = top[-k];
+    if (p.parent) {
+      const int n = m.off[q + 1] - m.off[q], at = q * p.width;
+      for (int i = 0; i < n; ++i) {
+        int u = m.up[at + i];
+        if (i > 0 && u == 255) {
+          raise_fault(p.status, DSPARK_FAULT_TREE);
+          u = i - 1;
+        }
+        m.bits[at + i] = i == 0 ? 0 : m.bits[at + u] | (uint64_t)1 << (i - 1);
+        m.req[m.off[q] + i] = (uint16_t)q;
+      }
     }
-    __syncthreads();
   }
-  const int rows = off[R];
-  for (int row = tid; row < rows; row += kSmallThreads) {
-    int lo = 0, hi = R;  // the last request that begins at or before the row
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (off[mid] <= row)
-        lo = mid;
-      else
-        hi = mid;
+  __syncthreads();
+  const int rows = m.off[R];
+  int half = 1;  // the largest power of two below R, or 1
+  while (2 * half < R) half *= 2;
+  for (int row0 = tid; row0 < rows; row0 += kBatch * NT) {
+    int q[kBatch], t[kBatch], page[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      q[u] = p.parent && row0 + u * NT < rows ? m.req[row0 + u * NT] : 0;
+    for (int s = p.parent ? 0 : half; s > 0; s >>= 1)  // the last that begins at or before the row
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int next = q[u] + s;
+        q[u] = next < R && m.off[next] <= row0 + u * NT ? next : q[u];
+      }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int row = row0 + u * NT;
+      t[u] = row < rows ? m.ctx[q[u]] + row - m.off[q[u]] : 0;
     }
-    plan_row(p, lo, off[lo], row - off[lo], held[lo], p.free_pages + (nf - 1 - first[lo]),
-             p.parent ? up + lo * p.width : nullptr);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int idx = t[u] >> lg, more = idx - m.held[q[u]];
+      const int32_t* at = more < 0 ? p.table + (size_t)q[u] * p.max_pages + idx
+                                   : p.free_pages + (nf - 1 - m.first[q[u]] - more);
+      page[u] = row0 + u * NT < rows ? *at : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int row = row0 + u * NT, i = row - m.off[q[u]];
+      if (row >= rows) break;
+      const bool known = page[u] >= 0 && page[u] <= (0x7fffffff >> lg);
+      if (!known) raise_fault(p.status, DSPARK_FAULT_PAGE);
+      p.slot[row] = known ? (page[u] << lg) + (t[u] & ((1 << lg) - 1)) : -1;
+      int depth = i;
+      if (p.parent) {
+        const uint64_t bits = m.bits[q[u] * p.width + i];
+        p.anc[row] = bits;
+        depth = __popcll(bits);
+      }
+      if (p.req) p.req[row] = q[u];
+      if (p.position) p.position[row] = t[u] - i + depth;
+    }
   }
+}
+
+template <class S>
+static void plan_small_launch(const PlanArgs& p, hipStream_t stream) {
+  static std::atomic<uint64_t> raised;
+  ensure_dynamic_lds(reinterpret_cast<const void*>(plan_small_kernel<S>), sizeof(typename S::Lds),
+                     raised);
+  plan_small_kernel<S><<<1, S::NT, sizeof(typename S::Lds), stream>>>(p);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -465,7 +547,7 @@ using namespace dspark;
 
 // whether one workgroup makes the whole plan
 static bool plan_small(int R, int rows, int width) {
-  return R <= kSmallR && rows <= kSmallRows && (int64_t)R * width <= kSmallNodes;
+  return SmallPlan::fits(R, rows, width) || MidPlan::fits(R, rows, width);
 }
 
 extern "C" size_t dspark_cache_plan_workspace_bytes(int R, int rows, int width) {
@@ -517,7 +599,10 @@ extern "C" int dspark_cache_plan(int R, int rows, int page_size, int max_pages, 
   p.status = dev_status;
   p.ws = w;
   if (small) {
-    plan_small_kernel<<<1, kSmallThreads, 0, stream>>>(p);
+    if (SmallPlan::fits(R, rows, parent ? width : 0))
+      plan_small_launch<SmallPlan>(p, stream);
+    else
+      plan_small_launch<MidPlan>(p, stream);
     return launch_status();
   }
   plan_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);

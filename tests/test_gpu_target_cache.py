@@ -67,7 +67,8 @@ def run_plan(c, page, rows, extra=1, ws=None):
 @pytest.mark.parametrize("R,gamma,page,ctx_hi,tree", [
     (1, 1, 8, 0, False), (1, 64, 8, 3, True), (4, 4, 16, 200, False), (37, 8, 16, 700, True),
     (257, 3, 64, 5000, False), (512, 16, 16, 8192, True), (1300, 2, 1024, 4000, False),
-    (3000, 1, 8, 60, True)])
+    (3000, 1, 8, 60, True), (700, 30, 16, 900, True), (1024, 15, 32, 100, False),
+    (1024, 11, 16, 50, True)])
 def test_plan(R, gamma, page, ctx_hi, tree):
     c = case(R + gamma, R, gamma, page, ctx_hi, R * (ref.cdiv(gamma + 1, page) + 1), tree)
     want, bits = run_plan(c, page, R * (gamma + 1))
@@ -92,11 +93,13 @@ def test_plan_sits_out():
 
 @pytest.mark.parametrize("spare", [0, 1, 3, 7])
 def test_plan_out_of_pages(spare):
-    """Those whose pages are had are served, those that need none too, the others not."""
-    c = case(7, 40, 12, 8, 90, spare)
-    want, bits = run_plan(c, 8, 40 * 13)
-    assert bits == 8 and 0 <= want["n_free"] <= spare
-    assert want["row_off"][-1] > 0 or spare == 0
+    """Those whose pages are had are served, those that need none too, the others not; at sizes
+    for one workgroup of each kind, and for two launches."""
+    for rows in (40 * 13, 3000, 20000):
+        c = case(7, 40, 12, 8, 90, spare)
+        want, bits = run_plan(c, 8, rows)
+        assert bits == 8 and 0 <= want["n_free"] <= spare
+        assert want["row_off"][-1] > 0 or spare == 0
 
 
 @pytest.mark.parametrize("rows", [0, 1, 17, 60])
@@ -120,8 +123,9 @@ def test_plan_faults():
     c["ctx"][7], c["lens"][7], c["held"][7] = 40, 3, 3
     c["table"][7][:3] = [5, 6, -1]              # its rows' page is unknown: slots -1
     c["lens"][8] = 2 ** 31 - 1            # no row count: refused
-    _, bits = run_plan(c, 16, 12 * 7)
-    assert bits == 4 | 8 | 16
+    for rows in (12 * 7, 3000, 20000):
+        _, bits = run_plan(c, 16, rows)
+        assert bits == 4 | 8 | 16
 
 
 def test_plan_page_ids_past_the_slots():

@@ -363,7 +363,7 @@ def test_workspaces_given():
     want = snap(s.run(ds))
     att = ds.tree_attention_workspace_bytes(s.R, s.rows, s.Hq, s.Hkv, 64, ds.BF16)
     for fill in (0, 255, 127):
-        ws = torch.full((max(att, ds.cache_plan_workspace_bytes(s.R, 5000)),), fill, dtype=torch.uint8,
+        ws = torch.full((max(att, ds.cache_plan_workspace_bytes(s.R, 20000)),), fill, dtype=torch.uint8,
                         device="cuda")
         for a, b in zip(s.state, s.state0):
             a.copy_(b)

@@ -35,8 +35,8 @@ def test_exports_every_declared_symbol(ds):
 def test_workspace_sizes(ds):
     assert ds.cache_plan_workspace_bytes(0, 5000) == 0
     assert ds.cache_plan_workspace_bytes(256, 1024) == 0          # small: needs none
-    assert ds.cache_plan_workspace_bytes(256, 1025) >= 3 * 4 * 256
-    assert ds.cache_plan_workspace_bytes(257, 300) >= 3 * 4 * 257
+    assert ds.cache_plan_workspace_bytes(256, 16385) >= 3 * 4 * 256
+    assert ds.cache_plan_workspace_bytes(1025, 300) >= 3 * 4 * 1025
     assert ds.cache_plan_workspace_bytes(200, 1000, 65) >= 3 * 4 * 200
     assert ds.cache_commit_workspace_bytes(-1, 10) == 0
     assert ds.cache_commit_workspace_bytes(7, 100) == 0
@@ -52,9 +52,9 @@ def test_workspace_sizes(ds):
 
 
 def test_plan_refusals(ds):
-    ws = ds.cache_plan_workspace_bytes(4, 2000)
+    ws = ds.cache_plan_workspace_bytes(4, 20000)
 
-    def call(R=4, rows=2000, page=16, W=10, free_len=8, extra=1, lens=P(), free=P(), parent=None,
+    def call(R=4, rows=20000, page=16, W=10, free_len=8, extra=1, lens=P(), free=P(), parent=None,
              width=0, slot=P(), anc=None, wsp=P(), ws_bytes=ws):
         return ds.lib().dspark_cache_plan(R, rows, page, W, free_len, extra, lens, P(), P(), P(),
                                           free, P(), parent, width, P(), None, None, slot, anc,
