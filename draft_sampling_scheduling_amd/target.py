@@ -100,8 +100,14 @@ def _chk(t, name, dev, shape, dtype):
     _refuse(t, name, dev, shape, dtype)
 
 
-def _opt(t, *a):
-    return None if t is None else _chk(t, *a)
+def _opt(t, name, dev, shape, dtype):
+    """_chk of an argument that may be None (written out: a call less)."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.get_device() == dev.index and t.is_contiguous()):
+        return t.data_ptr()
+    _refuse(t, name, dev, shape, dtype)
 
 
 def _dt(t, name):
@@ -290,7 +296,8 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
         from . import EINVAL, DsparkError
         raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
     ws, wp, wb = _workspace(nbytes, dev, ws)
-    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st, *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
+    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st,
+          *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
     return out
 
 
@@ -321,7 +328,7 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
         st = _strides(logits, 1)
         if st is None:
             raise ValueError("rows of logits must be contiguous")
-        lp, stride = logits.data_ptr(), max(st[0], V)
+        lp, stride = logits.data_ptr(), st[0] if rows > 1 else V
     if out is None:
         out = torch.empty((R, gamma + 1, V), dtype=logits.dtype, device=dev)
     op = _chk(out, "out", dev, (R, gamma + 1, V), logits.dtype)
@@ -329,13 +336,13 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
     if hist is not None:
         if hist_len is None:
             raise ValueError("hist needs hist_len")
-        n_hist = hist.shape[-1]
+        n_hist = _dims(hist, "hist", 2)[1]
     if (bias is None) != (bias_id is None):
         raise ValueError("bias and bias_id come together")
     if bias is not None:
-        nb = bias.shape[-1]
+        nb = _dims(bias, "bias", 2)[1]
     if mask is not None:
-        n_mask, words = mask.shape[0], mask.shape[-1]
+        n_mask, words = _dims(mask, "mask", 2)
         if mask_idx is None and n_mask < R * (gamma + 1):
             raise ValueError("without mask_idx there is a mask for every row")
     per = (R,)

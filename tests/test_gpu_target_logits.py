@@ -210,3 +210,13 @@ def test_refusals():
         ds.target_logits(lg, ell, x, mask=T([[1]]), mask_idx=T([[0] * 3] * 2))  # too few words
     with pytest.raises(ds.DsparkError):
         ds.target_logits(lg.view(6, 64), ell, x, row_off=T([0, 2, 4]), out=lg)  # packed, in place
+    off = T([0, 2, 4])
+    for bad in (lg.view(6, 64)[:1].expand(4, 64), lg.view(6, 64)[:4, :32].contiguous().view(-1)[:72]
+                .as_strided((4, 64), (2, 1))):  # rows over each other
+        with pytest.raises(ds.DsparkError):
+            ds.target_logits(bad, ell, x, row_off=off)
+    one = ds.target_logits(lg.view(6, 64)[:1], T([0]), x[:1], row_off=T([0, 1]))
+    assert torch.equal(one[0, 0], lg[0, 0])
+    for k in (dict(hist=[[1]], hist_len=ell), dict(mask=3), dict(bias=[0.0], bias_id=h)):
+        with pytest.raises(TypeError):
+            ds.target_logits(lg, ell, x, **k)
