@@ -42,7 +42,8 @@ def test_workspace_sizes(ds):
     assert ds.cache_commit_workspace_bytes(7, 100) == 0
     assert ds.cache_commit_workspace_bytes(7, 100, True) >= 3 * 4 * 7
     assert ds.cache_commit_workspace_bytes(1025, 1) >= 3 * 4 * 1025
-    assert ds.cache_commit_workspace_bytes(512, 33) >= 3 * 4 * 512
+    assert ds.cache_commit_workspace_bytes(512, 8) == 0
+    assert ds.cache_commit_workspace_bytes(512, 9) >= 3 * 4 * 512
     assert ds.tree_attention_workspace_bytes(4, 20, 8, 2, 64, ds.BF16) > 0
     assert ds.tree_attention_workspace_bytes(0, 20, 8, 2, 64, ds.BF16) == 0
     for bad in (dict(Hq=7), dict(Hkv=0), dict(D=96), dict(dt=2), dict(rows=-1)):
