@@ -934,8 +934,8 @@ static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, d
 }
 
 static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt) {
-  return R >= 0 && R <= kMaxRequests && rows >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && (D == 64 || D == 128) &&
-         (dt == DSPARK_F32 || dt == DSPARK_BF16) && (int64_t)rows * Hq < ((int64_t)1 << 31);
+  return R >= 0 && R <= kMaxRequests && rows >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
+         (D == 64 || D == 128) && (dt == DSPARK_F32 || dt == DSPARK_BF16) && (int64_t)rows * Hq < ((int64_t)1 << 31);
 }
 
 template <class T, int D, int NR>
@@ -991,7 +991,8 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
     return DSPARK_EINVAL;
   // a row's heads may be read after another's output is written
   const size_t row_bytes = (size_t)Hq * D * e;
-  if (overlap(q, (size_t)(rows - 1) * q_row * e + row_bytes, o, rows * row_bytes)) return DSPARK_EINVAL;
+  if (overlap(q, (size_t)(rows - 1) * q_row * e + row_bytes, o, rows * row_bytes))
+    return DSPARK_EINVAL;
   AttParams p{};
   p.R = R;
   p.rows = rows;

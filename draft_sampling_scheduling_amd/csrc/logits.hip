@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
   // them).  In a small step the round trips are all there is.
   int L = uniform_load(p.ell, q);
   const int64_t row0 = p.row_off ? uniform_load(p.row_off, q) : (int64_t)q * (p.gamma + 1);
+  const int64_t row1 = p.row_off ? uniform_load(p.row_off, (int64_t)q + 1) : p.rows;
+  const int64_t rows = row1 < p.rows ? row1 : p.rows;  // the request's end before them
   const bool has_hist = p.hist && p.hist_stride > 0;
   int hl = has_hist ? uniform_load(p.hist_len, q) : 0;
   const int pl = has_hist && p.prompt_len ? uniform_load(p.prompt_len, q) : 0;
@@ -120,7 +122,7 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
     L = L < 0 ? 0 : p.gamma;
   }
   auto param = [&](float x, float none, bool positive) {
-    const bool bad = !(fabsf(x) <= FLT_MAX) || (positive && !(x > 0.0f));
+    const bool bad = !(fabsf(x) <= FLT_MAX) || (positive && !(x >= FLT_MIN));
     if (bad && tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
     return bad ? none : x;
   };
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
     Raw8<T> x[kLogGroups];
     uint32_t bits[kLogGroups];
   };
-  auto row_ok = [&](int j) { return row0 + j >= 0 && row0 + j < p.rows; };
+  auto row_ok = [&](int j) { return row0 + j >= 0 && row0 + j < rows; };
   auto load_row = [&](int j, Row& r) {
 #pragma unroll
     for (int g = 0; g < kLogGroups; ++g) r.bits[g] = 0xFFu;

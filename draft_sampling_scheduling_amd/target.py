@@ -277,8 +277,8 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
     rows, Hq, _ = _dims(q, "q", 3)
     qp, qs = _rows(q, "q", dev, (rows, Hq, D), k_cache.dtype)
     R, W = _dims(table, "table", 2)
-    a = [_chk(table, "table", dev, (R, W), _I32), _chk(ctx, "ctx", dev, (R,), _I32), _chk(row_off, "row_off", dev, (R + 1,), _I32),
-         _opt(anc, "anc", dev, (rows,), _I64)]
+    a = [_chk(table, "table", dev, (R, W), _I32), _chk(ctx, "ctx", dev, (R,), _I32),
+         _chk(row_off, "row_off", dev, (R + 1,), _I32), _opt(anc, "anc", dev, (rows,), _I64)]
     if out is None:
         out = dict(o=torch.empty((rows, Hq, D), dtype=q.dtype, device=dev),
                    lse=torch.empty((rows, Hq), dtype=_F32, device=dev))
@@ -308,7 +308,8 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
     layout verify() takes: out [R][gamma+1][V], row j = 0..ell[q] following the anchor and
     x[q][:j] (x [R][gamma]: the drafted tokens).
     logits: packed [rows][V] with row_off [R+1] (a plan's), or [R][gamma+1][V] without; `out`
-    may be logits itself in the latter form.
+    may be logits itself in the latter form.  Rows that row_off does not give a request (one
+    that the plan did not serve, say) are left as they were and set FAULT_LEN.
     hist [R][n] with hist_len [R], prompt_len [R]: each request's tokens, prompt first, anchor
     included; rep divides positive and multiplies other logits of seen ids; pres and freq (times
     the count) are taken off generated ids; bias_id, bias [R][nbias] (-1: unused; the last

@@ -91,7 +91,8 @@ int dspark_cache_plan(int R, int rows, int page_size, int max_pages, int free_le
  * slot [rows] int32; slot -1 skips the row, any other value outside [0, n_pages *
  * page_size) skips it and sets DSPARK_FAULT_PAGE.  n_rows (device, nullable): only the first
  * *n_rows rows exist (pass row_off + R); no value of it reads past `rows`.  Slots of one
- * call are distinct; of rows with the same slot either's elements may remain.
+ * call are distinct; of rows with the same slot either's elements may remain.  k and v lie
+ * apart from the caches.
  * D % 8 == 0, D <= 1024; strides multiples of 16 bytes, pointers 16-byte aligned.
  * ------------------------------------------------------------------------------------ */
 int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size, int n_pages,
@@ -111,8 +112,8 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  * Scores, maxima, sums and o are held in float; with bf16 operands the weights exp(s - max)
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row
  * does not see (stale, infinite or NaN) does not reach it.
- * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.  D in {64, 128};
- * Hq a multiple of Hkv; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
+ * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.
+ * D in {64, 128}; Hq a multiple of Hkv; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
  * aligned.  ctx + n beyond max_pages pages, ctx < 0 or row_off out of order are clamped
  * (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0 (DSPARK_FAULT_PAGE); with
  * anc, nodes past 64 are seen by nobody but through ctx (DSPARK_FAULT_TREE).
@@ -141,7 +142,8 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  *   out[q][j][v] = l;  rows j > ell[q] are left as they were
  * hist holds the request's tokens, prompt first, the anchor included.
  * Inputs: logits: row row_off[q] + j, rows `row_stride` elements apart (row_off NULL: row
- *   q * (gamma + 1) + j), `rows` rows in all; ell [R]; x [R][gamma] int32;
+ *   q * (gamma + 1) + j), `rows` rows in all; row_off [R+1]: request q has no row at or
+ *   behind row_off[q+1]; ell [R]; x [R][gamma] int32;
  *   hist [R][hist_stride] int32, hist_len, prompt_len [R] (hist NULL: only drafted tokens
  *   count; prompt_len NULL: 0); rep, pres, freq [R] float (each nullable: 1, 0, 0);
  *   bias_id [R][nbias] int32 (-1: unused) and bias [R][nbias] float: of several entries for
@@ -151,10 +153,11 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  * out may be logits itself where row_off is NULL and row_stride is V, and overlaps it in no
  * other way.
  * A row whose mask allows nothing is all -inf.
- * Faults: ell outside [0, gamma] (DSPARK_FAULT_LEN, clamped); a row outside [0, rows)
- *   (DSPARK_FAULT_LEN, its out row is left as it was); hist_len outside [0, hist_stride],
+ * Faults: ell outside [0, gamma] (DSPARK_FAULT_LEN, clamped); a row that is
+ *   not the request's or outside [0, rows) (DSPARK_FAULT_LEN, its out row is left as it was:
+ *   what becomes of requests that the plan gave no rows); hist_len outside [0, hist_stride],
  *   prompt_len outside [0, hist_len] (DSPARK_FAULT_LEN, clamped); a token or bias id outside
- *   [0, V) (DSPARK_FAULT_TOKEN, ignored); rep not > 0 and finite, pres or freq not finite
+ *   [0, V) (DSPARK_FAULT_TOKEN, ignored); rep not finite or below FLT_MIN, pres or freq not finite
  *   (DSPARK_FAULT_PARAM: 1, 0, 0); a mask index outside [-1, n_mask) (DSPARK_FAULT_PARAM:
  *   no mask).
  * V % 8 == 0; logits, out and row_stride 16-byte aligned.
@@ -180,7 +183,8 @@ int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *l
  *     other way
  *   done [R] int32 (nullable): a request with done != 0 gives its pages back:
  *     free_pages[*n_free ..] takes table[q][0 .. held[q]) in request order, *n_free grows,
- *     held[q] = ctx_out[q] = 0 (its tokens are not moved)
+ *     held[q] = ctx_out[q] = 0 (its tokens are not moved).  Every page held is given back, so
+ *     no two requests hold the same one then
  * n_acc outside [-1, gamma] (gamma checked with a path only) or past the pages held is
  * clamped (DSPARK_FAULT_LEN); held outside [0, max_pages] counts as the nearer end
  * (DSPARK_FAULT_LEN); a path that does not ascend from 1 or passes the pages held, or n_acc

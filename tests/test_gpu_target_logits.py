@@ -171,8 +171,17 @@ def test_faults():
     st, o = go(ell=T([2, 7, -1]))
     assert st == 4 and torch.equal(o[:2], good[:2]) and torch.equal(o[2, :1], good[2, :1])
     assert torch.all(o[2, 1:] == 0)
-    st, o = go(row_off=T([0, -5, 8, 9]))
-    assert st == 4 and torch.equal(o[0], good[0]) and torch.all(o[1] == 0) and torch.all(o[2, 1:] == 0)
+    st, o = go(row_off=T([0, 3, -5, 9]))
+    assert st == 4 and torch.equal(o[0], good[0]) and torch.all(o[1:] == 0)
+    # requests that a step gave fewer rows than they have tokens, or none, take no one else's
+    st, o = go(row_off=T([0, 3, 8, 9]))
+    assert st == 4 and torch.equal(o[0], good[0]) and torch.all(o[2, 1:] == 0)
+    st, o = go(row_off=T([0, 0, 2, 11]))
+    assert st == 4 and torch.all(o[0] == 0) and torch.all(o[1, 2:] == 0)
+    st, want = go(row_off=T([0, 3, 5, 8]), ell=T([2, 1, 2]))
+    assert st == 0 and torch.all(want[1, 2:] == 0)
+    st, o = go(row_off=T([0, 3, 5, 8]))
+    assert st == 4 and torch.equal(o, want)
     for k in (dict(hist_len=T([4, 3, 3])), dict(prompt_len=T([0, 4, 0])), dict(hist_len=T([3, -1, 3]))):
         st, o = go(**k)
         assert st == 4 and torch.equal(o[2], good[2])
@@ -181,7 +190,7 @@ def test_faults():
               dict(bias_id=T([[64], [-1], [-1]]), bias=T([[1.0]] * 3, F32))):
         st, o = go(**k)
         assert st == 1 and torch.equal(o[1:], good[1:])
-    for k in (dict(rep=T([0.0, 1, 1], F32)), dict(rep=T([-1.0, 1, 1], F32)),
+    for k in (dict(rep=T([0.0, 1, 1], F32)), dict(rep=T([1e-39, 1, 1], F32)), dict(rep=T([-1.0, 1, 1], F32)),
               dict(rep=T([float("inf"), 1, 1], F32)), dict(freq=T([float("nan"), 0, 0], F32)),
               dict(mask=T([[-1, -1]]), mask_idx=T([[1, 0, 0]] + [[0, 0, -1]] * 2)),
               dict(mask=T([[-1, -1]]), mask_idx=T([[-2, 0, 0]] + [[0, 0, -1]] * 2))):
