@@ -48,6 +48,7 @@ struct AttJoint {
 
 struct AttParams {
   int R, rows, Hq, Hkv, G;  // G = Hq / Hkv
+  uint64_t inv_g;           // ceil(2^64 / G)
   int lg, max_pages, n_pages;
   const void* q;
   int64_t q_row;
@@ -62,6 +63,12 @@ struct AttParams {
   float* part;   // [grid][2][MR][D + 2]: O, then m, then l of each row
   AttJoint* joint;  // [grid] what the second kernel joins
 };
+
+// x / G and x % G of a query row of a request, a division by multiplication: exact for 32 bits
+__device__ __forceinline__ int node_of(const AttParams& p, int x) {
+  return p.G == 1 ? x : (int)__umul64hi((uint64_t)(uint32_t)x, p.inv_g);
+}
+__device__ __forceinline__ int group_of(const AttParams& p, int x) { return x - node_of(p, x) * p.G; }
 
 // a request's rows and tokens, as the host of the data should have them, clamped
 struct AttReq {
@@ -88,6 +95,13 @@ __device__ __forceinline__ AttReq att_req(const AttParams& p, int q, bool tell) 
     if (p.anc && n > DSPARK_MAX_TREE_NODES) raise_fault(p.status, DSPARK_FAULT_TREE);
   }
   return {a, n, c};
+}
+
+// tokens that the query rows before row m1 of a request see: a chain's see no node after their
+// last one's
+__device__ __forceinline__ int att_end(const AttParams& p, const AttReq& r, int m1) {
+  if (p.anc || m1 >= r.n * p.G) return r.ctx + r.n;
+  return r.ctx + node_of(p, m1 - 1) + 1;
 }
 
 // uniform loads through the scalar cache (the arrays are inputs, constant during the call)
@@ -205,6 +219,7 @@ struct AttWave {
   const char *kh, *vh;      // cache bases of the head
   const int32_t* pages;     // the request's block table
   int ctx, len, last_page;  // committed tokens, tokens in all, page of the last token
+  int seen;                 // tokens that every row of the row tile sees
   u32x4 qf[L::KSTEPS];
   uint64_t see;             // tree: nodes (bit j - 1) the lane's row sees
   int node;                 // chain: the lane's node
@@ -420,6 +435,7 @@ struct AttWave {
     vh = static_cast<const char*>(p.v) + head * p.head_b;
     len = rq.ctx + rq.n;
     last_page = (len - 1) >> p.lg;
+    seen = uni(rq.ctx + 1 + (p.anc ? 0 : node_of(p, m0)));
     m = -INFINITY;
     l = 0.0f;
 #pragma unroll
@@ -428,7 +444,7 @@ struct AttWave {
   __device__ __forceinline__ void queries(const AttReq& rq, int head, int m0, int M) {
     const int mi = m0 + n;
     const bool live = mi < M;
-    const int i = live ? mi / p.G : 0, g = live ? mi % p.G : 0;
+    const int i = live ? node_of(p, mi) : 0, g = live ? group_of(p, mi) : 0;
     const char* src = static_cast<const char*>(p.q) +
                       ((int64_t)(rq.a + i) * p.q_row + (int64_t)(head * p.G + g) * D) * L::kE;
 #pragma unroll
@@ -444,12 +460,7 @@ struct AttWave {
   __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr) {
     const int M = rq.n * p.G;
     begin(rq, q, head, m0, M);
-    // a chain's row tile sees no node after its last row's
-    int end = len;
-    if (!p.anc) {
-      const int last = m0 + NR * kRows - 1 < M - 1 ? m0 + NR * kRows - 1 : M - 1;
-      end = rq.ctx + last / p.G + 1;
-    }
+    int end = uni(att_end(p, rq, m0 + NR * kRows));
     end = end < (r0 + nr) * F::ROUND ? end : (r0 + nr) * F::ROUND;
     const int first = r0 * F::ROUND + (NR == 1 ? wave * kTok : 0);
     const int nt = first < end ? (end - first + F::ROUND - 1) / F::ROUND : 0;
@@ -474,7 +485,7 @@ struct AttWave {
     queries(rq, head, m0, M);
     for (int k = 0; k < nt; ++k) {
       const int t0 = first + k * F::ROUND, t1 = t0 + F::ROUND;
-      const bool more = k + 1 < nt, edge = t0 + kTok > ctx;
+      const bool more = k + 1 < nt, edge = t0 + kTok > seen;
       const int s = F::STAGES == 2 ? k & 1 : 0;
       const uint32_t ks = base + s * F::TILE, vs = ks + L::BYTES;
       if (F::STAGES == 1) {
@@ -555,10 +566,10 @@ struct AttWave {
       f32x16 sc = f32x16{};
       if (live) {
         scores(ks, sc);
-        if (t0 + kTok > ctx) mask(t0, sc);
+        if (t0 + kTok > seen) mask(t0, sc);
         weigh(sc);
       }
-      if (t0 + kTok > ctx && clean_values(t0, vs)) odd_values(ks, vs, sc);
+      if (t0 + kTok > seen && clean_values(t0, vs)) odd_values(ks, vs, sc);
       if (live) values(vs, sc);
       s = s + 1 == F::STAGES ? 0 : s + 1;
       s_next = s_next + 1 == F::STAGES ? 0 : s_next + 1;
@@ -609,15 +620,26 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
   extern __shared__ uint4 lds[];
   __shared__ int64_t sums[F::WAVES];
   __shared__ int64_t total_s, start_off;
-  __shared__ int start_s[4];
+  __shared__ int start_s[5];
   const int tid = threadIdx.x, wave = uni(tid >> 6);
   const int b = blockIdx.x;
 
-  auto list = [&](const AttReq& r) -> int64_t {
-    return (r.ctx + r.n + kRound - 1) / kRound + kSetup;
+  auto tiles = [&](const AttReq& r) { return (r.n * p.G + MR - 1) / MR; };
+  // A chain's row tile sees no tokens behind its last row's, and its list ends there.  Lists of
+  // trees are all as long as the last row tile's, and so are those of pieces short beside their
+  // context: alike, they divide evenly more often (16 pieces of 128 rows behind 1024 tokens: 67
+  // against 87 us; past an eighth the tokens nobody sees cost more).
+  auto even = [&](const AttReq& r) { return p.anc != nullptr || r.n <= (r.ctx + r.n) / 8; };
+  auto list = [&](const AttReq& r, int mt) -> int64_t {
+    const int end = even(r) ? r.ctx + r.n : att_end(p, r, (mt + 1) * MR);
+    return (end + kRound - 1) / kRound + kSetup;
   };
   auto units = [&](const AttReq& r) -> int64_t {
-    return r.n > 0 ? (int64_t)((r.n * p.G + MR - 1) / MR) * list(r) : 0;
+    const int n = tiles(r);
+    if (n < 2 || even(r)) return n * list(r, 0);
+    int64_t sum = 0;
+    for (int mt = 0; mt < n; ++mt) sum += list(r, mt);
+    return sum;
   };
   const int per = (p.R + kAttThreads - 1) / kAttThreads;
   const int lo = min(p.R, tid * per), hi = min(p.R, lo + per);
@@ -651,10 +673,13 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
         const AttReq r = q == lo ? mine0 : att_req(p, q, false);
         const int64_t x = units(r);
         if (w < at + x) {
+          int mt = 0;
+          for (int64_t len; w >= at + (len = list(r, mt)); ++mt) at += len;
           start_s[0] = q;
           start_s[1] = r.a;
           start_s[2] = r.n;
           start_s[3] = r.ctx;
+          start_s[4] = mt;
           start_off = w - at;
           break;
         }
@@ -665,15 +690,16 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
   __syncthreads();
   int q = uni(start_s[0]);
   AttReq rq = {uni(start_s[1]), uni(start_s[2]), uni(start_s[3])};
-  int64_t off = uni(start_off);  // units of q's lists before this workgroup's
+  int mt = uni(start_s[4]);
+  int64_t at = uni(start_off);  // units of the row tile's list before this workgroup's
 
   const uint32_t base = (uint32_t)uni((int)lds_addr(lds));
   AttWave<T, D, NR> wv(p, wave, base);
-  int64_t u = u0;  // the unit that `off` stands for
+  int64_t u = u0;
   bool first = true;
   while (true) {
-    if (off >= units(rq)) {  // on to the next request, or the next head
-      off -= units(rq);
+    if (mt >= tiles(rq)) {  // on to the next request, or the next head
+      mt = 0;
       if (++q == p.R) {
         q = 0;
         ++head;
@@ -683,15 +709,14 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
       rq = {uni(rq.a), uni(rq.n), uni(rq.ctx)};
       continue;
     }
-    const int64_t len = list(rq);
-    const int mt0 = (int)quotient(off, len);
-    const int64_t at = off - mt0 * len, s = u - at;  // the list's units are s .. s + len
+    const int64_t len = uni(list(rq, mt)), s = u - at;  // the list's units are s .. s + len
     int64_t from = first ? cut.snapped(at, len) : at;
     const int64_t to = u1 - s >= len ? len : (u1 - s <= 0 ? 0 : cut.snapped(u1 - s, len));
     first = false;
     if (to <= 0) break;
     u += len - at;
-    off += len - at;
+    at = 0;
+    const int mt0 = mt++;
     from = from > kSetup ? from - kSetup : 0;
     const int r0 = (int)from, nr = (int)(to - kSetup - from), rounds = (int)len - kSetup;
     if (nr <= 0) continue;
@@ -708,7 +733,7 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
       }
       const int mi = mt0 * MR + row;
       T* out = static_cast<T*>(p.o) +
-               ((int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G) * D + d;
+               ((int64_t)(rq.a + node_of(p, mi)) * p.Hq + head * p.G + group_of(p, mi)) * D + d;
       if constexpr (F::kBf) {
         bf16x4 zb;
 #pragma unroll
@@ -724,7 +749,7 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
         part[MR * D + row] = m;
         part[MR * (D + 1) + row] = l;
       } else if (p.lse) {
-        p.lse[(int64_t)(rq.a + mi / p.G) * p.Hq + head * p.G + mi % p.G] =
+        p.lse[(int64_t)(rq.a + node_of(p, mi)) * p.Hq + head * p.G + group_of(p, mi)] =
             (m + __builtin_amdgcn_logf(l)) * kLn2;
       }
     };
@@ -809,9 +834,10 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
 // DEEP: lists of many pieces, twelve loads in flight where few lists leave the chip to few
 // waves; otherwise four at most, in registers for twice the waves.
 template <class T, int D, int NR, bool DEEP>
-__global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
+__global__ void __launch_bounds__(256) attention_join_kernel(AttParams p, bool across) {
   constexpr int MR = kRows * NR, LP = D / 4, NP = kWave / LP;
-  const int b = blockIdx.x;
+  const int b = across ? blockIdx.y : blockIdx.x;
+  const int slice = across ? blockIdx.x : blockIdx.y, slices = across ? gridDim.x : gridDim.y;
   const AttJoint jt = p.joint[b];
   if (jt.count == 0) return;
   const int lane = threadIdx.x & 63;
@@ -820,7 +846,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
     return p.part + ((int64_t)(b - 1 + k) * 2 + (k == 0)) * MR * (D + 2);
   };
   const int rows = min(MR, jt.M - jt.tile * MR);
-  for (int row = blockIdx.y * 4 + (threadIdx.x >> 6); row < rows; row += 4 * gridDim.y) {
+  for (int row = slice * 4 + (threadIdx.x >> 6); row < rows; row += 4 * slices) {
     const int mi = jt.tile * MR + row;
     float m = -INFINITY, l = 0.0f;
     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -876,7 +902,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p) {
     }
     if (mine != 0) continue;
     acc *= l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = (int64_t)(jt.a + mi / p.G) * p.Hq + jt.head * p.G + mi % p.G;
+    const int64_t at = (int64_t)(jt.a + node_of(p, mi)) * p.Hq + jt.head * p.G + group_of(p, mi);
     T* out = static_cast<T*>(p.o) + at * D + d;
     if constexpr (std::is_same<T, uint16_t>::value) {
       bf16x4 z;
@@ -951,11 +977,16 @@ static int att_launch(const AttParams& p, hipStream_t stream) {
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
   const int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
-  const dim3 blocks(grid, slices);
+  // Workgroups go to the eight dies in turn.  The joints lie some workgroups apart, often all
+  // with the same remainder by 8 or two of them, so where there is much to read (112 row tiles
+  // of 128: 12 to 29 us) neighbours are the slices of one joint (13 us); where there is little,
+  // one die is as good (two requests of 5 rows: 8 against 11 us).
+  const bool across = slices >= 8;
+  const dim3 blocks = across ? dim3(slices, grid) : dim3(grid, slices);
   if (grid / p.R / p.Hkv >= 16)  // pieces of a list, were there one row tile a request
-    attention_join_kernel<T, D, NR, true><<<blocks, 256, 0, stream>>>(p);
+    attention_join_kernel<T, D, NR, true><<<blocks, 256, 0, stream>>>(p, across);
   else
-    attention_join_kernel<T, D, NR, false><<<blocks, 256, 0, stream>>>(p);
+    attention_join_kernel<T, D, NR, false><<<blocks, 256, 0, stream>>>(p, across);
   return launch_status();
 }
 
@@ -999,6 +1030,7 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
   p.Hq = Hq;
   p.Hkv = Hkv;
   p.G = Hq / Hkv;
+  p.inv_g = p.G > 1 ? ~(uint64_t)0 / p.G + 1 : 0;
   p.lg = log2_of(page_size);
   p.max_pages = max_pages;
   p.n_pages = n_pages;

@@ -263,3 +263,27 @@ def test_cache_beyond_32_bits():
             for i, src in ((1, 2), (2, 4), (3, 3), (0, 0)):
                 at = ctx + i
                 assert torch.equal(x[int(table[q, at // page]), :, at % page].cpu(), r[ctx + src])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ctx", [0, 75])
+def test_later_tokens_of_a_prompt_hold_anything(ctx, D, dtype):
+    """A prompt's tokens reach no row before them, in its own row tile or in another."""
+    import draft_sampling_scheduling_amd as ds
+    n, Hq = 300, 4
+    g = np.random.default_rng(ctx + D)
+    c = ref.Cache(ctx + D, [ctx], [n], 2, D, 16, dtype)
+    q = torch.from_numpy(g.standard_normal((n, Hq, D), np.float32)).to(dtype)
+    clean = [c.tokens(x, 0, ctx + n) for x in (c.k, c.v)]
+    w = ref.attention(q.double().numpy(), *clean, ctx, D ** -0.5, ref.sees(n, None))
+    tol, _ = ref.attention_tol(*w, ctx + n, D, dtype is BF)
+    for at, bad in ((299, float("nan")), (222, float("inf")), (190, float("nan")), (64, float("-inf"))):
+        t = ctx + at
+        for x in (c.k, c.v):
+            x[c.table[0, t // 16], :, t % 16] = bad
+        o = ds.tree_attention(q.to("cuda:0"), c.dev(c.k), c.dev(c.v),
+                              torch.from_numpy(c.table).to("cuda:0"), T([ctx]),
+                              T([0, n]))["o"].double().cpu().numpy()
+        assert (np.abs(o - w[0]) <= tol)[:at].all(), at
+        assert not np.isfinite(o[at]).any(), at
