@@ -275,21 +275,38 @@ struct AttWave {
   __device__ __forceinline__ void scores(uint32_t ks, f32x16& sc) const {
     const uint32_t krow = here(ks + n * L::RB), kx = here((uint32_t)(h ^ L::kswz(n)) << 4);
     sc = f32x16{};
+    // Eight reads under way before the first is used (the fence keeps them so): one takes longer
+    // than a product, and read one at a time 8192 rows take 789 us for 776.
+    constexpr int kBatch = 8;
 #pragma unroll
-    for (int st = 0; st < L::KSTEPS; ++st)
-      mfma_qk<T>(lds_get<u32x4>(krow + (kx ^ (uint32_t)(st << 5))), qf[st], sc);
+    for (int s0 = 0; s0 < L::KSTEPS; s0 += kBatch) {
+      constexpr int kN = L::KSTEPS < kBatch ? L::KSTEPS : kBatch;
+      u32x4 f[kN];
+#pragma unroll
+      for (int st = 0; st < kN; ++st) f[st] = lds_get<u32x4>(krow + (kx ^ (uint32_t)((s0 + st) << 5)));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int st = 0; st < kN; ++st) mfma_qk<T>(f[st], qf[s0 + st], sc);
+    }
   }
 
-  // scores of tokens that the lane's row does not see: -inf
+  // scores of tokens that the lane's row does not see: -inf (t0 + 32 > ctx, as of edge tiles)
   __device__ __forceinline__ void mask(int t0, f32x16& sc) const {
-    const bool tree = p.anc != nullptr;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int j = t0 + reg_row(r, h) - ctx;
-      const bool below = tree ? j <= 64 && ((see >> ((j - 1) & 63)) & 1) : j <= node;
-      const bool ok = (j <= 0 || below) && j < len - ctx;
-      sc[r] = ok ? sc[r] : -INFINITY;
+    const int j0 = t0 - ctx, left = len - t0;  // node of the tile's first token, tokens from it on
+    uint32_t vis;                              // tokens of the tile that the row sees
+    if (p.anc) {  // nodes from j0 on; below node 1 all are seen
+      if (j0 > 0)
+        vis = j0 <= 64 ? (uint32_t)(see >> (j0 - 1)) : 0;
+      else
+        vis = (uint32_t)see << 1 << -j0 | ((2u << -j0) - 1);
+    } else {
+      const int top = node - j0;
+      vis = top < 0 ? 0 : ~0u >> (top < 31 ? 31 - top : 0);
     }
+    if (left < 32) vis &= (1u << left) - 1;
+    vis >>= 4 * h;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) sc[r] = vis & (1u << reg_row(r, 0)) ? sc[r] : -INFINITY;
   }
 
   // the scores' weights, m, l and O's scale
@@ -332,24 +349,27 @@ struct AttWave {
       const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
       const uint32_t vrow = here(vs + r0 * L::RB + (j & 1) * 8);
       const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ L::vswz(r0)) << 4);
+      union {
+        s16x4 half[2];
+        bf16x8 all;
+      } a[2][ND];
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            a[st][dt].half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (DSPARK_LDS s16x4*)(uintptr_t)(vrow + (vx ^ (uint32_t)(dt << 6)) + 8 * (2 * st + b) * L::RB));
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         bf16x8 pb;
 #pragma unroll
         for (int e = 0; e < 8; ++e) pb[e] = (__bf16)sc[8 * st + e];
 #pragma unroll
-        for (int dt = 0; dt < ND; ++dt) {
-          union {
-            s16x4 half[2];
-            bf16x8 all;
-          } a;
-          const uint32_t at = vrow + (vx ^ (uint32_t)(dt << 6));
-#pragma unroll
-          for (int b = 0; b < 2; ++b)
-            a.half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (DSPARK_LDS s16x4*)(uintptr_t)(at + 8 * (2 * st + b) * L::RB));
-          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a.all, pb, o[dt], 0, 0, 0);
-        }
+        for (int dt = 0; dt < ND; ++dt)
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[st][dt].all, pb, o[dt], 0, 0, 0);
       }
     } else {
       // register r is token reg_row(r, h): the two halves' tokens are one step's pair
