@@ -156,6 +156,10 @@ struct Fit {
   static constexpr int WAVES = NR == 1 ? 2 : NR;
   static constexpr int THREADS = WAVES * kWave;
   static constexpr int ROUND = NR == 1 ? 2 * kTok : kTok;  // tokens of a round
+  // what a list costs beside its tokens, in rounds: 6 to 8 us, where a round of 64 tokens takes 3
+  // and one of 32 about 1 (at 3 there a prompt of 8192 rows took 750 us, at 6 704 and at 7
+  // 684; 64 trees 47.0, 46.1 and 47.4)
+  static constexpr int SETUP = NR == 1 ? 3 : 6;
   static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
   static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : 2;
   static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
@@ -598,23 +602,24 @@ struct AttWave {
   }
 };
 
-// Where the rounds of a head go.  Each row tile of each request has a list of kSetup + rounds
-// units, kSetup of them for what a list costs beside its tokens (the queries, the first
-// tile's wait, the merge of the waves; about 8 us where a round takes 3 us with all CUs
-// streaming), which no tokens stand for; all lists, head after head, are one row of
-// units, cut evenly: workgroup b begins at unit begin(b).  A cut costs the later piece's
-// set-up and the join, so short lists stay whole (39 against 43 us for 2112 lists of 3 to
-// 4 rounds of 64 tokens), but not where a share is hardly more than one (at shares of 9 units,
-// lists of 8 rounds kept whole cost 52 against 48 us); moving cuts of longer lists to a near
-// end lost more in balance than it saved in joins (105 against 117 us for 184 lists of 30).  A list that is cut has
-// its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
-constexpr int kSetup = 3, kWhole = 4;
+// Where the rounds of a head go.  Each row tile of each request has a list of SETUP + rounds
+// units, SETUP of them for what a list costs beside its tokens (the queries, the first
+// tile's wait, the merge of the waves, the output), which no tokens stand for; all lists, head
+// after head, are one row of units, cut evenly: workgroup b begins at unit begin(b).  A cut
+// costs the later piece's set-up and the join, so short lists stay whole (39 against 43 us for
+// 2112 lists of 3 to 4 rounds of 64 tokens), but not where a share is hardly more than one (at
+// shares of 9 units, lists of 8 rounds kept whole cost 52 against 48 us); moving cuts of longer
+// lists to a near end lost more in balance than it saved in joins (105 against 117 us for 184
+// lists of 30).  A list that is cut has its pieces in the workspace; the first workgroup that
+// begins inside one says so in joint[b].
+constexpr int kWhole = 4;
 
 // a / b, both at least 0; a 64-bit division is some hundred instructions
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+template <int SETUP>
 struct AttShares {
   int64_t share, more;  // units of a workgroup; the first `more` have one more
   int whole;            // rounds up to which a list stays whole
@@ -627,8 +632,8 @@ struct AttShares {
   }
   // where a cut at unit `at` of a list of len units falls
   __device__ __forceinline__ int64_t snapped(int64_t at, int64_t len) const {
-    if (len <= kSetup + whole) return 2 * at <= len ? 0 : len;
-    return at <= kSetup ? 0 : at;
+    if (len <= SETUP + whole) return 2 * at <= len ? 0 : len;
+    return at <= SETUP ? 0 : at;
   }
 };
 
@@ -636,7 +641,8 @@ template <class T, int D, int NR>
 __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_SIMD))
     attention_kernel(AttParams p) {
   using F = Fit<T, D, NR>;
-  constexpr int MR = kRows * NR, ND = D / 32, kRound = F::ROUND, kAttThreads = F::THREADS;
+  constexpr int MR = kRows * NR, ND = D / 32, kRound = F::ROUND, kAttThreads = F::THREADS,
+                kSetup = F::SETUP;
   extern __shared__ uint4 lds[];
   __shared__ int64_t sums[F::WAVES];
   __shared__ int64_t total_s, start_off;
@@ -654,13 +660,26 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
     const int end = even(r) ? r.ctx + r.n : att_end(p, r, (mt + 1) * MR);
     return (end + kRound - 1) / kRound + kSetup;
   };
-  auto units = [&](const AttReq& r) -> int64_t {
-    const int n = tiles(r);
-    if (n < 2 || even(r)) return n * list(r, 0);
-    int64_t sum = 0;
-    for (int mt = 0; mt < n; ++mt) sum += list(r, mt);
-    return sum;
+  // Units of the first mt lists.  kPeriod * G row tiles on, a chain's lists are kMore rounds
+  // longer, so a sum takes one period's lists at most.
+  constexpr int kPeriod = kRound > MR ? kRound / MR : 1, kMore = MR > kRound ? MR / kRound : 1;
+  auto before = [&](const AttReq& r, int mt) -> int64_t {
+    if (even(r)) return mt * list(r, 0);
+    const int n = tiles(r), inner = mt < n ? mt : n - 1;  // the last list ends with the rows
+    const int period = kPeriod * p.G, c = inner / period, rest = inner - c * period;
+    int64_t sum = 0, part = 0;
+    for (int k = 0; k < (c > 0 ? period : rest); ++k) {
+      const int64_t x = list(r, k);
+      sum += x;
+      part += k < rest ? x : 0;
+    }
+    if (c == 0)
+      sum = part;
+    else
+      sum = c * sum + part + kMore * (period * ((int64_t)c * (c - 1) / 2) + (int64_t)rest * c);
+    return mt < n ? sum : sum + list(r, n - 1);
   };
+  auto units = [&](const AttReq& r) -> int64_t { return r.n > 0 ? before(r, tiles(r)) : 0; };
   const int per = (p.R + kAttThreads - 1) / kAttThreads;
   const int lo = min(p.R, tid * per), hi = min(p.R, lo + per);
   int64_t mine = 0;
@@ -677,7 +696,7 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
   const int64_t W = uni(total_s), U = W * p.Hkv;
   const int64_t P = U < gridDim.x ? U : gridDim.x;
   if (b >= P) return;
-  AttShares cut;
+  AttShares<kSetup> cut;
   cut.share = quotient(U, P);
   cut.more = U - cut.share * P;
   // kWhole rounds, and up to 256 tokens where a share is several such lists
@@ -693,8 +712,15 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
         const AttReq r = q == lo ? mine0 : att_req(p, q, false);
         const int64_t x = units(r);
         if (w < at + x) {
-          int mt = 0;
-          for (int64_t len; w >= at + (len = list(r, mt)); ++mt) at += len;
+          int mt = 0, end = tiles(r);  // the last list that begins at or before w
+          while (end - mt > 1) {
+            const int mid = mt + (end - mt) / 2;
+            if (at + before(r, mid) <= w)
+              mt = mid;
+            else
+              end = mid;
+          }
+          at += before(r, mt);
           start_s[0] = q;
           start_s[1] = r.a;
           start_s[2] = r.n;
