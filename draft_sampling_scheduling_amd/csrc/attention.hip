@@ -258,20 +258,25 @@ struct AttWave {
     if (bad && lane == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
   }
   // The copies of the wave's rows of tile t0's K or V into stage s.  Rows past the last token
-  // read inside its page, and are never used.
+  // read inside its page, and are never used.  Scalar work is serial in a wave, so the 8 rows
+  // of a group, which lie in one page, share an offset.
   template <bool V>
   __device__ __forceinline__ void copy(int t0, const int (&pg)[CG], int s) const {
     const int lr = lane / L::CPR, pos = lane % L::CPR;
-    const uint32_t row = (uint32_t)(lr * (int)p.tok_b);
+    const uint32_t tok_b = (uint32_t)p.tok_b, row = (uint32_t)lr * tok_b;
     const uint32_t to = base + s * F::TILE + V * L::BYTES + mine * L::RB;
     const int in_page = (1 << p.lg) - 1;
     const int xl = V ? L::vswz(lr) ^ L::vswz(mine) : L::kswz(lr) ^ L::kswz(mine);
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t off = pg[(c * L::RPC) >> 3] * p.page_b +
-                          (int64_t)((t0 + mine + c * L::RPC) & in_page) * p.tok_b;
-      const int x = xl ^ (V ? L::vswz(c * L::RPC) : L::kswz(c * L::RPC));
-      dma16s((V ? vh : kh) + off, row + (uint32_t)((pos ^ x) << 4), to + c * 1024);
+    for (int g = 0; g < CG; ++g) {
+      const char* rows = (V ? vh : kh) + (uint64_t)(uint32_t)pg[g] * (uint64_t)p.page_b +
+                         (uint64_t)(uint32_t)((t0 + mine + 8 * g) & in_page) * tok_b;
+#pragma unroll
+      for (int i = 0; i < 8; i += L::RPC) {
+        const int c = (8 * g + i) / L::RPC;
+        const int x = xl ^ (V ? L::vswz(8 * g + i) : L::kswz(8 * g + i));
+        dma16s(rows + (uint32_t)i * tok_b, row + (uint32_t)((pos ^ x) << 4), to + c * 1024);
+      }
     }
   }
 
