@@ -22,9 +22,11 @@
 //     request fills the chip.  A piece of a row tile's list that is not all of it goes to
 //     the workspace, and a second kernel joins the pieces in order.
 // Measured, bf16, D = 128, both kernels: 256 requests of 512 to 4096 tokens, 32 heads on 8, up to
-// nine rows (2.44 GB) 450 us, 5.4 TB/s where a kernel that only reads gets 5.7; two single
-// tokens over 100001 to 131071, 40 heads on 8 (0.95 GB) 161 to 176 us; 64 trees over 100 to
-// 2048, 20 heads on 4 (145 MB) 48 us, of which 29 us are the bytes at a copy's rate.
+// nine rows (2.44 GB) 446 us, 5.5 TB/s where a kernel that only reads gets 5.7; two single
+// tokens over 100001 to 131071, 40 heads on 8 (0.95 GB) 161 to 180 us; 64 trees over 100 to
+// 2048, 20 heads on 4 (145 MB) 47 us, of which 29 us are the bytes at a copy's rate.  Prompts are
+// bound by the softmax's vector work, which takes as long as the products and overlaps them in
+// part: 8192 rows, 32 heads on 8, 688 us, 800 TFLOP/s of the pairs seen.
 #include <type_traits>
 
 #include "sweep.h"
@@ -57,6 +59,7 @@ struct AttParams {
   const int32_t *table, *ctx, *row_off;
   const uint64_t* anc;
   float scale;
+  int whole;  // rounds of a list up to which it is not cut
   void* o;
   float* lse;
   int32_t* status;
@@ -146,8 +149,8 @@ struct Tile {
 //   are taken, V's as soon as O is: half the LDS, twice the workgroups.
 //   NR 2 or 4, up to 64 or 128 rows: every wave has 32 rows of its own, and all share each
 //   tile of 32 tokens, copied one ahead by all of them, with a barrier per tile; the cache is
-//   read once for all rows.  More stages made four waves slower (196 against 187 us for 128
-//   rows), and two with fewer workgroups in their place (50 to 53 against 48 us for 64 trees).
+//   read once for all rows.  A third stage made them slower (453 against 440 us for
+//   256 requests of 512 to 4096 tokens).
 //   PER_CU workgroups are resident; where registers allow two waves a SIMD, one's set-up,
 //   exponentials and merge hide behind the other's tiles.
 template <class T, int D, int NR>
@@ -596,7 +599,11 @@ struct AttWave {
       if (live) {
         scores(ks, sc);
         if (t0 + kTok > seen) mask(t0, sc);
+        // the exponentials first: the SIMD's other wave has products to issue meanwhile (4096 rows
+        // at D = 64: 164 without, 158 us; 8192 at D = 128: 697, 688)
+        __builtin_amdgcn_s_setprio(1);
         weigh(sc);
+        __builtin_amdgcn_s_setprio(0);
       }
       if (t0 + kTok > seen && clean_values(t0, vs)) odd_values(ks, vs, sc);
       if (live) values(vs, sc);
@@ -611,12 +618,12 @@ struct AttWave {
 // units, SETUP of them for what a list costs beside its tokens (the queries, the first
 // tile's wait, the merge of the waves, the output), which no tokens stand for; all lists, head
 // after head, are one row of units, cut evenly: workgroup b begins at unit begin(b).  A cut
-// costs the later piece's set-up and the join, so short lists stay whole (39 against 43 us for
-// 2112 lists of 3 to 4 rounds of 64 tokens), but not where a share is hardly more than one (at
-// shares of 9 units, lists of 8 rounds kept whole cost 52 against 48 us); moving cuts of longer
-// lists to a near end lost more in balance than it saved in joins (105 against 117 us for 184
-// lists of 30).  A list that is cut has its pieces in the workspace; the first workgroup that
-// begins inside one says so in joint[b].
+// costs the later piece's set-up and the join; moving cuts to a near end lost more in balance
+// than it saved in joins (120 requests of 180 to 254 tokens, lists of 6 to 8 rounds: 32 us with
+// these kept whole, 27 cut), unless no list need be cut at all: block tables of no more than
+// kWhole rounds leave every list whole and launch no join (4 requests of up to 204 tokens, float:
+// 17 against 19 us).  A list that is cut has its pieces
+// in the workspace; the first workgroup that begins inside one says so in joint[b].
 constexpr int kWhole = 4;
 
 // a / b, both at least 0; a 64-bit division is some hundred instructions
@@ -627,7 +634,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 template <int SETUP>
 struct AttShares {
   int64_t share, more;  // units of a workgroup; the first `more` have one more
-  int whole;            // rounds up to which a list stays whole
+  int whole;            // lists of so many rounds stay whole
   __device__ __forceinline__ int64_t begin(int64_t b) const {
     return b * share + (b < more ? b : more);
   }
@@ -704,9 +711,7 @@ __global__ void __launch_bounds__((Fit<T, D, NR>::THREADS), (Fit<T, D, NR>::PER_
   AttShares<kSetup> cut;
   cut.share = quotient(U, P);
   cut.more = U - cut.share * P;
-  // kWhole rounds, and up to 256 tokens where a share is several such lists
-  constexpr int kMost = 256 / kRound > kWhole ? 256 / kRound : kWhole;
-  cut.whole = cut.share >= 2 * kMost ? kMost : (cut.share >= 2 * kWhole ? (int)cut.share / 2 : kWhole);
+  cut.whole = p.whole;
   const int64_t u0 = cut.begin(b), u1 = cut.begin(b + 1);
   int head = (int)quotient(u0, W);
   {
@@ -981,13 +986,13 @@ struct Variant {
 // f(variant) of the variant that runs these shapes: as many waves over query rows as a
 // request's rows (rows / R, the bound the host knows, times heads to a cache head) fill, so
 // that the cache is read once for all of them.  33 to 64 rows at D = 128 run four waves too,
-// two of them only copying: half the workgroups cut half the lists (430 against 442 us for 256
-// requests of 512 to 4096 tokens, 29 against 36 us for one of 16000, 153 against 161 us for
-// 64 of 500 to 4000; 49 against 47 us for 64 of 100 to 2048); at D = 64, with half the bytes
-// under way, that costs more than it saves (90 against 77 us).  Float has only the first
+// two of them only copying: half the workgroups cut half the lists (440 against 453 us for 256
+// requests of 512 to 4096 tokens, 26 against 33 us for one of 16000, 149 against 158 us for
+// 64 of 500 to 4000, 46 us both for 64 of 100 to 2048); at D = 64, with half the bytes
+// under way, that costs more than it saves (89 against 77 us).  Float has only the first
 // variant: its products, sixteen times as slow, bound it, and rows that are not there cost it
-// as much as others (22 requests of up to 56 rows: 180 us so, 212 us with two waves over
-// rows; 16 of 128 rows: 144 against 123 us).
+// as much as others (22 requests of up to 56 rows: 169 us so, 214 us with two waves over
+// rows; 16 of 128 rows: 137 against 131 us).
 template <class F>
 static auto att_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
   if (dt == DSPARK_F32) return D == 64 ? f(Variant<float, 64, 1>{}) : f(Variant<float, 128, 1>{});
@@ -1016,15 +1021,15 @@ static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt
 }
 
 template <class T, int D, int NR>
-static int att_launch(const AttParams& p, hipStream_t stream) {
+static int att_launch(AttParams p, hipStream_t stream) {
   using F = Fit<T, D, NR>;
   static std::atomic<uint64_t> raised;
   auto kern = attention_kernel<T, D, NR>;
   const int grid = Variant<T, D, NR>::grid();
   ensure_dynamic_lds(reinterpret_cast<const void*>(kern), F::LDS, raised);
+  p.whole = ((int64_t)p.max_pages << p.lg) <= kWhole * F::ROUND ? kWhole : 0;
   kern<<<grid, F::THREADS, F::LDS, stream>>>(p);
-  // where no request can have more than kWhole rounds, no list is cut
-  if (((int64_t)p.max_pages << p.lg) <= kWhole * F::ROUND) return launch_status();
+  if (p.whole > 0) return launch_status();
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
   const int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
