@@ -159,10 +159,10 @@ struct Fit {
   static constexpr int WAVES = NR == 1 ? 2 : NR;
   static constexpr int THREADS = WAVES * kWave;
   static constexpr int ROUND = NR == 1 ? 2 * kTok : kTok;  // tokens of a round
-  // what a list costs beside its tokens, in rounds: 6 to 8 us, where a round of 64 tokens takes 3
-  // and one of 32 about 1 (at 3 there a prompt of 8192 rows took 750 us, at 6 704 and at 7
-  // 684; 64 trees 47.0, 46.1 and 47.4)
-  static constexpr int SETUP = NR == 1 ? 3 : 6;
+  // what a list costs beside its tokens, in rounds: 6 to 8 us, where a round of 64 tokens takes 3,
+  // of float ones more (at 3 there 16 requests of 128 rows took 136 us, at 2 133), and one of 32
+  // about 1 (at 3 a prompt of 8192 rows took 750 us, at 6 704)
+  static constexpr int SETUP = NR > 1 ? 6 : (kBf ? 3 : 2);
   static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
   static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : 2;
   static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
