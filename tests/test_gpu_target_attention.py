@@ -287,3 +287,14 @@ def test_later_tokens_of_a_prompt_hold_anything(ctx, D, dtype):
                               T([0, n]))["o"].double().cpu().numpy()
         assert (np.abs(o - w[0]) <= tol)[:at].all(), at
         assert not np.isfinite(o[at]).any(), at
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 5, 7, 16])
+@pytest.mark.parametrize("ctx,n", [([0], [700]), ([13, 0, 90], [333, 2, 450]),
+                                   ([0] * 12, [330] + [1] * 11)], ids=["one", "three", "mixed"])
+def test_prompts_of_many_row_tiles(ctx, n, G, dtype):
+    """Row tiles that see more and more tokens, in every split of the waves: many rows a request on
+    average, and few with one prompt among them."""
+    check(G + len(n), ctx, n, 2 * G, 2, 64, 16, dtype)
+    check(G + len(n), ctx, n, G, 1, 128, 32, dtype)

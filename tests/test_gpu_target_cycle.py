@@ -377,3 +377,44 @@ def test_workspaces_given():
         ds.cache_append(k, v, *s.cache, p["slot"], n_rows=p["row_off"][-1:])
         a = ds.tree_attention(q, *s.cache, s.state[1], s.ctx, p["row_off"], anc=p["anc"], ws=ws)
         assert torch.equal(a["o"][:live].view(torch.int16), want[3][:live])
+
+
+def test_a_step_that_cannot_serve_everybody():
+    """Pages for two of three requests: the third gets no rows, nothing of it is written, and it
+    goes on as it was once committed with n_acc = -1; then there are pages again."""
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V, H, D, page = 3, 2, 64, 2, 64, 8
+    ctx, held, ell = T([7, 7, 7]), T([1, 1, 1]), T([2, 2, 2])
+    table, free, n_free = T([[0, -1], [1, -1], [2, -1]]), T([5, 4, 3]), T([2])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    kc, vc = (torch.randn(6, H, page, D, device="cuda:0", generator=g) for _ in range(2))
+    q, k, v = (torch.randn(9, H, D, device="cuda:0", generator=g) for _ in range(3))
+    x = T([[1, 2], [3, 4], [5, 6]])
+
+    def step(rows):
+        st = T([0])
+        p = ds.cache_plan(ell, ctx, held, table, free, n_free, page, rows=9, extra=1, status=st)
+        plan_status = int(st)
+        before = kc[2].clone()
+        n_rows = p["row_off"][-1:]
+        assert int(n_rows) == rows
+        ds.cache_append(k, v, kc, vc, p["slot"], n_rows=n_rows, status=st)
+        a = dict(o=torch.full((9, H, D), 9.0, device="cuda:0"), lse=torch.full((9, H), 9.0, device="cuda:0"))
+        ds.tree_attention(q, kc, vc, table, ctx, p["row_off"], out=a, status=st)
+        assert int(st) == plan_status
+        assert torch.isfinite(a["o"]).all() and torch.all(a["o"][rows:] == 9)
+        out = ds.target_logits(torch.randn(9, V, device="cuda:0"), ell, x, row_off=p["row_off"],
+                               out=torch.full((R, gamma + 1, V), 9.0, device="cuda:0"), status=st)
+        return plan_status, int(st), out, torch.equal(before, kc[2])
+
+    plan_status, status, out, same = step(6)
+    assert plan_status == ds.FAULT_PAGE and status == ds.FAULT_PAGE | 4 and same
+    assert torch.all(out[2] == 9) and not (out[:2] == 9).any()
+    assert held.tolist() == [2, 2, 1] and table.tolist() == [[0, 4], [1, 5], [2, -1]] and int(n_free) == 0
+    st = T([0])
+    ctx = ds.cache_commit(T([1, 2, -1]), ctx, held, table, free, n_free, page, done=T([0, 1, 0]), status=st)
+    assert int(st) == 0 and ctx.tolist() == [9, 0, 7] and held.tolist() == [2, 0, 1] and int(n_free) == 2
+    ell = T([2, 0, 2])
+    plan_status, status, out, same = step(7)
+    assert (plan_status, status, same) == (0, 0, False) and not (out[2] == 9).any()
+    assert held.tolist() == [2, 1, 2]
