@@ -112,6 +112,13 @@ def test_parts_left_out(drop):
           n_mask=0 if drop in ("mask", "all") else 5)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_many_requests(dtype):
+    """Enough slices that a workgroup walks all rows of its request."""
+    check(12, 130, 3, 8200, dtype)
+    check(13, 600, 2, 264, dtype, packed=False, in_place=True)
+
+
 def test_headline_vocabulary():
     check(8, 3, 8, 151936, BF, n_hist=2000, nb=20)
 
