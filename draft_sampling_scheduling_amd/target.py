@@ -55,9 +55,12 @@ def set_argtypes(L):
 # checks and calls (a decode step makes many of them, so the passing case costs little: about
 # 0.4 us a tensor; what is wrong with one is found out only once something is)
 # ----------------------------------------------------------------------------------------
-try:
+try:  # (there are device tensors by then, so the device's state exists)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream
+    from torch._C import _cuda_getDevice as _current_device
 except ImportError:
+    _current_device = torch.cuda.current_device
+
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
@@ -177,28 +180,31 @@ def _call(dev, name, *args):
     """The library's `name`(*args, stream) on `dev`; raises on a refusal."""
     f = _fn(name)
     index = dev.index
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         rc = f(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
             rc = f(*args, _raw_stream(index))
     if rc != 0:
-        from . import DsparkError
+        from . import EWORKSPACE, DsparkError
+        if rc == EWORKSPACE:
+            raise ValueError("workspace too small")
         raise DsparkError(name, rc)
 
 
-def _workspace(nbytes, dev, ws):
-    if ws is None:
-        if nbytes == 0:
-            return None, None, 0
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        return ws, ws.data_ptr(), nbytes
+def _workspace(nbytes, dev):
+    """A workspace of its own for one call."""
+    if nbytes == 0:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _given(ws, dev):
+    """The caller's workspace (the library looks at its size)."""
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {dev}")
-    have = ws.numel() * ws.element_size()
-    if have < nbytes:
-        raise ValueError("workspace too small")
-    return ws, ws.data_ptr(), have
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def cache_plan_workspace_bytes(R, rows, width=0) -> int:
@@ -239,7 +245,10 @@ def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, e
     if R == 0:
         out["row_off"].zero_()
         return out
-    ws, wp, wb = _workspace(cache_plan_workspace_bytes(R, rows, width), dev, ws)
+    if ws is None:
+        ws, wp, wb = _workspace(cache_plan_workspace_bytes(R, rows, width), dev)
+    else:
+        ws, wp, wb = _given(ws, dev)
     _call(dev, "dspark_cache_plan", R, rows, page_size, W, F, extra, *a, width, *b, wp, wb)
     return out
 
@@ -287,15 +296,18 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
          _opt(status, "status", dev, (1,), _I32)]
     if R == 0 or rows == 0:
         return out
-    if torch.cuda.current_device() == dev.index:
-        nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
-    else:  # the size goes by the device's compute units
-        with torch.cuda.device(dev):
+    if ws is None:
+        if _current_device() == dev.index:
             nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
-    if nbytes == 0:
-        from . import EINVAL, DsparkError
-        raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
-    ws, wp, wb = _workspace(nbytes, dev, ws)
+        else:  # the size goes by the device's compute units
+            with torch.cuda.device(dev):
+                nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
+        if nbytes == 0:
+            from . import EINVAL, DsparkError
+            raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
+        ws, wp, wb = _workspace(nbytes, dev)
+    else:
+        ws, wp, wb = _given(ws, dev)
     _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st,
           *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
     return out
@@ -396,7 +408,10 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     sp = _opt(status, "status", dev, (1,), _I32)
     if R == 0:
         return out
-    ws, wp, wb = _workspace(
-        cache_commit_workspace_bytes(R, W, path is not None and a[3] == b[0]), dev, ws)
+    if ws is None:
+        ws, wp, wb = _workspace(
+            cache_commit_workspace_bytes(R, W, path is not None and a[3] == b[0]), dev)
+    else:
+        ws, wp, wb = _given(ws, dev)
     _call(dev, "dspark_cache_commit", R, gamma, page_size, W, F, *a, *b, *c, sp, wp, wb)
     return out

@@ -340,3 +340,25 @@ def test_commit_faults():
 def test_commit_pages_past_the_pool_and_the_list():
     assert run_commit(4, 10, 6, 8, 60, 1, 2, 64, torch.bfloat16, True, P_known=20)[4] & 8
     assert run_commit(5, 10, 6, 8, 60, 1, 2, 64, torch.bfloat16, False, free_len=5)[4] & 8
+
+
+def test_workspaces_of_the_callers():
+    """Too small, elsewhere or strided: refused before anything is enqueued."""
+    import draft_sampling_scheduling_amd as ds
+    R, W = 2000, 4
+    one, zero = T([1] * R), T([0] * R)
+    need = ds.cache_plan_workspace_bytes(R, R)
+    assert need > 16 and ds.cache_commit_workspace_bytes(R, W) > 16
+    for ws, why in ((torch.empty(16, dtype=torch.uint8, device="cuda:0"), "too small"),
+                    (torch.empty(need, dtype=torch.uint8), "on cuda"),
+                    (torch.empty(2 * need, dtype=torch.uint8, device="cuda:0")[::2], "contiguous")):
+        table, held, nf = T([[7] * W] * R), T([0] * R), T([R])
+        free = T(list(range(R)))
+        with pytest.raises(ValueError, match=why):
+            ds.cache_plan(one, zero, held, table, free, nf, 16, rows=R, ws=ws)
+        with pytest.raises(ValueError, match=why):
+            ds.cache_commit(zero, one, held, table, free, nf, 16, done=one, ws=ws)
+        assert int(nf) == R and int(held.sum()) == 0 and torch.all(table == 7)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda:0")
+    p = ds.cache_plan(one, zero, held, table, free, nf, 16, rows=R, ws=ws)
+    assert int(p["row_off"][-1]) == R and int(nf) == 0
