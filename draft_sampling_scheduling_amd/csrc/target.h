@@ -8,16 +8,31 @@
 
 namespace dspark {
 
+// 64-bit inclusive scan over a wave, in registers: within rows of 16 lanes, then each row's last
+// lane onto the rows behind it (with shuffles, which go through LDS, a plan of 512 trees takes 10.6
+// us for 9.8).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t moved(int64_t v) {  // lanes that nothing moves to: 0
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xf, false);
+  return (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {
+  v += moved<0x111, 0xf>(v);  // from 1, 2, 4, 8 lanes before, in the row
+  v += moved<0x112, 0xf>(v);
+  v += moved<0x114, 0xf>(v);
+  v += moved<0x118, 0xf>(v);
+  v += moved<0x142, 0xa>(v);  // lane 15 onto row 1, 47 onto row 3
+  v += moved<0x143, 0xc>(v);  // lane 31 onto rows 2 and 3
+  return v;
+}
+
 // 64-bit inclusive scan over the whole workgroup (NT threads, a multiple of 64, every thread
 // calls); `sums` is LDS of NT / 64 entries, free again after the call's last barrier.
 template <int NT>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int64_t u = __shfl_up(v, o, kWave);
-    if (lane >= o) v += u;
-  }
+  v = wave_scan(v);
   if (lane == kWave - 1) sums[wave] = v;
   __syncthreads();
   int64_t base = 0;
@@ -33,14 +48,8 @@ __device__ __forceinline__ void block_scan2(int64_t& a, int64_t& b, int64_t& all
                                             int64_t* sums) {
   constexpr int NW = NT / kWave;
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
-#pragma unroll
-  for (int o = 1; o < kWave; o <<= 1) {
-    const int64_t u = __shfl_up(a, o, kWave), v = __shfl_up(b, o, kWave);
-    if (lane >= o) {
-      a += u;
-      b += v;
-    }
-  }
+  a = wave_scan(a);
+  b = wave_scan(b);
   if (lane == kWave - 1) {
     sums[wave] = a;
     sums[NW + wave] = b;
