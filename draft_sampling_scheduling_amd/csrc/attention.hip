@@ -24,7 +24,7 @@
 // Measured, bf16, D = 128, both kernels: 256 requests of 512 to 4096 tokens, 32 heads on 8, up to
 // nine rows (2.44 GB) 446 us, 5.5 TB/s where a kernel that only reads gets 5.7; two single
 // tokens over 100001 to 131071, 40 heads on 8 (0.95 GB) 161 to 180 us; 64 trees over 100 to
-// 2048, 20 heads on 4 (145 MB) 43 us, of which 29 us are the bytes at a copy's rate.  Prompts are
+// 2048, 20 heads on 4 (145 MB) 42 to 45 us, of which 29 us are the bytes at a copy's rate.  Prompts are
 // bound by the softmax's vector work, which takes as long as the products and overlaps them in
 // part: 8192 rows, 32 heads on 8, 677 to 700 us, 800 TFLOP/s of the pairs seen.
 #include <type_traits>
