@@ -20,7 +20,7 @@ F32, BF16 = 0, 1
 SYNC_BREAK, GLOBAL, ASYNC_LAG2 = 0, 1, 2
 FIXED, THRESHOLD = 3, 4  # decode-driver length policies beyond the scheduler's modes
 OK, EINVAL, ERANGE, EWORKSPACE, EDEVICE = 0, -1, -2, -3, -4
-FAULT_TOKEN, FAULT_CONF, FAULT_LEN = 1, 2, 4
+FAULT_TOKEN, FAULT_CONF, FAULT_LEN, FAULT_EMPTY = 1, 2, 4, 64
 EXPORTS = ("dspark_draft_workspace_bytes", "dspark_draft_markov", "dspark_draft_markov_timed",
            "dspark_draft_markov_noalloc_max_bytes", "dspark_draft_markov_noalloc",
            "dspark_draft_parallel",
@@ -367,7 +367,9 @@ def verify(target, U, W2t, bias_rows, x, lse, logit_x, ell, seed=0, cycle=0, *, 
            ws=None, status=None):
     """Verification; returns dict(n_acc, y, c_star, x_next) (device tensors).  x_next [R]
     holds y[q][n_acc[q]], the next cycle's anchors; a caller's `out` may map it to the tensor
-    the next draft call takes as x0 (or leave it out: then it is not written)."""
+    the next draft call takes as x0 (or leave it out: then it is not written).  Where the last
+    token's target row is -inf throughout (a grammar mask that allows nothing), -1 stands in
+    its place and FAULT_EMPTY is set."""
     torch = _torch()
     _chk(U, "U")
     R, gamma, V = U.shape

@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(64) verify_decide_kernel(
   // independent; the best (G, block) with ties to the lowest block; the bonus row's winner
   const int tiles = lse_witems(V);
   float lset_j = 0.0f;
+  bool no_bonus = false;
   for (int jj = j; jj <= L + 1; jj += kWave) {
     const int i = ws.offA[q] + jj - 1;
     float M = -INFINITY, S = 0.0f, G = -INFINITY;
@@ -390,10 +391,15 @@ __global__ void __launch_bounds__(64) verify_decide_kernel(
         }
       }
     }
-    const float ls = M + __logf(S);
+    // a row without a logit above -inf has no distribution: with a normaliser of +inf, p is 0
+    // at every id of it in all that follows
+    const float ls = M == -INFINITY ? INFINITY : M + __logf(S);
     ws.lset[i] = ls;
     if (jj == j) lset_j = ls;
-    if (jj == L + 1) ws.bonus[q] = make_float2(G, __int_as_float(Bk));
+    if (jj == L + 1) {
+      ws.bonus[q] = make_float2(G, __int_as_float(Bk));
+      no_bonus = ls == INFINITY;
+    }
   }
   bool reject = false;
   if (j <= L) {
@@ -405,6 +411,7 @@ __global__ void __launch_bounds__(64) verify_decide_kernel(
   const int js = rm ? __ffsll(rm) : 0;
   const int na = js ? js - 1 : L;
   if (bad && j <= (js ? js : L)) raise_fault(status, DSPARK_FAULT_TOKEN);
+  if (js ? j == js && lset_j == INFINITY : no_bonus) raise_fault(status, DSPARK_FAULT_EMPTY);
   if (lane == 0) {
     ws.jstar[q] = js;
     n_acc[q] = na;
@@ -620,9 +627,10 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
   const int L = clamp_len(ell[q], gamma);
   const int nblocks = (V + kVB - 1) / kVB;
   const int js = ws.jstar[q];
-  const size_t offB = (size_t)ws.offB[q];
+  const size_t offA = (size_t)ws.offA[q], offB = (size_t)ws.offB[q];
 
-  // c* = 1 - 1/2 sum |p - q| for every verified row (eq. (8)); NaN past the scheduled length
+  // c* = 1 - 1/2 sum |p - q| for every verified row (eq. (8)), 0 where p has no distribution;
+  // NaN past the scheduled length
   for (int j0 = 1; j0 <= gamma; j0 += kJ) {
     float sum[kJ];
     // every range of the kJ rows at once (unconditional loads of clamped addresses, so
@@ -640,6 +648,8 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
 #pragma unroll
       for (int u = 0; u < kJ; ++u) sum[u] += (j0 + u <= L && i < nranges) ? v[u] : 0.0f;
     }
+    const bool mine = tid < kJ && j0 + tid <= L;
+    const float norm = mine ? ws.lset[offA + j0 + tid - 1] : 0.0f;
 #pragma unroll
     for (int u = 0; u < kJ; ++u) {
       const float t = wave_sum(sum[u]);
@@ -651,11 +661,13 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) t += tvs[w][tid];
       c_star[(size_t)q * gamma + (j0 + tid - 1)] =
-          (j0 + tid <= L) ? 1.0f - 0.5f * t : __int_as_float(0x7fc00000);
+          mine ? (norm == INFINITY ? 0.0f : 1.0f - 0.5f * t) : __int_as_float(0x7fc00000);
     }
     __syncthreads();
   }
 
+  const int jrow = js > 0 ? js : L + 1;  // target row of the draw
+  const float lp = ws.lset[offA + jrow - 1];
   const Rng rng(seed, cycle);
   // the block the token is drawn from: the residual's winning block at the first rejected
   // row, or the bonus row's
@@ -698,7 +710,6 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
   }
   const bool resid_ok = js > 0 && mass > 0.0f && Bk >= 0 && Bk < nblocks;
   if (Bk < 0 || Bk >= nblocks) Bk = 0;
-  const int jrow = js > 0 ? js : L + 1;  // target row of the draw
   const T* trow = target + ((size_t)q * (gamma + 1) + (jrow - 1)) * V;
   const int v = Bk * kVB + lane;
 
@@ -728,10 +739,12 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
   }
   if (wave != 0) return;
   int token;
-  if (js > 0) {
+  if (lp == INFINITY) {
+    token = -1;  // nothing to draw: the request ends here
+  } else if (js > 0) {
     if (resid_ok) {
       const size_t rj = (size_t)q * gamma + (js - 1);
-      const float lq = lse[rj], lp = ws.lset[ws.offA[q] + js - 1];
+      const float lq = lse[rj];
       float score = -INFINITY;
       if (v < V) {
         float acc = 0.0f;

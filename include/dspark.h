@@ -71,8 +71,13 @@ enum {
   DSPARK_EDEVICE = -4
 };
 
-/* bits OR-ed into *dev_status */
-enum { DSPARK_FAULT_TOKEN = 1, DSPARK_FAULT_CONF = 2, DSPARK_FAULT_LEN = 4 };
+/* bits OR-ed into *dev_status (8, 16 and 32 are dspark_target.h's) */
+enum {
+  DSPARK_FAULT_TOKEN = 1,
+  DSPARK_FAULT_CONF = 2,
+  DSPARK_FAULT_LEN = 4,
+  DSPARK_FAULT_EMPTY = 64 /* a target row without a logit above -inf (dspark_verify) */
+};
 
 /* ------------------------------------------------------------------------------------
  * W2 re-layout (digest, Module B eq. (5): the Markov head's bias is W1[x] W2 with
@@ -250,6 +255,10 @@ int dspark_schedule(int R, int gamma, const float *c, const float *c_lag, int R_
  * If some j* <= L is rejected: emit x_1..x_{j*-1}, then a two-level Gumbel sample of
  *   max(0, p_j* - q_j*) (streams 3, 4; if that mass is 0 in floating point, of p_j*).
  * Otherwise: emit x_1..x_L, then a sample of target row L+1 (the bonus; streams 5, 6).
+ * A target row whose logits are all -inf (a grammar mask that allows nothing) has p = 0 at
+ *   every id: its drafted token is rejected, its c_star is 0, and where it is the row to draw
+ *   the last token from, -1 is emitted in that token's place (y[q][n_acc[q]] and x_next[q]: the
+ *   request can go no further) and DSPARK_FAULT_EMPTY is set; all other outputs hold as ever.
  * Inputs
  *   target [R][gamma+1][V] dt   target logits for positions 1..gamma+1
  *   U [R][gamma][V] dt, W2t [V][r] dt      as in draft

@@ -152,7 +152,8 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  *   -1 none (mask_idx NULL: mask q * (gamma + 1) + j).
  * out may be logits itself where row_off is NULL and row_stride is V, and overlaps it in no
  * other way.
- * A row whose mask allows nothing is all -inf.
+ * A row whose mask allows nothing is all -inf (dspark_verify rejects the token drafted there,
+ *   emits -1 where it had to draw from that row, and sets DSPARK_FAULT_EMPTY).
  * Faults: ell outside [0, gamma] (DSPARK_FAULT_LEN, clamped); a row that is
  *   not the request's or outside [0, rows) (DSPARK_FAULT_LEN, its out row is left as it was:
  *   what becomes of requests that the plan gave no rows); hist_len outside [0, hist_stride],
