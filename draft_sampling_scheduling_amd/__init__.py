@@ -363,13 +363,15 @@ def verify_workspace_bytes(R, gamma, V, r) -> int:
     return int(lib().dspark_verify_workspace_bytes(R, gamma, V, r))
 
 
-def verify(target, U, W2t, bias_rows, x, lse, logit_x, ell, seed=0, cycle=0, *, out=None,
-           ws=None, status=None):
+def verify(target, U, W2t, bias_rows, x, lse, logit_x, ell, seed=0, cycle=0, *, row_off=None,
+           x0=None, out=None, ws=None, status=None):
     """Verification; returns dict(n_acc, y, c_star, x_next) (device tensors).  x_next [R]
     holds y[q][n_acc[q]], the next cycle's anchors; a caller's `out` may map it to the tensor
     the next draft call takes as x0 (or leave it out: then it is not written).  Where the last
     token's target row is -inf throughout (a grammar mask that allows nothing), -1 stands in
-    its place and FAULT_EMPTY is set."""
+    its place and FAULT_EMPTY is set.
+    row_off [R+1] (a plan's): requests that the step gave no rows (too few pages or rows) are
+    left out; they get n_acc = -1, y -1 and c_star NaN, and keep their anchor x0 [R] in x_next."""
     torch = _torch()
     _chk(U, "U")
     R, gamma, V = U.shape
@@ -392,15 +394,21 @@ def verify(target, U, W2t, bias_rows, x, lse, logit_x, ell, seed=0, cycle=0, *, 
     x_next = out.get("x_next")
     if x_next is not None:
         _chk(x_next, "x_next", (R,), torch.int32)
+    if row_off is not None:
+        _chk(row_off, "row_off", (R + 1,), torch.int32)
+        if x0 is None and x_next is not None:
+            raise ValueError("row_off needs x0, the anchors of requests without rows")
+    if x0 is not None:
+        _chk(x0, "x0", (R,), torch.int32)
     nbytes = verify_workspace_bytes(R, gamma, V, r)
     if nbytes == 0 and R > 0:
         raise DsparkError("dspark_verify_workspace_bytes", EINVAL)
     ws = _ws(nbytes, dev, ws)
-    rc = lib().dspark_verify(R, gamma, V, r, dt, _p(target), _p(U), _p(W2t), _p(bias_rows),
-                             bdt, _p(x), _p(lse), _p(logit_x), _p(ell), seed, cycle,
-                             _p(out["n_acc"]), _p(out["y"]), _p(out["c_star"]), _p(x_next),
-                             _p(status),
-                             _p(ws), ws.numel() * ws.element_size(), _stream())
+    rc = lib().dspark_verify_rows(R, gamma, V, r, dt, _p(target), _p(U), _p(W2t), _p(bias_rows),
+                                  bdt, _p(x), _p(lse), _p(logit_x), _p(ell), _p(row_off), _p(x0),
+                                  seed, cycle, _p(out["n_acc"]), _p(out["y"]), _p(out["c_star"]),
+                                  _p(x_next), _p(status), _p(ws), ws.numel() * ws.element_size(),
+                                  _stream())
     _raise("dspark_verify", rc)
     return out
 

@@ -7,7 +7,8 @@
 // is padded.  Launches:
 //   prep    one workgroup: exclusive scans of ell; list A = (q, j) for j = 1..ell_q + 1
 //           (every row whose target normaliser is needed, the bonus row included), list B
-//           = (q, j) for j = 1..ell_q (every verified position);
+//           = (q, j) for j = 1..ell_q (every verified position); a request that the step gave
+//           no rows has none in either;
 //   lse     each list-A row in wave items of 64 blocks of 64 ids (a grid of at most four
 //           workgroups per CU walks the items, whose count is known on the device only;
 //           loads coalesced, 8 lanes per block): (max, sum exp) of the target logits; on
@@ -27,6 +28,7 @@
 #include "dev.h"
 #include "host.h"
 #include "sweep.h"
+#include "../../include/dspark_target.h"
 
 namespace dspark {
 
@@ -37,6 +39,7 @@ __host__ __device__ inline int lse_witems(int V) { return ((V + kVB - 1) / kVB +
 
 struct VerifyWs {
   int* hdr;        // [0] = |A|, [1] = |B|
+  int* len;        // [R] positions verified, -1: the step gave the request no rows
   int* offA;       // [R]
   int* offB;       // [R]
   int4* rowA;      // [R*(gamma+1)] (q, j, 1 if j is the bonus row, 0)
@@ -54,6 +57,7 @@ static VerifyWs carve_verify(void* ws, int R, int gamma, int V, int r) {
   Carve cv(ws);
   VerifyWs w{};
   w.hdr = cv.take<int>(4);
+  w.len = cv.take<int>((size_t)R);
   w.offA = cv.take<int>((size_t)R);
   w.offB = cv.take<int>((size_t)R);
   w.rowA = cv.take<int4>((size_t)R * (gamma + 1));
@@ -73,19 +77,27 @@ static VerifyWs carve_verify(void* ws, int R, int gamma, int V, int r) {
 // prep: ragged row lists from ell
 // ---------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) verify_prep_kernel(int R, int gamma, const int32_t* ell_in,
-                                                           VerifyWs ws, int32_t* status) {
+                                                           const int32_t* row_off, VerifyWs ws,
+                                                           int32_t* status) {
   __shared__ int totA[1024 / kWave], totB[1024 / kWave];
   const int per = (R + 1023) / 1024;
   const int lo = threadIdx.x * per, hi = min(R, lo + per);
   int sa = 0, sb = 0;
   for (int q = lo; q < hi; ++q) {
     int L = ell_in[q];
-    if (L < 0 || L > gamma) {
-      raise_fault(status, DSPARK_FAULT_LEN);
-      L = L < 0 ? 0 : gamma;
+    bool bad = L < 0 || L > gamma;
+    L = L < 0 ? 0 : (L > gamma ? gamma : L);
+    if (row_off) {  // a row for the anchor and for every position, or none at all
+      const int64_t n = (int64_t)row_off[q + 1] - row_off[q];
+      if (n <= L) {
+        bad = n != 0;
+        L = n < 1 ? -1 : (int)n - 1;
+      }
     }
+    if (bad) raise_fault(status, DSPARK_FAULT_LEN);
+    ws.len[q] = L;
     sa += L + 1;
-    sb += L;
+    sb += max(L, 0);
   }
   // exclusive prefix sums of the per-thread totals: inclusive scans inside each wave, then a
   // scan of the 16 wave totals (two barriers)
@@ -123,22 +135,19 @@ __global__ void __launch_bounds__(1024) verify_prep_kernel(int R, int gamma, con
   int oa = ia - sa + (wave > 0 ? totA[wave - 1] : 0);
   int ob = ib - sb + (wave > 0 ? totB[wave - 1] : 0);
   for (int q = lo; q < hi; ++q) {
-    int L = ell_in[q];
-    L = L < 0 ? 0 : (L > gamma ? gamma : L);
+    const int L = ws.len[q];
     ws.offA[q] = oa;
     ws.offB[q] = ob;
     for (int j = 1; j <= L + 1; ++j) ws.rowA[oa + j - 1] = make_int4(q, j, j == L + 1, 0);
     for (int j = 1; j <= L; ++j) ws.rowB[ob + j - 1] = make_int2(q, j);
     oa += L + 1;
-    ob += L;
+    ob += max(L, 0);
   }
   if (threadIdx.x == 1023) {
     ws.hdr[0] = totA[1024 / kWave - 1];
     ws.hdr[1] = totB[1024 / kWave - 1];
   }
 }
-
-__device__ __forceinline__ int clamp_len(int L, int gamma) { return L < 0 ? 0 : (L > gamma ? gamma : L); }
 
 // ---------------------------------------------------------------------------------------
 // lse: (max, sum exp) of every 4096-id wave item of the list-A rows (+ first level of the
@@ -193,7 +202,7 @@ struct LseRaw<float> {
 template <class T>
 __global__ void __launch_bounds__(kLseThreads) verify_lse_kernel(int R, int gamma, int V,
                                                                  const T* __restrict__ target,
-                                                                 const int32_t* ell, VerifyWs ws,
+                                                                 VerifyWs ws,
                                                                  uint64_t seed, uint64_t cycle) {
   constexpr float kLog2e = 1.4426950408889634f;
   constexpr float kLn2 = 0.69314718055994531f;
@@ -314,12 +323,12 @@ __global__ void __launch_bounds__(kLseThreads) verify_lse_kernel(int R, int gamm
 template <class T>
 __global__ void __launch_bounds__(64) verify_decide_kernel(
     int R, int gamma, int V, const T* __restrict__ target, const int32_t* __restrict__ x,
-    const float* __restrict__ lse, const float* __restrict__ logit_x, const int32_t* ell,
-    VerifyWs ws, uint64_t seed, uint64_t cycle, int32_t* n_acc, int32_t* y, int32_t* status,
+    const float* __restrict__ lse, const float* __restrict__ logit_x, VerifyWs ws,
+    uint64_t seed, uint64_t cycle, int32_t* n_acc, int32_t* y, int32_t* status,
     const uint16_t* __restrict__ brows, int r) {
   // one wave per request; lane j - 1 tests position j (gamma <= 64)
   const int q = blockIdx.x, lane = threadIdx.x, j = lane + 1;
-  const int L = clamp_len(ell[q], gamma);
+  const int L = ws.len[q];
   // the acceptance test's operands first (they do not depend on the normalisers, so this
   // chain of loads overlaps the packing and the merges below): x_j, its target logit,
   // log q_j(x_j) and the uniform
@@ -616,15 +625,20 @@ template <class T, class BT>
 __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
     int R, int gamma, int V, int r, const T* __restrict__ target, const T* __restrict__ U,
     const T* __restrict__ W2t, const BT* __restrict__ brows, const float* __restrict__ lse,
-    const int32_t* ell, VerifyWs ws, int nranges, uint64_t seed, uint64_t cycle,
-    const int32_t* n_acc, int32_t* y, float* c_star, int32_t* x_next) {
+    VerifyWs ws, int nranges, uint64_t seed, uint64_t cycle, const int32_t* n_acc, int32_t* y,
+    float* c_star, const int32_t* x0, int32_t* x_next) {
   constexpr int kWaves = kFinalThreads / kWave;
   constexpr int kJ = 8;  // verified rows whose range sums are in flight together
   __shared__ float tvs[kWaves][kJ];
   __shared__ float4 red[kWaves];
   __shared__ float dotp[kWaves][kWave];
   const int q = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int L = clamp_len(ell[q], gamma);
+  const int L = ws.len[q];
+  if (L < 0) {  // nothing was checked, and nothing is drawn: the anchor stays
+    if (tid < gamma) c_star[(size_t)q * gamma + tid] = __int_as_float(0x7fc00000);
+    if (tid == 0 && x_next) x_next[q] = x0[q];
+    return;
+  }
   const int nblocks = (V + kVB - 1) / kVB;
   const int js = ws.jstar[q];
   const size_t offA = (size_t)ws.offA[q], offB = (size_t)ws.offB[q];
@@ -791,9 +805,10 @@ __global__ void __launch_bounds__(kFinalThreads) verify_final_kernel(
 template <class T, class BT>
 static int verify_run(int R, int gamma, int V, int r, const void* target_, const void* U_,
                       const void* W2t_, const void* brows_, const int32_t* x, const float* lse,
-                      const float* logit_x, const int32_t* ell, uint64_t seed, uint64_t cycle,
-                      int32_t* n_acc, int32_t* y, float* c_star, int32_t* x_next,
-                      int32_t* status, const VerifyWs& ws, hipStream_t stream) {
+                      const float* logit_x, const int32_t* ell, const int32_t* row_off,
+                      const int32_t* x0, uint64_t seed, uint64_t cycle, int32_t* n_acc,
+                      int32_t* y, float* c_star, int32_t* x_next, int32_t* status,
+                      const VerifyWs& ws, hipStream_t stream) {
   const T* target = static_cast<const T*>(target_);
   const T* U = static_cast<const T*>(U_);
   const T* W2t = static_cast<const T*>(W2t_);
@@ -801,18 +816,18 @@ static int verify_run(int R, int gamma, int V, int r, const void* target_, const
   constexpr bool BF = sizeof(T) == 2;
   constexpr bool SPLIT = BF && sizeof(BT) == 4;
 
-  verify_prep_kernel<<<1, 1024, 0, stream>>>(R, gamma, ell, ws, status);
+  verify_prep_kernel<<<1, 1024, 0, stream>>>(R, gamma, ell, row_off, ws, status);
   {
     // a grid-stride walk over the items of list A (its length is known on the device only)
     const int wgs = (R * (gamma + 1) * lse_witems(V) + 3) / 4, cap = 4 * device_cus();
     verify_lse_kernel<T><<<wgs < cap ? wgs : cap, kLseThreads, 0, stream>>>(
-        R, gamma, V, target, ell, ws, seed, cycle);
+        R, gamma, V, target, ws, seed, cycle);
   }
   // bf16 bias rows go to the sweep in its packed order (float ones, split hi + lo, do not)
   const uint16_t* brows16 =
       (BF && !SPLIT) ? reinterpret_cast<const uint16_t*>(brows_) : nullptr;
-  verify_decide_kernel<T><<<R, 64, 0, stream>>>(R, gamma, V, target, x, lse, logit_x, ell, ws,
-                                                seed, cycle, n_acc, y, status, brows16, r);
+  verify_decide_kernel<T><<<R, 64, 0, stream>>>(R, gamma, V, target, x, lse, logit_x, ws, seed,
+                                                cycle, n_acc, y, status, brows16, r);
 
   const int rows_max = R * gamma;
   int nranges;
@@ -846,7 +861,7 @@ static int verify_run(int R, int gamma, int V, int r, const void* target_, const
         seed, cycle, nranges, nblocks);
   }
   verify_final_kernel<T, BT><<<R, kFinalThreads, 0, stream>>>(R, gamma, V, r, target, U, W2t, brows, lse,
-                                                    ell, ws, nranges, seed, cycle, n_acc, y, c_star,
+                                                    ws, nranges, seed, cycle, n_acc, y, c_star, x0,
                                                     x_next);
   return launch_status();
 }
@@ -860,12 +875,13 @@ size_t dspark_verify_workspace_bytes(int R, int gamma, int V, int r) {
   return dspark::carve_verify(nullptr, R, gamma, V, r).bytes;
 }
 
-int dspark_verify(int R, int gamma, int V, int r, dspark_dtype dt, const void* target,
-                  const void* U, const void* W2t, const void* bias_rows, dspark_dtype bias_dt,
-                  const int32_t* x, const float* lse, const float* logit_x, const int32_t* ell,
-                  uint64_t seed, uint64_t cycle, int32_t* n_acc, int32_t* y, float* c_star,
-                  int32_t* x_next, int32_t* dev_status, void* ws, size_t ws_bytes,
-                  hipStream_t stream) {
+int dspark_verify_rows(int R, int gamma, int V, int r, dspark_dtype dt, const void* target,
+                       const void* U, const void* W2t, const void* bias_rows,
+                       dspark_dtype bias_dt, const int32_t* x, const float* lse,
+                       const float* logit_x, const int32_t* ell, const int32_t* row_off,
+                       const int32_t* x0, uint64_t seed, uint64_t cycle, int32_t* n_acc,
+                       int32_t* y, float* c_star, int32_t* x_next, int32_t* dev_status, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
   using namespace dspark;
   if (!dims_ok(R, gamma, V, r, 0) || (dt != DSPARK_F32 && dt != DSPARK_BF16)) return DSPARK_EINVAL;
   if (bias_dt != DSPARK_F32 && bias_dt != dt) return DSPARK_EINVAL;
@@ -873,7 +889,7 @@ int dspark_verify(int R, int gamma, int V, int r, dspark_dtype dt, const void* t
   if (R == 0) return DSPARK_OK;
   if ((long)R * (gamma + 1) > (long)0x7fffffff / 2) return DSPARK_EINVAL;
   if (!target || !U || !W2t || !bias_rows || !x || !lse || !logit_x || !ell || !n_acc || !y ||
-      !c_star || !ws)
+      !c_star || !ws || (row_off && x_next && !x0))
     return DSPARK_EINVAL;
   if (!aligned16(target) || !aligned16(U) || !aligned16(W2t) || !aligned16(bias_rows))
     return DSPARK_EINVAL;
@@ -883,18 +899,24 @@ int dspark_verify(int R, int gamma, int V, int r, dspark_dtype dt, const void* t
   if (ws_bytes < carve_verify(nullptr, R, gamma, V, r).bytes) return DSPARK_EWORKSPACE;
   if (!aligned16(ws)) return DSPARK_EINVAL;
   const VerifyWs lay = carve_verify(ws, R, gamma, V, r);
-  if (dt == DSPARK_BF16) {
-    if (bias_dt == DSPARK_BF16)
-      return verify_run<uint16_t, uint16_t>(R, gamma, V, r, target, U, W2t, bias_rows, x, lse,
-                                            logit_x, ell, seed, cycle, n_acc, y, c_star,
-                                            x_next, dev_status, lay, stream);
-    return verify_run<uint16_t, float>(R, gamma, V, r, target, U, W2t, bias_rows, x, lse,
-                                       logit_x, ell, seed, cycle, n_acc, y, c_star, x_next,
-                                       dev_status, lay, stream);
-  }
-  return verify_run<float, float>(R, gamma, V, r, target, U, W2t, bias_rows, x, lse, logit_x,
-                                  ell, seed, cycle, n_acc, y, c_star, x_next, dev_status, lay,
-                                  stream);
+  auto run = [&](auto f) {
+    return f(R, gamma, V, r, target, U, W2t, bias_rows, x, lse, logit_x, ell, row_off, x0, seed,
+             cycle, n_acc, y, c_star, x_next, dev_status, lay, stream);
+  };
+  if (dt == DSPARK_F32) return run(verify_run<float, float>);
+  if (bias_dt == DSPARK_BF16) return run(verify_run<uint16_t, uint16_t>);
+  return run(verify_run<uint16_t, float>);
+}
+
+int dspark_verify(int R, int gamma, int V, int r, dspark_dtype dt, const void* target,
+                  const void* U, const void* W2t, const void* bias_rows, dspark_dtype bias_dt,
+                  const int32_t* x, const float* lse, const float* logit_x, const int32_t* ell,
+                  uint64_t seed, uint64_t cycle, int32_t* n_acc, int32_t* y, float* c_star,
+                  int32_t* x_next, int32_t* dev_status, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+  return dspark_verify_rows(R, gamma, V, r, dt, target, U, W2t, bias_rows, bias_dt, x, lse,
+                            logit_x, ell, nullptr, nullptr, seed, cycle, n_acc, y, c_star, x_next,
+                            dev_status, ws, ws_bytes, stream);
 }
 
 const char* dspark_version(void) { return "dspark-mi355x 0.1 (gfx950)"; }

@@ -6,6 +6,7 @@
   target_logits   penalties, biases and grammar masks, into the layout verify() reads
   cache_commit    after verify(): accepted path moved, lengths advanced, pages given back
 
+verify() takes the plan's row_off, so that requests the plan could not serve are left out.
 As in the other calls, tensors are device tensors, work goes to the current stream (of the
 tensors' device), bad shapes and types raise before anything is enqueued, and faults in the
 data set bits of `status` ([1] int32, nullable).  A cache is [n_pages][Hkv][page_size][D]
@@ -22,7 +23,7 @@ FAULT_PAGE, FAULT_TREE, FAULT_PARAM = 8, 16, 32
 MAX_TREE_NODES = 65
 TARGET_EXPORTS = ("dspark_cache_plan_workspace_bytes", "dspark_cache_plan",
                   "dspark_cache_append", "dspark_tree_attention_workspace_bytes",
-                  "dspark_tree_attention", "dspark_target_logits",
+                  "dspark_tree_attention", "dspark_target_logits", "dspark_verify_rows",
                   "dspark_cache_commit_workspace_bytes", "dspark_cache_commit")
 
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
@@ -31,6 +32,7 @@ _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat1
 def set_argtypes(L):
     """ctypes signatures of the library's target-side entry points."""
     i, i64, sz, vp, f = C.c_int, C.c_int64, C.c_size_t, C.c_void_p, C.c_float
+    u64 = C.c_uint64
     L.dspark_cache_plan_workspace_bytes.argtypes = [i] * 3
     L.dspark_cache_plan_workspace_bytes.restype = sz
     L.dspark_cache_plan.argtypes = ([i] * 6 + [vp] * 7 + [i] + [vp] * 7 + [sz, vp])
@@ -42,6 +44,8 @@ def set_argtypes(L):
                                         [f] + [vp] * 4 + [sz, vp])
     L.dspark_target_logits.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 4 + [i] + [vp] * 7 +
                                        [i, vp, i, i] + [vp] * 4)
+    L.dspark_verify_rows.argtypes = ([i] * 5 + [vp] * 4 + [i] + [vp] * 6 + [u64] * 2 + [vp] * 6 +
+                                     [sz, vp])
     L.dspark_cache_commit_workspace_bytes.argtypes = [i] * 3
     L.dspark_cache_commit_workspace_bytes.restype = sz
     L.dspark_cache_commit.argtypes = ([i] * 5 + [vp] * 9 + [i] * 5 + [vp] * 2 + [i64] * 4 +

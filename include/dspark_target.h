@@ -7,7 +7,7 @@
  *   dspark_cache_plan          rows, pages and cache slots of this step, from ell on the device
  *   per layer: dspark_cache_append, dspark_tree_attention
  *   dspark_target_logits       penalties, biases, grammar masks; packed rows -> verify's layout
- *   dspark_verify -> n_acc
+ *   dspark_verify_rows -> n_acc (-1 for requests that the plan gave no rows)
  *   dspark_cache_commit        accepted path moved, lengths advanced, finished requests' pages back
  *
  * The conventions are those of dspark.h: device pointers unless said otherwise, caller-owned
@@ -58,7 +58,8 @@ enum { DSPARK_MAX_TREE_NODES = 65 };
  * Requests are served in index order: q gets its rows iff n_0 + .. + n_q <= rows and
  * need_q = 0 or need_0 + .. + need_q <= *n_free (sums over the requests before it that fit
  * in `rows`).  One that is not served gets none (row_off[q+1] = row_off[q]) and keeps what
- * it holds; DSPARK_FAULT_LEN (rows) or DSPARK_FAULT_PAGE (pages) says so.
+ * it holds; DSPARK_FAULT_LEN (rows) or DSPARK_FAULT_PAGE (pages) says so.  Its target logits are
+ * nobody's, so verification has to leave it out: dspark_verify_rows takes row_off for that.
  *   pages  the k-th page handed out is free_pages[*n_free - 1 - k] (a stack); in place:
  *          table[q][held[q] ..], held[q] += need_q, *n_free -= all of them.  Nothing else of
  *          table is written, and a call repeated for the same step changes nothing.
@@ -174,13 +175,30 @@ int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *l
                          hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * dspark_verify (dspark.h) behind a step plan, which may give a request no rows.  row_off [R+1]
+ * int32: the plan's (NULL: exactly dspark_verify).  A request with row_off[q+1] = row_off[q] was
+ * not in the step: its target rows are not read, n_acc = -1 (which dspark_cache_commit takes to
+ * leave it as it is), y all -1, c_star all NaN, and x_next[q] = x0[q], its anchor (x0 [R] int32,
+ * needed with x_next; may be x_next itself).  One with fewer rows than ell + 1 counts as
+ * scheduled for rows - 1 positions, with fewer than 0 as not in the step (both
+ * DSPARK_FAULT_LEN).  Workspace: dspark_verify_workspace_bytes(R, gamma, V, r).
+ * ------------------------------------------------------------------------------------ */
+int dspark_verify_rows(int R, int gamma, int V, int r, dspark_dtype dt, const void *target,
+                       const void *U, const void *W2t, const void *bias_rows,
+                       dspark_dtype bias_dt, const int32_t *x, const float *lse,
+                       const float *logit_x, const int32_t *ell, const int32_t *row_off,
+                       const int32_t *x0, uint64_t seed, uint64_t cycle, int32_t *n_acc,
+                       int32_t *y, float *c_star, int32_t *x_next, int32_t *dev_status, void *ws,
+                       size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * Commit after verification.
  *   path [R][gamma] int32 (NULL: chains, nothing moves): the accepted nodes of a tree in
  *     order, ascending; for i = 1..n_acc[q], in every one of `layers` caches (layer_stride
  *     elements apart), token ctx[q] + i takes the keys and values that token
  *     ctx[q] + path[q][i-1] had before the call
- *   ctx_out[q] = ctx[q] + n_acc[q] + 1 (the anchor and the accepted nodes; n_acc = -1: the
- *     request had no rows); ctx_out may be ctx, and overlaps ctx, n_acc and held in no
+ *   ctx_out[q] = ctx[q] + n_acc[q] + 1 (the anchor and the accepted nodes; n_acc = -1, as
+ *     dspark_verify_rows gives it: the request had no rows); ctx_out may be ctx, and overlaps ctx, n_acc and held in no
  *     other way
  *   done [R] int32 (nullable): a request with done != 0 gives its pages back:
  *     free_pages[*n_free ..] takes table[q][0 .. held[q]) in request order, *n_free grows,

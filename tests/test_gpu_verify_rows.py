@@ -88,3 +88,140 @@ def test_rows_that_allow_nothing(gamma, V, dtype):
     got, st = go(ell, idx)
     assert st == 0 and np.array_equal(got["y"], plain["y"])
     assert np.isfinite(got["c_star"][~np.isnan(plain["c_star"])]).all()
+
+
+def T32(x):
+    return torch.tensor(x, dtype=I32, device="cuda:0")
+
+
+def cycle(ds, ops, lg, ell, ctx, held, table, free, n_free, page, rows, x0, status):
+    """Plan, logits, verify and commit of one step as a program runs them; `lg` [R][gamma+1][V]
+    are the rows that a target would give, packed here by the plan."""
+    I, U, W2t, d = ops
+    R, gamma, V = U.shape
+    p = ds.cache_plan(ell, ctx, held, table, free, n_free, page, rows=rows, extra=1, status=status)
+    row = torch.arange(rows, device="cuda:0")
+    q = p["req"].long().clamp(0, R - 1)
+    j = row - p["row_off"].long()[q]
+    live = row < p["row_off"][-1]
+    packed = torch.where(live[:, None], lg[q, j.clamp(0, gamma)], float("nan"))
+    out = torch.full((R, gamma + 1, V), float("nan"), dtype=lg.dtype, device="cuda:0")
+    t = ds.target_logits(packed, ell, d["x"], row_off=p["row_off"], out=out)
+    v = ds.verify(t, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell, 5, 1,
+                  row_off=p["row_off"], x0=x0, status=status)
+    new = ds.cache_commit(v["n_acc"], ctx, held, table, free, n_free, page, status=status)
+    return p, v, new
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("short", ["pages", "rows", "none", "all"])
+def test_a_step_that_lacks_pages_or_rows(short, dtype):
+    """Requests that the plan cannot serve keep their anchor, their length and their pages,
+    though their last page has room; the others' tokens are those of a step that serves all."""
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V, page = 7, 6, 1000, 8
+    I, U, W2t, d, lg = drafted(R, gamma, V, dtype)
+    ops = (I, U, W2t, d)
+    ell = T32([6, 3, 6, 0, 6, 5, 6])
+    ctx0 = [4, 2, 13, 5, 3, 6, 5]      # the last page held has room in all of them
+    held0 = [1, 1, 2, 1, 1, 1, 1]
+    # pages lacked: 1, 0, 1, 0, 1, 1, 1
+    pages, rows = {"pages": (2, 49), "rows": (9, 20), "none": (9, 49), "all": (0, 3)}[short]
+    served = {"pages": [1, 1, 1, 1, 0, 0, 0], "rows": [1, 1, 1, 1, 0, 0, 0], "none": [1] * 7,
+              "all": [0] * 7}[short]
+    ell_short = ell if short != "all" else torch.full_like(ell, 6)
+    x0 = T32(list(range(100, 107)))
+    want = ds.verify(lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell_short, 5, 1)
+
+    def run(status):
+        table = torch.full((R, 4), -1, dtype=I32, device="cuda:0")
+        table[:, :2] = torch.arange(2 * R, device="cuda:0", dtype=I32).view(R, 2)
+        ctx, held = T32(ctx0), T32(held0)
+        free, n_free = T32(list(range(20, 29))), T32([pages])
+        p, v, new = cycle(ds, ops, lg, ell_short, ctx, held, table, free, n_free, page, rows, x0, status)
+        return p, v, new, held
+
+    st = T32([0])
+    p, v, new, held = run(st)
+    off = p["row_off"].tolist()
+    assert [int(b > a) for a, b in zip(off, off[1:])] == served
+    fault = {"pages": ds.FAULT_PAGE, "rows": ds.FAULT_LEN, "none": 0, "all": ds.FAULT_LEN}[short]
+    assert int(st) == fault
+    for q in range(R):
+        if served[q]:
+            for k in v:
+                assert torch.equal(v[k][q].nan_to_num(9), want[k][q].nan_to_num(9)), (q, k)
+            assert int(new[q]) == ctx0[q] + int(v["n_acc"][q]) + 1
+        else:
+            assert int(v["n_acc"][q]) == -1 and torch.all(v["y"][q] == -1)
+            assert torch.isnan(v["c_star"][q]).all() and int(v["x_next"][q]) == 100 + q
+            assert int(new[q]) == ctx0[q] and int(held[q]) == held0[q]
+
+
+def test_unserved_anchor_stays_in_place_and_replays():
+    """x_next may be x0 itself; captured, the plan's rows change from replay to replay."""
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V = 12, 4, 520
+    I, U, W2t, d, lg = drafted(R, gamma, V, torch.bfloat16)
+    g = np.random.default_rng(2)
+    ell, off, x0 = T32([gamma] * R), T32([0] * (R + 1)), T32(list(range(R)))
+    out = ds.verify(lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell, 5, 1)
+    out["x_next"] = x0
+
+    def run():
+        return ds.verify(lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell, 5, 1,
+                         row_off=off, x0=x0, out=out)
+
+    def change():
+        L = g.integers(0, gamma + 1, R)
+        ell.copy_(T32(L.tolist()))
+        n = np.where(g.random(R) < 0.5, L + 1, 0)
+        off.copy_(T32([0] + np.cumsum(n).tolist()))
+        x0.copy_(T32(list(range(R))))
+        return n
+
+    run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        n = change()
+        full = ds.verify(lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell, 5, 1)
+        graph.replay()
+        torch.cuda.synchronize()
+        for q in range(R):
+            if n[q]:
+                for k in out:
+                    assert torch.equal(out[k][q].nan_to_num(9), full[k][q].nan_to_num(9)), (q, k)
+            else:
+                assert int(out["n_acc"][q]) == -1 and int(x0[q]) == q
+
+
+def test_fewer_rows_than_tokens():
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V = 3, 4, 264
+    I, U, W2t, d, lg = drafted(R, gamma, V, torch.float32)
+    a = (lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"])
+    x0, st = T32([1, 2, 3]), T32([0])
+    v = ds.verify(*a, T32([4, 4, 2]), 5, 1, row_off=T32([0, 5, 8, 11]), x0=x0, status=st)
+    want = ds.verify(*a, T32([4, 2, 2]), 5, 1)
+    assert int(st) == ds.FAULT_LEN
+    for k in v:
+        assert torch.equal(v[k].nan_to_num(9), want[k].nan_to_num(9)), k
+    st.zero_()
+    v = ds.verify(*a, T32([4, 2, 2]), 5, 1, row_off=T32([0, 5, 3, 6]), x0=x0, status=st)
+    assert int(st) == ds.FAULT_LEN and v["n_acc"].tolist()[1] == -1 and v["x_next"].tolist()[1] == 2
+    # more rows than tokens: the scheduled ones count
+    v = ds.verify(*a, T32([4, 2, 2]), 5, 1, row_off=T32([0, 5, 10, 15]), x0=x0, status=st.zero_())
+    assert int(st) == 0
+    for k in v:
+        assert torch.equal(v[k].nan_to_num(9), want[k].nan_to_num(9)), k
+    with pytest.raises(ValueError):
+        ds.verify(*a, T32([4, 2, 2]), 5, 1, row_off=T32([0, 5, 10, 15]))
+    with pytest.raises(ValueError):
+        ds.verify(*a, T32([4, 2, 2]), 5, 1, row_off=T32([0, 5, 10]), x0=x0)

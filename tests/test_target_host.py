@@ -1,0 +1,34 @@
+"""Host-side checks of the calls around the target's pass (no GPU needed)."""
+import ctypes as C
+import os
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def ds():
+    import draft_sampling_scheduling_amd as ds
+    if not os.path.exists(ds.LIB_PATH):
+        from draft_sampling_scheduling_amd import build
+        build.build()
+    ds.lib()
+    return ds
+
+
+def P(x=0x1000):
+    return C.c_void_p(x)  # never dereferenced: these calls return before any launch
+
+
+def test_verify_rows_refusals(ds):
+    ws = ds.verify_workspace_bytes(4, 4, 1024, 16)
+
+    def call(row_off=P(), x0=P(), x_next=P(), ws_bytes=ws, ell=P(), R=4):
+        return ds.lib().dspark_verify_rows(R, 4, 1024, 16, ds.BF16, P(), P(), P(), P(), ds.BF16, P(), P(),
+                                           P(), ell, row_off, x0, 0, 0, P(), P(), P(), x_next, None, P(),
+                                           ws_bytes, None)
+
+    assert call(x0=None) == ds.EINVAL  # nothing to keep in x_next
+    assert call(ell=None) == ds.EINVAL
+    assert call(R=0) == ds.OK
+    for k in (dict(), dict(x0=None, x_next=None), dict(row_off=None, x0=None)):
+        assert call(ws_bytes=ws - 1, **k) == ds.EWORKSPACE  # past the checks of arguments
