@@ -5,12 +5,14 @@
 // and a slice of the vocabulary and walks the request's rows (all of them, or some where there are
 // few requests): it scans the history once, into a word per id in LDS (times generated, seen in
 // the prompt), and from there a thread keeps the words of its ids in registers; from one row to
-// the next they change only by the drafted token between them.  A row's operands load while the
-// row before it is worked on.  Ids that nothing touches are copied as they are. Measured: 256
+// the next they change only by the drafted token between them (in a tree: by the tokens above one
+// of the two nodes and not the other).  A row's operands load while the row before it is worked on.  Ids that nothing touches are copied as they are. Measured: 256
 // requests, 151936 ids, bf16, up to nine rows each (786 MB): 154 to 170 us, 4.6 to 5.1 TB/s, a
 // copy's rate; loads that were not all issued a row ahead (the mask's bits behind the next row's
 // logits) had made it 257 us.  4 requests of 1024 ids, up to five rows: 5.8 us, the trips to
 // memory.
+#include <type_traits>
+
 #include "target.h"
 
 namespace dspark {
@@ -27,6 +29,7 @@ struct LogitsParams {
   int64_t row_stride;
   const void* logits;
   const int32_t *row_off, *ell, *x, *hist, *hist_len, *prompt_len;
+  const uint64_t* anc;
   const float *rep, *pres, *freq;
   const int32_t* bias_id;
   const float* bias;
@@ -83,8 +86,9 @@ __device__ __forceinline__ V uniform_load(const V* p, int64_t i) {
   return ((const __attribute__((address_space(4))) V*)p)[i];
 }
 
-// PARTS: a request's rows go to several workgroups, p.per to each.
-template <class T, bool PARTS>
+// PARTS: a request's rows go to several workgroups, p.per to each.  TREE: the drafted tokens
+// that a row counts are those of its mask in p.anc, not all before it.
+template <class T, bool PARTS, bool TREE>
 __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams p) {
   // one word per id of the slice: first what the history holds of it, then (its words in
   // registers) which bias entry is its last
@@ -119,7 +123,10 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
   if (has_hist) load_ids(tid);
   const int32_t* bias_id = p.bias_id + (int64_t)q * p.nbias;
   // tokens drafted before the workgroup's first row count as the history's
-  const int drafted = PARTS && tid < j0 ? p.x[(int64_t)q * p.gamma + tid] : -1;
+  const int drafted = PARTS && !TREE && tid < j0 ? p.x[(int64_t)q * p.gamma + tid] : -1;
+  // a tree's tokens, one a lane (gamma <= 64)
+  const int lane = tid & (kWave - 1);
+  const int tokens = TREE ? p.x[(int64_t)q * p.gamma + (lane < p.gamma ? lane : p.gamma - 1)] : 0;
   int first_bias = -1;
   if (p.nbias > 0) first_bias = bias_id[tid < p.nbias ? tid : p.nbias - 1];
 
@@ -143,12 +150,14 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
   struct Row {
     Raw8<T> x[kLogGroups];
     uint32_t bits[kLogGroups];
+    uint64_t anc;  // TREE: the nodes j >= 1 (bit j - 1) on the way to the row's
   };
   auto row_ok = [&](int j) { return row0 + j >= 0 && row0 + j < rows; };
   auto load_row = [&](int j, Row& r) {
 #pragma unroll
     for (int g = 0; g < kLogGroups; ++g) r.bits[g] = 0xFFu;
     if (!row_ok(j)) return;
+    if (TREE) r.anc = uniform_load(p.anc, row0 + j) & (~(uint64_t)0 >> (kMaxGamma - p.gamma));
     if (p.mask) {
       const int64_t at = (int64_t)q * (p.gamma + 1) + j;
       const int64_t i = p.mask_idx ? uniform_load(p.mask_idx, at) : at;
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
       }
     }
   }
-  if (PARTS && tid < j0) {
+  if (PARTS && !TREE && tid < j0) {
     if (drafted < 0 || drafted >= p.V) {
       if (blockIdx.x == 0) raise_fault(p.status, DSPARK_FAULT_TOKEN);
     } else if ((uint32_t)(drafted - v0) < kLogSlice) {
@@ -250,22 +259,33 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
       }
   }
 
+  // one more drafted token (or, by = -1, one less) among what the rows count
+  auto count = [&](int id, uint32_t by) {
+    if ((id < 0 || id >= p.V) && tell) raise_fault(p.status, DSPARK_FAULT_TOKEN);
+    const uint32_t in = (uint32_t)(id - v0);
+    if (id < 0 || id >= p.V || in >= kLogSlice) return;
+#pragma unroll
+    for (int g = 0; g < kLogGroups; ++g) {
+      const uint32_t at = in - (uint32_t)(g * kLogSpan + tid * 8);
+      touched[g] = touched[g] || at < 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[g][e] += at == (uint32_t)e ? by : 0u;
+    }
+  };
+  uint64_t above = 0;  // TREE: the nodes counted
   for (int j = j0; j <= last; ++j) {
     Row cur = next;
     if (j < last) load_row(j + 1, next);
-    if (j > j0) {  // the token drafted between the last row and this one
-      const int id = uniform_load(p.x, (int64_t)q * p.gamma + j - 1);
-      if ((id < 0 || id >= p.V) && tell) raise_fault(p.status, DSPARK_FAULT_TOKEN);
-      const uint32_t in = (uint32_t)(id - v0);
-      if (id >= 0 && id < p.V && in < kLogSlice) {
-#pragma unroll
-        for (int g = 0; g < kLogGroups; ++g) {
-          const uint32_t at = in - (uint32_t)(g * kLogSpan + tid * 8);
-          touched[g] = touched[g] || at < 8;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[g][e] += at == (uint32_t)e ? 1u : 0u;
+    if (TREE) {
+      if (row_ok(j)) {
+        for (uint64_t turn = above ^ cur.anc; turn != 0; turn &= turn - 1) {
+          const int b = __builtin_ctzll(turn);
+          count(__builtin_amdgcn_readlane(tokens, b), (cur.anc >> b) & 1 ? 1u : ~0u);
         }
+        above = cur.anc;
       }
+    } else if (j > j0) {  // the token drafted between the last row and this one
+      count(uniform_load(p.x, (int64_t)q * p.gamma + j - 1), 1u);
     }
     if (!row_ok(j)) {
       if (tell) raise_fault(p.status, DSPARK_FAULT_LEN);
@@ -299,15 +319,13 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
 
 using namespace dspark;
 
-extern "C" int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void* logits,
-                                    int64_t row_stride, int rows, const int32_t* row_off,
-                                    const int32_t* ell, const int32_t* x, const int32_t* hist,
-                                    int hist_stride, const int32_t* hist_len,
-                                    const int32_t* prompt_len, const float* rep,
-                                    const float* pres, const float* freq, const int32_t* bias_id,
-                                    const float* bias, int nbias, const uint32_t* mask,
-                                    int n_mask, int mask_stride, const int32_t* mask_idx,
-                                    void* out, int32_t* dev_status, hipStream_t stream) {
+extern "C" int dspark_target_logits_tree(
+    int R, int gamma, int V, dspark_dtype dt, const void* logits, int64_t row_stride, int rows,
+    const int32_t* row_off, const int32_t* ell, const int32_t* x, const uint64_t* anc,
+    const int32_t* hist, int hist_stride, const int32_t* hist_len, const int32_t* prompt_len,
+    const float* rep, const float* pres, const float* freq, const int32_t* bias_id,
+    const float* bias, int nbias, const uint32_t* mask, int n_mask, int mask_stride,
+    const int32_t* mask_idx, void* out, int32_t* dev_status, hipStream_t stream) {
   if (R < 0 || R > 65535 || gamma < 1 || gamma > kMaxGamma || V < 8 || V % 8 != 0 ||
       (dt != DSPARK_F32 && dt != DSPARK_BF16) || rows < 0 || row_stride < V || nbias < 0)
     return DSPARK_EINVAL;
@@ -338,6 +356,7 @@ extern "C" int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, co
   p.row_off = row_off;
   p.ell = ell;
   p.x = x;
+  p.anc = anc;
   p.hist = hist;
   p.hist_len = hist_len;
   p.prompt_len = prompt_len;
@@ -358,9 +377,33 @@ extern "C" int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, co
   p.per = parts > 1 ? (gamma + (int)parts) / (int)parts : gamma + 1;
   const dim3 grid(slices, R, gamma / p.per + 1);
   auto run = [&](auto kern) { kern<<<grid, kLogThreads, 0, stream>>>(p); };
-  if (dt == DSPARK_BF16)
-    run(parts > 1 ? target_logits_kernel<uint16_t, true> : target_logits_kernel<uint16_t, false>);
+  auto pick = [&](auto tree) {
+    constexpr bool TREE = decltype(tree)::value;
+    if (dt == DSPARK_BF16)
+      run(parts > 1 ? target_logits_kernel<uint16_t, true, TREE>
+                    : target_logits_kernel<uint16_t, false, TREE>);
+    else
+      run(parts > 1 ? target_logits_kernel<float, true, TREE>
+                    : target_logits_kernel<float, false, TREE>);
+  };
+  if (anc)
+    pick(std::true_type{});
   else
-    run(parts > 1 ? target_logits_kernel<float, true> : target_logits_kernel<float, false>);
+    pick(std::false_type{});
   return launch_status();
+}
+
+extern "C" int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void* logits,
+                                    int64_t row_stride, int rows, const int32_t* row_off,
+                                    const int32_t* ell, const int32_t* x, const int32_t* hist,
+                                    int hist_stride, const int32_t* hist_len,
+                                    const int32_t* prompt_len, const float* rep,
+                                    const float* pres, const float* freq, const int32_t* bias_id,
+                                    const float* bias, int nbias, const uint32_t* mask,
+                                    int n_mask, int mask_stride, const int32_t* mask_idx,
+                                    void* out, int32_t* dev_status, hipStream_t stream) {
+  return dspark_target_logits_tree(R, gamma, V, dt, logits, row_stride, rows, row_off, ell, x,
+                                   nullptr, hist, hist_stride, hist_len, prompt_len, rep, pres,
+                                   freq, bias_id, bias, nbias, mask, n_mask, mask_stride, mask_idx,
+                                   out, dev_status, stream);
 }

@@ -23,7 +23,8 @@ FAULT_PAGE, FAULT_TREE, FAULT_PARAM = 8, 16, 32
 MAX_TREE_NODES = 65
 TARGET_EXPORTS = ("dspark_cache_plan_workspace_bytes", "dspark_cache_plan",
                   "dspark_cache_append", "dspark_tree_attention_workspace_bytes",
-                  "dspark_tree_attention", "dspark_target_logits", "dspark_verify_rows",
+                  "dspark_tree_attention", "dspark_target_logits",
+                  "dspark_target_logits_tree", "dspark_verify_rows",
                   "dspark_cache_commit_workspace_bytes", "dspark_cache_commit")
 
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
@@ -44,6 +45,8 @@ def set_argtypes(L):
                                         [f] + [vp] * 4 + [sz, vp])
     L.dspark_target_logits.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 4 + [i] + [vp] * 7 +
                                        [i, vp, i, i] + [vp] * 4)
+    L.dspark_target_logits_tree.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 5 + [i] + [vp] * 7 +
+                                            [i, vp, i, i] + [vp] * 4)
     L.dspark_verify_rows.argtypes = ([i] * 5 + [vp] * 4 + [i] + [vp] * 6 + [u64] * 2 + [vp] * 6 +
                                      [sz, vp])
     L.dspark_cache_commit_workspace_bytes.argtypes = [i] * 3
@@ -317,7 +320,7 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
     return out
 
 
-def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, prompt_len=None,
+def target_logits(logits, ell, x, *, row_off=None, anc=None, hist=None, hist_len=None, prompt_len=None,
                   rep=None, pres=None, freq=None, bias_id=None, bias=None, mask=None,
                   mask_idx=None, out=None, status=None):
     """The target's logits with each request's penalties, biases and grammar masks, in the
@@ -326,6 +329,8 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
     logits: packed [rows][V] with row_off [R+1] (a plan's), or [R][gamma+1][V] without; `out`
     may be logits itself in the latter form.  Rows that row_off does not give a request (one
     that the plan did not serve, say) are left as they were and set FAULT_LEN.
+    anc [rows] int64 (a plan's): a tree, row j follows the anchor and the tokens x[q][i-1] of the
+    nodes i in its mask.
     hist [R][n] with hist_len [R], prompt_len [R]: each request's tokens, prompt first, anchor
     included; rep divides positive and multiplies other logits of seen ids; pres and freq (times
     the count) are taken off generated ids; bias_id, bias [R][nbias] (-1: unused; the last
@@ -363,9 +368,12 @@ def target_logits(logits, ell, x, *, row_off=None, hist=None, hist_len=None, pro
         if mask_idx is None and n_mask < R * (gamma + 1):
             raise ValueError("without mask_idx there is a mask for every row")
     per = (R,)
-    _call(dev, "dspark_target_logits", R, gamma, V, dt, lp, stride, rows,
+    name, masks = "dspark_target_logits", ()
+    if anc is not None:
+        name, masks = "dspark_target_logits_tree", (_chk(anc, "anc", dev, (rows,), _I64),)
+    _call(dev, name, R, gamma, V, dt, lp, stride, rows,
           _opt(row_off, "row_off", dev, (R + 1,), _I32), _chk(ell, "ell", dev, per, _I32), xp,
-          _opt(hist, "hist", dev, (R, n_hist), _I32), n_hist,
+          *masks, _opt(hist, "hist", dev, (R, n_hist), _I32), n_hist,
           _opt(hist_len, "hist_len", dev, per, _I32),
           _opt(prompt_len, "prompt_len", dev, per, _I32), _opt(rep, "rep", dev, per, _F32),
           _opt(pres, "pres", dev, per, _F32), _opt(freq, "freq", dev, per, _F32),

@@ -6,7 +6,7 @@
  *   dspark_schedule -> ell
  *   dspark_cache_plan          rows, pages and cache slots of this step, from ell on the device
  *   per layer: dspark_cache_append, dspark_tree_attention
- *   dspark_target_logits       penalties, biases, grammar masks; packed rows -> verify's layout
+ *   dspark_target_logits[_tree] penalties, biases, grammar masks; packed rows -> verify's layout
  *   dspark_verify_rows -> n_acc (-1 for requests that the plan gave no rows)
  *   dspark_cache_commit        accepted path moved, lengths advanced, finished requests' pages back
  *
@@ -173,6 +173,21 @@ int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *l
                          const uint32_t *mask, int n_mask, int mask_stride,
                          const int32_t *mask_idx, void *out, int32_t *dev_status,
                          hipStream_t stream);
+
+/* The same for trees of drafted tokens, whose rows do not follow one another: row j of request q
+ * is node j, x[q][j-1] its token, and anc [rows] uint64 (a plan's; row row_off[q] + j as logits
+ * are; NULL: a chain, exactly dspark_target_logits) the nodes on the way to it.  Wherever
+ * x_1 .. x_j stands above, it is the tokens x_i of the row's mask (bits i - 1) instead.  Bits of
+ * nodes past gamma are ignored. */
+int dspark_target_logits_tree(int R, int gamma, int V, dspark_dtype dt, const void *logits,
+                              int64_t row_stride, int rows, const int32_t *row_off,
+                              const int32_t *ell, const int32_t *x, const uint64_t *anc,
+                              const int32_t *hist, int hist_stride, const int32_t *hist_len,
+                              const int32_t *prompt_len, const float *rep, const float *pres,
+                              const float *freq, const int32_t *bias_id, const float *bias,
+                              int nbias, const uint32_t *mask, int n_mask, int mask_stride,
+                              const int32_t *mask_idx, void *out, int32_t *dev_status,
+                              hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * dspark_verify (dspark.h) behind a step plan, which may give a request no rows.  row_off [R+1]

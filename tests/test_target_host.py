@@ -32,3 +32,15 @@ def test_verify_rows_refusals(ds):
     assert call(R=0) == ds.OK
     for k in (dict(), dict(x0=None, x_next=None), dict(row_off=None, x0=None)):
         assert call(ws_bytes=ws - 1, **k) == ds.EWORKSPACE  # past the checks of arguments
+
+
+def test_logits_tree_refusals(ds):
+    def call(lg=P(), out=P(0x9000), off=P(), ell=P(), R=4):
+        return ds.lib().dspark_target_logits_tree(R, 4, 1024, ds.BF16, lg, 1024, 20, off, ell, P(), P(),
+                                                  None, 0, None, None, None, None, None, None, None, 0, None,
+                                                  0, 0, None, out, None, None)
+
+    for bad in (dict(lg=None), dict(out=None), dict(ell=None), dict(R=65536), dict(out=P()),
+                dict(lg=P(0x10000))):
+        assert call(**bad) == ds.EINVAL, bad
+    assert call(R=0) == ds.OK
