@@ -21,7 +21,7 @@ constexpr int kRowThreads = 256;
 struct PlanWs {
   int32_t* held;   // [R] pages held before the call
   int32_t* take;   // [R] pages handed out to q
-  int32_t* first;  // [R] index of q's first page among those handed out
+  int32_t* first;  // [R] pages handed out before q's
   int32_t* nfree;  // [1] free pages before the call
   int32_t* off;    // [R + 1] the row offsets again, or null
   size_t bytes;
@@ -56,9 +56,9 @@ struct PlanArgs {
 // which everybody is served.  Otherwise a request's rows fit in a prefix of the requests that
 // ask for any, and of those its pages are had in a prefix of the ones that need any, so the
 // exclusive sum of the needs is also the count of pages handed out before it.
-// `to`: where the rows' kernel, or part, finds what it needs.
+// `to`: where the rows' kernel, or part, finds what it needs.  Returns the pages handed out.
 template <int NT>
-__device__ __forceinline__ void plan_scan(const PlanArgs& p, const PlanWs& to, int64_t* sums) {
+__device__ __forceinline__ int plan_scan(const PlanArgs& p, const PlanWs& to, int64_t* sums) {
   const int R = p.R, tid = threadIdx.x;
   const int per = (R + NT - 1) / NT;
   const int lo = min(R, tid * per), hi = min(R, lo + per);
@@ -141,13 +141,14 @@ __device__ __forceinline__ void plan_scan(const PlanArgs& p, const PlanWs& to, i
     const int h = p.held[q];
     to.held[q] = h;
     to.take[q] = lack ? 0 : need;
-    to.first[q] = (int32_t)(before < nf ? before : 0);
+    to.first[q] = (int32_t)(before < given ? before : given);
     if (!lack && need > 0) p.held[q] = h + need;
   }
   if (tid == NT - 1) {
     to.nfree[0] = nf;
     *p.n_free = nf - (int32_t)given;
   }
+  return (int)given;
 }
 
 // Row i of request q, whose rows begin at a: slot, position and ancestors (a walk up at most
@@ -209,9 +210,13 @@ __global__ void __launch_bounds__(kRowThreads) plan_rows_kernel(PlanArgs p) {
 }
 
 // The whole plan in one workgroup, for steps of not too many requests and rows: the scan; then
-// a thread per request takes its tree from the anchor down (a node's mask is its parent's and
-// its own bit) and names its rows' request; then a thread per row, four rows at a time (of
-// chains, which may be whole prompts, it finds the request in the row offsets).
+// a thread per request hands out its pages, takes its tree from the anchor down (a node's mask is
+// its parent's and its own bit) and names its rows' request; then a thread per row, four rows at
+// a time (of chains, which may be whole prompts, it finds the request in the row offsets).
+// Where a request takes more than kOwn pages, as prompts do, all pages go to a thread each, which
+// finds the request likewise.  Measured (with the launch): a prompt of 8192 rows in pages of 8
+// takes 11 us, handed out by its own thread 114; 256 chains that bring a page or none take 11.0
+// us, with a thread a page 13.6.
 template <int NT_, int R_, int ROWS_, int NODES_>
 struct PlanSize {
   static constexpr int NT = NT_, R = R_, ROWS = ROWS_, NODES = NODES_;
@@ -222,6 +227,7 @@ struct PlanSize {
     uint64_t bits[NODES];  // masks of the nodes, [R][width]
     int64_t sums[2 * NT / kWave];
     int held[R], take[R], first[R], off[R + 1], nfree[1], ctx[R];
+    int many;  // a request takes more pages than its thread hands out
     uint16_t req[ROWS];  // request of each row (trees)
     uint8_t up[NODES];
   };
@@ -231,10 +237,11 @@ using MidPlan = PlanSize<1024, 1024, 16384, 10240>;
 
 template <class S>
 __global__ void __launch_bounds__(S::NT) plan_small_kernel(PlanArgs p) {
-  constexpr int NT = S::NT, kBatch = 4;
+  constexpr int NT = S::NT, kBatch = 4, kOwn = 2;
   extern __shared__ uint64_t plan_lds[];
   auto& m = *reinterpret_cast<typename S::Lds*>(plan_lds);
   const int tid = threadIdx.x, R = p.R, lg = p.lg;
+  if (tid == 0) m.many = 0;
   if (p.parent) {  // (checked against the rows once those are known)
     constexpr int kLoads = 12;
     const int nodes = R * p.width;
@@ -252,13 +259,21 @@ __global__ void __launch_bounds__(S::NT) plan_small_kernel(PlanArgs p) {
       }
     }
   }
-  plan_scan<NT>(p, PlanWs{m.held, m.take, m.first, m.nfree, m.off, 0}, m.sums);
+  const int given =
+      plan_scan<NT>(p, PlanWs{m.held, m.take, m.first, m.nfree, m.off, 0}, m.sums);
   __syncthreads();
   const int nf = m.nfree[0];
+  int half = 1;  // the largest power of two below R, or 1
+  while (2 * half < R) half *= 2;
   for (int q = tid; q < R; q += NT) {
     m.ctx[q] = p.ctx[q];
-    const int32_t* top = p.free_pages + (nf - 1 - m.first[q]);
-    for (int k = 0; k < m.take[q]; ++k) p.table[(size_t)q * p.max_pages + m.held[q] + k] = top[-k];
+    const int take = m.take[q];
+    if (take > kOwn) {
+      m.many = 1;
+    } else {
+      const int32_t* top = p.free_pages + (nf - 1 - m.first[q]);
+      for (int k = 0; k < take; ++k) p.table[(size_t)q * p.max_pages + m.held[q] + k] = top[-k];
+    }
     if (p.parent) {
       const int n = m.off[q + 1] - m.off[q], at = q * p.width;
       for (int i = 0; i < n; ++i) {
@@ -273,9 +288,30 @@ __global__ void __launch_bounds__(S::NT) plan_small_kernel(PlanArgs p) {
     }
   }
   __syncthreads();
+  if (m.many) {
+    for (int k0 = tid; k0 < given; k0 += kBatch * NT) {
+      int page[kBatch], q[kBatch];
+  #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * NT;
+        page[u] = p.free_pages[nf - 1 - (k < given ? k : given - 1)];
+        q[u] = 0;
+      }
+      for (int s = half; s > 0; s >>= 1)  // the last whose pages begin at or before page k
+  #pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int next = q[u] + s;
+          q[u] = next < R && m.first[next] <= k0 + u * NT ? next : q[u];
+        }
+  #pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int k = k0 + u * NT;
+        if (k < given)
+          p.table[(size_t)q[u] * p.max_pages + m.held[q[u]] + k - m.first[q[u]]] = page[u];
+      }
+    }
+  }
   const int rows = m.off[R];
-  int half = 1;  // the largest power of two below R, or 1
-  while (2 * half < R) half *= 2;
   for (int row0 = tid; row0 < rows; row0 += kBatch * NT) {
     int q[kBatch], t[kBatch], page[kBatch];
 #pragma unroll
