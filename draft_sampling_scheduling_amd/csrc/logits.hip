@@ -342,7 +342,7 @@ extern "C" int dspark_target_logits_tree(
     const float* rep, const float* pres, const float* freq, const int32_t* bias_id,
     const float* bias, int nbias, const uint32_t* mask, int n_mask, int mask_stride,
     const int32_t* mask_idx, void* out, int32_t* dev_status, hipStream_t stream) {
-  if (R < 0 || R > 65535 || gamma < 1 || gamma > kMaxGamma || V < 8 || V % 8 != 0 ||
+  if (R < 0 || R > 65535 || gamma < 1 || gamma > kMaxGamma || V < 8 || V > 1 << 30 || V % 8 != 0 ||
       (dt != DSPARK_F32 && dt != DSPARK_BF16) || rows < 0 || row_stride < V || nbias < 0)
     return DSPARK_EINVAL;
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;

@@ -44,3 +44,14 @@ def test_logits_tree_refusals(ds):
                 dict(lg=P(0x10000))):
         assert call(**bad) == ds.EINVAL, bad
     assert call(R=0) == ds.OK
+
+
+def test_logits_vocabulary_limit(ds):
+    def call(V, logits=P(), rows=20):
+        return ds.lib().dspark_target_logits(0, 4, V, ds.BF16, logits, V, rows, P(), P(), P(), None, 0, None,
+                                             None, None, None, None, None, None, 0, None, 0, 0, None, P(0x9000),
+                                             None, None)
+
+    assert call(1 << 30) == ds.OK  # (no requests: returns before any launch)
+    assert call((1 << 30) + 8) == ds.EINVAL
+    assert call((1 << 31) - 8) == ds.EINVAL  # a slice's end would pass 31 bits
