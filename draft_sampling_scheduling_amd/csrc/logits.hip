@@ -348,7 +348,7 @@ extern "C" int dspark_target_logits_tree(
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;
   if (!stride_ok(row_stride, e)) return DSPARK_EINVAL;
   if (R == 0) return DSPARK_OK;
-  if (!logits || !ell || !x || !out || !aligned16(logits) || !aligned16(out) ||
+  if ((!logits && rows > 0) || !ell || !x || !out || !aligned16(logits) || !aligned16(out) ||
       (hist && (!hist_len || hist_stride < 0)) || (nbias > 0 && (!bias_id || !bias)) ||
       (mask && (n_mask < 1 || mask_stride < (V + 31) / 32)))
     return DSPARK_EINVAL;

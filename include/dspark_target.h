@@ -162,7 +162,7 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  *   [0, V) (DSPARK_FAULT_TOKEN, ignored); rep not finite or below FLT_MIN, pres or freq not finite
  *   (DSPARK_FAULT_PARAM: 1, 0, 0); a mask index outside [-1, n_mask) (DSPARK_FAULT_PARAM:
  *   no mask).
- * V % 8 == 0, V <= 2^30; logits, out and row_stride 16-byte aligned.
+ * V % 8 == 0, V <= 2^30; logits (NULL where rows is 0), out and row_stride 16-byte aligned.
  * ------------------------------------------------------------------------------------ */
 int dspark_target_logits(int R, int gamma, int V, dspark_dtype dt, const void *logits,
                          int64_t row_stride, int rows, const int32_t *row_off,

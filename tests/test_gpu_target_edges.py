@@ -1,0 +1,21 @@
+"""Calls of the target's side at the ends of what their documentation allows."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+I32, F32, BF = torch.int32, torch.float32, torch.bfloat16
+
+
+def T(x, dtype=I32):
+    return torch.tensor(np.asarray(x), dtype=dtype, device="cuda:0")
+
+
+def test_logits_of_a_step_without_rows():
+    """Nobody was served: every request is reported, nothing is written."""
+    import draft_sampling_scheduling_amd as ds
+    for dtype in (F32, BF):
+        out, st = torch.full((3, 3, 64), 5.0, dtype=dtype, device="cuda:0"), T([0])
+        got = ds.target_logits(torch.empty(0, 64, dtype=dtype, device="cuda:0"), T([2, 0, 1]),
+                               T([[1, 2]] * 3), row_off=T([0, 0, 0, 0]), out=out, status=st)
+        assert got is out and torch.all(out == 5) and int(st) == ds.FAULT_LEN
