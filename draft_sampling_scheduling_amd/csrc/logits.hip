@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
   const int64_t row1 = p.row_off ? uniform_load(p.row_off, (int64_t)q + 1) : p.rows;
   const int64_t rows = row1 < p.rows ? row1 : p.rows;  // the request's end before them
   const bool has_hist = p.hist && p.hist_stride > 0;
-  int hl = has_hist ? uniform_load(p.hist_len, q) : 0;
-  const int pl = has_hist && p.prompt_len ? uniform_load(p.prompt_len, q) : 0;
+  int hl = p.hist ? uniform_load(p.hist_len, q) : 0;
+  const int pl = p.hist && p.prompt_len ? uniform_load(p.prompt_len, q) : 0;
   const float rep_in = p.rep ? uniform_load(p.rep, q) : 1.0f;
   const float pres_in = p.pres ? uniform_load(p.pres, q) : 0.0f;
   const float freq_in = p.freq ? uniform_load(p.freq, q) : 0.0f;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kLogThreads) target_logits_kernel(LogitsParams
   float add[kLogGroups][8];
   bool touched[kLogGroups];
   clear();
-  if (has_hist) {
+  if (p.hist) {
     const bool bad = hl < 0 || hl > p.hist_stride || pl < 0 || pl > hl;
     if (bad && tell) raise_fault(p.status, DSPARK_FAULT_LEN);
     hl = hl < 0 ? 0 : (hl > p.hist_stride ? p.hist_stride : hl);

@@ -355,10 +355,14 @@ def target_logits(logits, ell, x, *, row_off=None, anc=None, hist=None, hist_len
         out = torch.empty((R, gamma + 1, V), dtype=logits.dtype, device=dev)
     op = _chk(out, "out", dev, (R, gamma + 1, V), logits.dtype)
     n_hist = nb = n_mask = words = 0
+    histp = None
     if hist is not None:
         if hist_len is None:
             raise ValueError("hist needs hist_len")
         n_hist = _dims(hist, "hist", 2)[1]
+        histp = _chk(hist, "hist", dev, (R, n_hist), _I32)
+        if n_hist == 0:  # (a tensor of no elements has no address)
+            histp = xp
     if (bias is None) != (bias_id is None):
         raise ValueError("bias and bias_id come together")
     if bias is not None:
@@ -373,7 +377,7 @@ def target_logits(logits, ell, x, *, row_off=None, anc=None, hist=None, hist_len
         name, masks = "dspark_target_logits_tree", (_chk(anc, "anc", dev, (rows,), _I64),)
     _call(dev, name, R, gamma, V, dt, lp, stride, rows,
           _opt(row_off, "row_off", dev, (R + 1,), _I32), _chk(ell, "ell", dev, per, _I32), xp,
-          *masks, _opt(hist, "hist", dev, (R, n_hist), _I32), n_hist,
+          *masks, histp, n_hist,
           _opt(hist_len, "hist_len", dev, per, _I32),
           _opt(prompt_len, "prompt_len", dev, per, _I32), _opt(rep, "rep", dev, per, _F32),
           _opt(pres, "pres", dev, per, _F32), _opt(freq, "freq", dev, per, _F32),

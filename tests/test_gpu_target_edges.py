@@ -19,3 +19,15 @@ def test_logits_of_a_step_without_rows():
         got = ds.target_logits(torch.empty(0, 64, dtype=dtype, device="cuda:0"), T([2, 0, 1]),
                                T([[1, 2]] * 3), row_off=T([0, 0, 0, 0]), out=out, status=st)
         assert got is out and torch.all(out == 5) and int(st) == ds.FAULT_LEN
+
+
+def test_logits_of_a_history_without_places():
+    import draft_sampling_scheduling_amd as ds
+    lg, x, ell = torch.randn(2, 3, 64, device="cuda:0"), T([[1, 2], [3, 4]]), T([2, 2])
+    hist = torch.empty(2, 0, dtype=I32, device="cuda:0")
+    pres = torch.ones(2, device="cuda:0")
+    want = ds.target_logits(lg, ell, x, pres=pres)
+    for lens, fault in (([0, 0], 0), ([0, 5], ds.FAULT_LEN), ([-1, 0], ds.FAULT_LEN)):
+        st = T([0])
+        got = ds.target_logits(lg, ell, x, hist=hist, hist_len=T(lens), pres=pres, status=st)
+        assert int(st) == fault and torch.equal(got, want), lens
