@@ -732,8 +732,13 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
     return DSPARK_EINVAL;
   const size_t len_bytes = (size_t)R * sizeof(int32_t);
   const bool apart = !overlap(ctx_out, len_bytes, ctx, len_bytes);
-  if ((!apart && ctx_out != ctx) || overlap(ctx_out, len_bytes, n_acc, len_bytes) ||
-      overlap(ctx_out, len_bytes, held, len_bytes))
+  // what is read after the first lengths are written, or written beside them
+  auto over = [&](const void* a, size_t ints) {
+    return a && overlap(ctx_out, len_bytes, a, ints * sizeof(int32_t));
+  };
+  if ((!apart && ctx_out != ctx) || over(n_acc, R) || over(held, R) ||
+      over(path, (size_t)R * gamma) || over(table, (size_t)R * max_pages) || over(done, R) ||
+      (done && (over(free_pages, free_len) || over(n_free, 1))))
     return DSPARK_EINVAL;
   const bool small = commit_small(R, done ? (int64_t)R * max_pages : 0, path && !apart);
   const CommitWs w = carve_commit(ws, R);

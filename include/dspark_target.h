@@ -213,8 +213,8 @@ int dspark_verify_rows(int R, int gamma, int V, int r, dspark_dtype dt, const vo
  *     elements apart), token ctx[q] + i takes the keys and values that token
  *     ctx[q] + path[q][i-1] had before the call
  *   ctx_out[q] = ctx[q] + n_acc[q] + 1 (the anchor and the accepted nodes; n_acc = -1, as
- *     dspark_verify_rows gives it: the request had no rows); ctx_out may be ctx, and overlaps ctx, n_acc and held in no
- *     other way
+ *     dspark_verify_rows gives it: the request had no rows); ctx_out may be ctx, and overlaps no
+ *     other argument, nor ctx in any other way
  *   done [R] int32 (nullable): a request with done != 0 gives its pages back:
  *     free_pages[*n_free ..] takes table[q][0 .. held[q]) in request order, *n_free grows,
  *     held[q] = ctx_out[q] = 0 (its tokens are not moved).  Every page held is given back, so

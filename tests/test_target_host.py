@@ -55,3 +55,23 @@ def test_logits_vocabulary_limit(ds):
     assert call(1 << 30) == ds.OK  # (no requests: returns before any launch)
     assert call((1 << 30) + 8) == ds.EINVAL
     assert call((1 << 31) - 8) == ds.EINVAL  # a slice's end would pass 31 bits
+
+
+def test_commit_lengths_over_other_arguments(ds):
+    """ctx_out may be ctx itself; over anything else that the call reads or writes it is refused."""
+    ws = ds.cache_commit_workspace_bytes(4, 10, True)
+
+    def call(out, ctx=0x2000, done=0x4000, ws_bytes=ws):
+        return ds.lib().dspark_cache_commit(4, 4, 16, 10, 8, P(0x1000), P(0x5000), P(done) if done else None,
+                                            P(ctx), P(out), P(0x3000), P(0x6000), P(0x7000), P(0x8000), 1, 2,
+                                            64, ds.BF16, 40, P(0x10000), P(0x20000), 0, 2048, 1024, 64, None,
+                                            P(0x9000), ws_bytes, None)
+
+    assert call(0x2000, ws_bytes=ws - 1) == ds.EWORKSPACE          # ctx: past the checks
+    for base, ints in ((0x1000, 4), (0x3000, 4), (0x4000, 4), (0x5000, 16), (0x6000, 40), (0x7000, 8),
+                       (0x8000, 1)):
+        for at in (base - 12, base, base + 4 * ints - 4):
+            assert call(at) == ds.EINVAL, (hex(base), hex(at))
+    assert call(0x2004) == ds.EINVAL
+    # the list is not touched without `done`
+    assert call(0x7000, ctx=0x7000, done=0, ws_bytes=ws - 1) == ds.EWORKSPACE
