@@ -415,6 +415,8 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     if path is not None:
         if k_cache is None or v_cache is None:
             raise ValueError("a path needs the caches")
+        if gamma == 0:
+            raise ValueError("path has no places")
         kp, vp, shape, st = _cache(k_cache, v_cache, dev, 5 if k_cache.dim() == 5 else 4)
         if len(shape) == 4:
             shape, st = (1, *shape), [0, *st]

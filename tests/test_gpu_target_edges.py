@@ -31,3 +31,13 @@ def test_logits_of_a_history_without_places():
         st = T([0])
         got = ds.target_logits(lg, ell, x, hist=hist, hist_len=T(lens), pres=pres, status=st)
         assert int(st) == fault and torch.equal(got, want), lens
+
+
+def test_commit_of_a_path_without_places():
+    """Not taken for a chain, whose n_acc has no such bound."""
+    import draft_sampling_scheduling_amd as ds
+    ctx, held, nf = T([0, 0]), T([1, 1]), T([0])
+    kc = torch.zeros(2, 1, 8, 64, device="cuda:0")
+    with pytest.raises(ValueError):
+        ds.cache_commit(T([2, 0]), ctx, held, T([[0], [1]]), T([0]), nf, 8, k_cache=kc, v_cache=kc.clone(),
+                        path=torch.empty(2, 0, dtype=I32, device="cuda:0"))
