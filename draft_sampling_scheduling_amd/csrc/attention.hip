@@ -1017,7 +1017,8 @@ static size_t att_carve(AttParams& p, void* ws, int R, int rows, int G, int D, d
 
 static bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt) {
   return R >= 0 && R <= kMaxRequests && rows >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 &&
-         (D == 64 || D == 128) && (dt == DSPARK_F32 || dt == DSPARK_BF16) && (int64_t)rows * Hq < ((int64_t)1 << 31);
+         (D == 64 || D == 128) && (dt == DSPARK_F32 || dt == DSPARK_BF16) &&
+         (int64_t)rows * Hq <= ((int64_t)1 << 31) - 1024;  // ends of row tiles in 31 bits
 }
 
 template <class T, int D, int NR>

@@ -114,7 +114,7 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row
  * does not see (stale, infinite or NaN) does not reach it.
  * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.
- * D in {64, 128}; Hq a multiple of Hkv; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
+ * D in {64, 128}; Hq a multiple of Hkv; rows * Hq <= 2^31 - 1024; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
  * aligned.  ctx + n beyond max_pages pages, ctx < 0 or row_off out of order are clamped
  * (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0 (DSPARK_FAULT_PAGE); with
  * anc, nodes past 64 are seen by nobody but through ctx (DSPARK_FAULT_TREE).

@@ -75,3 +75,11 @@ def test_commit_lengths_over_other_arguments(ds):
     assert call(0x2004) == ds.EINVAL
     # the list is not touched without `done`
     assert call(0x7000, ctx=0x7000, done=0, ws_bytes=ws - 1) == ds.EWORKSPACE
+
+
+def test_attention_rows_limit(ds):
+    """The end of the last row tile is counted in 31 bits."""
+    b = ds.tree_attention_workspace_bytes
+    assert b(1, (1 << 28) - 128, 8, 1, 64, ds.BF16) > 0
+    for rows, Hq in (((1 << 28) - 127, 8), ((1 << 28) - 1, 8), ((1 << 31) - 1, 1)):
+        assert b(1, rows, Hq, 1, 64, ds.BF16) == 0, (rows, Hq)
