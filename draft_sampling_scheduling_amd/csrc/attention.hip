@@ -1067,7 +1067,8 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
                                      void* o, float* lse, int32_t* dev_status, void* ws,
                                      size_t ws_bytes, hipStream_t stream) {
   if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || max_pages < 1 || !pages_ok(page_size, n_pages) ||
-      !table_ok(page_size, max_pages) || !(scale > 0.0f) || scale > FLT_MAX)
+      !table_ok(page_size, max_pages) || !(scale > 0.0f) ||
+      !(scale * kLog2e <= FLT_MAX))
     return DSPARK_EINVAL;
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;
   if (!stride_ok(q_row, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||

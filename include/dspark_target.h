@@ -108,7 +108,7 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  *   every token t < ctx[q], the anchor (t = ctx[q]), and node j >= 1 of its block (t =
  *   ctx[q] + j) iff j <= i (anc NULL: a chain, or a piece of a prompt of any length) or bit
  *   j-1 of anc[row] is set (a tree; j < n_q <= 65).
- *   o[row][a]   = sum_t softmax_t(scale * q[row][a] . K[t]) V[t],   scale > 0, finite
+ *   o[row][a]   = sum_t softmax_t(scale * q[row][a] . K[t]) V[t],   scale > 0, scale log2(e) finite
  *   lse[row][a] = ln sum_t exp(scale * q . K[t])        (nullable, float)
  * Scores, maxima, sums and o are held in float; with bf16 operands the weights exp(s - max)
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row

@@ -83,3 +83,16 @@ def test_attention_rows_limit(ds):
     assert b(1, (1 << 28) - 128, 8, 1, 64, ds.BF16) > 0
     for rows, Hq in (((1 << 28) - 127, 8), ((1 << 28) - 1, 8), ((1 << 31) - 1, 1)):
         assert b(1, rows, Hq, 1, 64, ds.BF16) == 0, (rows, Hq)
+
+
+def test_attention_scale_limit(ds):
+    """Scores are taken in powers of two: scale * log2(e) has to be a float."""
+    def call(scale):
+        return ds.lib().dspark_tree_attention(4, 20, 8, 2, 64, ds.BF16, 16, 10, 40, P(), 512, P(), P(), 2048,
+                                              1024, 64, P(), P(), P(), None, scale, P(0x100000), None, None, P(),
+                                              0, None)
+
+    for scale in (0.125, 1e-40, 2.3e38):
+        assert call(scale) == ds.EWORKSPACE, scale  # past the checks of arguments
+    for scale in (2.4e38, 3.4e38, float("inf"), float("nan"), 0.0, -0.125):
+        assert call(scale) == ds.EINVAL, scale
