@@ -209,6 +209,8 @@ def _workspace(nbytes, dev):
 
 def _given(ws, dev):
     """The caller's workspace (the library looks at its size)."""
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
     if ws.device != dev or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {dev}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
@@ -417,7 +419,8 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
             raise ValueError("a path needs the caches")
         if gamma == 0:
             raise ValueError("path has no places")
-        kp, vp, shape, st = _cache(k_cache, v_cache, dev, 5 if k_cache.dim() == 5 else 4)
+        layered = isinstance(k_cache, torch.Tensor) and k_cache.dim() == 5
+        kp, vp, shape, st = _cache(k_cache, v_cache, dev, 5 if layered else 4)
         if len(shape) == 4:
             shape, st = (1, *shape), [0, *st]
         if shape[3] != page_size:

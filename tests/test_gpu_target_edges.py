@@ -41,3 +41,21 @@ def test_commit_of_a_path_without_places():
     with pytest.raises(ValueError):
         ds.cache_commit(T([2, 0]), ctx, held, T([[0], [1]]), T([0]), nf, 8, k_cache=kc, v_cache=kc.clone(),
                         path=torch.empty(2, 0, dtype=I32, device="cuda:0"))
+
+
+def test_workspaces_that_are_no_tensors():
+    import draft_sampling_scheduling_amd as ds
+    one, zero, nf = T([1, 1]), T([0, 0]), T([0])
+    kc = torch.zeros(2, 1, 8, 64, device="cuda:0")
+    for ws in (3, [0] * 4, np.zeros(64, np.uint8)):
+        with pytest.raises(TypeError):
+            ds.cache_plan(one, zero, one, T([[0], [1]]), T([0]), nf, 8, rows=2, ws=ws)
+        with pytest.raises(TypeError):
+            ds.cache_commit(zero, zero, one, T([[0], [1]]), T([0]), nf, 8, ws=ws)
+        with pytest.raises(TypeError):
+            ds.tree_attention(torch.zeros(2, 1, 64, device="cuda:0"), kc, kc, T([[0], [1]]), zero, T([0, 1, 2]),
+                              ws=ws)
+    # nor are caches
+    with pytest.raises(TypeError):
+        ds.cache_commit(zero, zero, one, T([[0], [1]]), T([0]), nf, 8, path=T([[1], [1]]), k_cache=[0],
+                        v_cache=kc)
