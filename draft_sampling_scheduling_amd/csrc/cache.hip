@@ -685,6 +685,14 @@ extern "C" int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, in
   const int chunks = D / u;
   const int64_t pieces = (int64_t)Hkv * chunks, blocks = (rows * pieces + 255) / 256;
   if (blocks >= (1 << 24)) return DSPARK_EINVAL;  // a grid holds 2^32 threads
+  // a row may be read after another is written
+  const size_t row_bytes = (size_t)pieces * 16;
+  const size_t kb = (size_t)(rows - 1) * k_row * e + row_bytes;
+  const size_t vb = (size_t)(rows - 1) * v_row * e + row_bytes;
+  const size_t cb = ((size_t)(n_pages - 1) * page_stride + (size_t)(Hkv - 1) * head_stride +
+                     (size_t)(page_size - 1) * tok_stride + D) * e;
+  for (const void* cache : {k_cache, v_cache})
+    if (overlap(k, kb, cache, cb) || overlap(v, vb, cache, cb)) return DSPARK_EINVAL;
   append_kernel<<<(unsigned)blocks, 256, 0, stream>>>(
       rows, (int)pieces, chunks, log2_of(page_size), n_pages, static_cast<const uint4*>(k),
       static_cast<const uint4*>(v), k_row / u, v_row / u, slot, n_rows,

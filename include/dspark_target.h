@@ -93,7 +93,7 @@ int dspark_cache_plan(int R, int rows, int page_size, int max_pages, int free_le
  * page_size) skips it and sets DSPARK_FAULT_PAGE.  n_rows (device, nullable): only the first
  * *n_rows rows exist (pass row_off + R); no value of it reads past `rows`.  Slots of one
  * call are distinct; of rows with the same slot either's elements may remain.  k and v lie
- * apart from the caches.
+ * outside the memory from the caches' first to their last element.
  * D % 8 == 0, D <= 1024; strides multiples of 16 bytes, pointers 16-byte aligned.
  * ------------------------------------------------------------------------------------ */
 int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size, int n_pages,

@@ -59,3 +59,25 @@ def test_workspaces_that_are_no_tensors():
     with pytest.raises(TypeError):
         ds.cache_commit(zero, zero, one, T([[0], [1]]), T([0]), nf, 8, path=T([[1], [1]]), k_cache=[0],
                         v_cache=kc)
+
+
+def test_append_from_beside_a_cache():
+    """Rows right before and right behind the caches in one allocation are taken; rows in them are
+    refused, and leave them as they were."""
+    import draft_sampling_scheduling_amd as ds
+    n, rows = 3 * 2 * 8 * 64, 4
+    for dtype in (F32, BF):
+        mem = torch.randn(2 * n + 2 * rows * 128, device="cuda:0").to(dtype)
+        before, behind = mem[:rows * 128].view(rows, 2, 64), mem[-rows * 128:].view(rows, 2, 64)
+        kc, vc = mem[rows * 128:-rows * 128].view(2, 3, 2, 8, 64)
+        slot = T([3, 8, 23, 0])
+        ds.cache_append(before, behind, kc, vc, slot)
+        for i, s in enumerate(slot.tolist()):
+            assert torch.equal(kc[s // 8, :, s % 8], before[i]) and torch.equal(vc[s // 8, :, s % 8], behind[i])
+        was = mem.clone()
+        for at in (8, rows * 128, rows * 128 + n - 64, mem.numel() - rows * 128 - 8):
+            inside = mem[at:at + rows * 128].view(rows, 2, 64)
+            for a in ((inside, behind), (behind, inside)):
+                with pytest.raises(ds.DsparkError):
+                    ds.cache_append(*a, kc, vc, slot)
+        assert torch.equal(mem, was)

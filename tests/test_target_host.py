@@ -96,3 +96,19 @@ def test_attention_scale_limit(ds):
         assert call(scale) == ds.EWORKSPACE, scale  # past the checks of arguments
     for scale in (2.4e38, 3.4e38, float("inf"), float("nan"), 0.0, -0.125):
         assert call(scale) == ds.EINVAL, scale
+
+
+def test_append_rows_inside_the_caches(ds):
+    """Rows that lie in a cache are refused, whichever of the two."""
+    rows, Hkv, D, page, n = 4, 2, 64, 16, 10
+    size = 2 * n * Hkv * page * D       # bytes of a cache: 40960
+    row = 2 * Hkv * D                   # of a row: 256
+
+    def call(k, v=0x900000, kc=0x100000, vc=0x200000):
+        return ds.lib().dspark_cache_append(rows, Hkv, D, ds.BF16, page, n, P(k), P(v), 128, 128, P(0x1000),
+                                            None, P(kc), P(vc), Hkv * page * D, page * D, D, None, None)
+
+    for base in (0x100000, 0x200000):
+        for at in (base - rows * row + 16, base, base + 4096, base + size - 16):
+            assert call(at) == ds.EINVAL, hex(at)
+            assert call(0x900000, v=at) == ds.EINVAL, hex(at)
