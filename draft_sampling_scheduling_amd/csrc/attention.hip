@@ -166,7 +166,10 @@ struct Fit {
   static constexpr int TILE = 2 * kTok * D * (kBf ? 2 : 4);  // bytes of a K and a V tile
   static constexpr int STAGES = NR == 1 ? (kBf && D == 64 ? 2 : 1) : 2;
   static constexpr int LDS = (NR == 1 ? 2 : 1) * STAGES * TILE;
-  // two waves a SIMD, but for float rows of 128, whose one wave takes its registers
+  // two waves a SIMD, but for float rows of 128, whose one wave takes its registers.  (bf16 of 64
+  // has registers, and from 33 rows on LDS, for three: full row tiles gain, 64 requests of 72 rows
+  // 98 -> 92 us, 2048 rows behind 4096 tokens 221 -> 209, others lose, 64 of 45 rows over 100 to
+  // 800 tokens 27.5 -> 28.2, over 500 to 4000 78.1 -> 78.8.)
   static constexpr int PER_SIMD = !kBf && D == 128 ? 1 : 2;
   static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
 };
@@ -355,9 +358,12 @@ struct AttWave {
   __device__ __forceinline__ void values(uint32_t vs, const f32x16& sc) {
     if constexpr (L::kBf) {
       // 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens of it, rounded to
-      // bf16 (each weight off by 2^-8 of itself at most, as o is when stored); V's fragment is
-      // two transposing reads of 4 tokens x 16 d.  Rows 8 apart share a swizzle, so a lane has
-      // one address per 32 d and the rest are immediates.
+      // bf16 (each weight off by 2^-8 of itself at most, as o is when stored: o's error against 64
+      // bits is 0.0023 of its norm, one rounding's 0.0017).  The weights' remainders in products of
+      // their own would leave that one rounding, and take 861 for 700 us for a prompt of 8192
+      // rows, 447 for 440 for 256 requests of 512 to 4096 tokens, 46 for 44.5 for 64 trees.  V's
+      // fragment is two transposing reads of 4 tokens x 16 d.  Rows 8 apart share a swizzle, so a
+      // lane has one address per 32 d and the rest are immediates.
       const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
       const uint32_t vrow = here(vs + r0 * L::RB + (j & 1) * 8);
       const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ L::vswz(r0)) << 4);
@@ -619,11 +625,14 @@ struct AttWave {
 // tile's wait, the merge of the waves, the output), which no tokens stand for; all lists, head
 // after head, are one row of units, cut evenly: workgroup b begins at unit begin(b).  A cut
 // costs the later piece's set-up and the join; moving cuts to a near end lost more in balance
-// than it saved in joins (120 requests of 180 to 254 tokens, lists of 6 to 8 rounds: 32 us with
-// these kept whole, 27 cut), unless no list need be cut at all: block tables of no more than
-// kWhole rounds leave every list whole and launch no join (4 requests of up to 204 tokens, float:
-// 17 against 19 us).  A list that is cut has its pieces
-// in the workspace; the first workgroup that begins inside one says so in joint[b].
+// than it saved in joins (120 requests of 180 to 254 tokens in tables of more, lists of 6 to 8
+// rounds: 32 us with these kept whole, 27 cut), unless no list need be cut at all: block tables of
+// no more than kWhole rounds leave every list whole and launch no join.  Kernels alone, whole
+// against cut, bf16, tables of 256 tokens, 32 heads on 8: 32 requests 15.4 and 17.1 us, 120 23.8
+// and 27.5, 512 79 and 84; 17 rows, tables of 128: 32 requests 16.8 and 24.2.  In float a list's
+// products take longer, and it is the call, a launch shorter, that gains: 4 requests of up to 204
+// tokens 17 against 18 to 20 us a call, 19 against 13 captured in a graph.  A list that is cut has
+// its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
 constexpr int kWhole = 4;
 
 // a / b, both at least 0; a 64-bit division is some hundred instructions
