@@ -6,12 +6,13 @@
 // few requests): it scans the history once, into a word per id in LDS (times generated, seen in
 // the prompt), and from there a thread keeps the words of its ids in registers; from one row to
 // the next they change only by the drafted token between them (in a tree: by the tokens above one
-// of the two nodes and not the other).  A row's operands load while the row before it is worked on.  Ids that nothing touches are copied as they are. Measured: 256
-// requests, 151936 ids, bf16, up to nine rows each (786 MB): 154 to 170 us, 4.6 to 5.1 TB/s, a
-// copy's rate; loads that were not all issued a row ahead (the mask's bits behind the next row's
-// logits) had made it 257 us.  4 requests of 1024 ids, up to five rows: 5.8 us, the trips to
-// memory.  Trees: 256 requests of nine nodes as long as chains; 16 of 65 nodes, 32000 ids, 52 us
-// where chains take 32, for the tokens turned over between rows.
+// of the two nodes and not the other).  A row's operands load while the row before it is worked
+// on.  Ids that nothing touches are copied as they are.  Measured: 256 requests, 151936 ids, bf16,
+// up to nine rows each (786 MB): 154 to 170 us, 4.6 to 5.1 TB/s, a copy's rate; loads that were not
+// all issued a row ahead (the mask's bits behind the next row's logits) had made it 257 us.  4
+// requests of 1024 ids, up to five rows: 5.8 us, the trips to memory.  Trees: 256 requests of nine
+// nodes as long as chains; 16 of 65 nodes, 32000 ids, 52 us where chains take 32, for the tokens
+// turned over between rows.
 #include <type_traits>
 
 #include "target.h"

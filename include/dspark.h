@@ -255,10 +255,11 @@ int dspark_schedule(int R, int gamma, const float *c, const float *c_lag, int R_
  * If some j* <= L is rejected: emit x_1..x_{j*-1}, then a two-level Gumbel sample of
  *   max(0, p_j* - q_j*) (streams 3, 4; if that mass is 0 in floating point, of p_j*).
  * Otherwise: emit x_1..x_L, then a sample of target row L+1 (the bonus; streams 5, 6).
- * A target row whose logits are all -inf (a grammar mask that allows nothing) has p = 0 at
- *   every id: its drafted token is rejected, its c_star is 0, and where it is the row to draw
- *   the last token from, -1 is emitted in that token's place (y[q][n_acc[q]] and x_next[q]: the
- *   request can go no further) and DSPARK_FAULT_EMPTY is set; all other outputs hold as ever.
+ * A target row whose logits are all -inf (a grammar mask that allows nothing), or all as low as
+ *   the type's lowest value, has p = 0 at every id: its drafted token is rejected, its c_star is 0,
+ *   and where it is the row to draw the last token from, -1 is emitted in that token's place
+ *   (y[q][n_acc[q]] and x_next[q]: the request can go no further) and DSPARK_FAULT_EMPTY is set;
+ *   all other outputs hold as ever.
  * Inputs
  *   target [R][gamma+1][V] dt   target logits for positions 1..gamma+1
  *   U [R][gamma][V] dt, W2t [V][r] dt      as in draft

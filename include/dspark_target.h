@@ -114,10 +114,11 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row
  * does not see (stale, infinite or NaN) does not reach it.
  * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.
- * D in {64, 128}; Hq a multiple of Hkv; rows * Hq <= 2^31 - 1024; dt as the cache's; strides multiples of 16 bytes, pointers 16-byte
- * aligned.  ctx + n beyond max_pages pages, ctx < 0 or row_off out of order are clamped
- * (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0 (DSPARK_FAULT_PAGE); with
- * anc, nodes past 64 are seen by nobody but through ctx (DSPARK_FAULT_TREE).
+ * D in {64, 128}; Hq a multiple of Hkv; rows * Hq <= 2^31 - 1024; dt as the cache's; strides
+ * multiples of 16 bytes, pointers 16-byte aligned.  ctx + n beyond max_pages pages, ctx < 0 or
+ * row_off out of order are clamped (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0
+ * (DSPARK_FAULT_PAGE); with anc, nodes past 64 are seen by nobody but through ctx
+ * (DSPARK_FAULT_TREE).
  * Workspace: ws_bytes >= dspark_tree_attention_workspace_bytes(...) (0: sizes out of range).
  * ------------------------------------------------------------------------------------ */
 size_t dspark_tree_attention_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
@@ -154,7 +155,7 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
  * out may be logits itself where row_off is NULL and row_stride is V, and overlaps it in no
  * other way.
  * A row whose mask allows nothing is all -inf (dspark_verify rejects the token drafted there,
- *   emits -1 where it had to draw from that row, and sets DSPARK_FAULT_EMPTY).
+ * emits -1 where it had to draw from that row, and sets DSPARK_FAULT_EMPTY).
  * Faults: ell outside [0, gamma] (DSPARK_FAULT_LEN, clamped); a row that is
  *   not the request's or outside [0, rows) (DSPARK_FAULT_LEN, its out row is left as it was:
  *   what becomes of requests that the plan gave no rows); hist_len outside [0, hist_stride],

@@ -90,6 +90,31 @@ def test_rows_that_allow_nothing(gamma, V, dtype):
     assert np.isfinite(got["c_star"][~np.isnan(plain["c_star"])]).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_rows_of_the_lowest_value(dtype):
+    """A mask written as the type's lowest value: whole rows of it count as empty, and beside real
+    logits those ids are never drawn."""
+    import draft_sampling_scheduling_amd as ds
+    R, gamma, V = 6, 3, 8200
+    _, U, W2t, d, lg = drafted(R, gamma, V, dtype)
+    low = torch.finfo(dtype).min
+    ell = torch.full((R,), gamma, dtype=I32, device="cuda:0")
+    lg[0, 0] = low
+    lg[1] = low
+    lg[1, :, ::3] = -float("inf")
+    lg[2:, :, 5000:] = low                 # whole blocks of it, and a window's
+    lg[2:, :, :64] = low
+    st = torch.zeros(1, dtype=I32, device="cuda:0")
+    v = ds.verify(lg, U, W2t, d["bias_rows"], d["x"], d["lse"], d["logit_x"], ell, 5, 1, status=st)
+    v = {k: N(x) for k, x in v.items()}
+    assert int(st) == ds.FAULT_EMPTY
+    assert v["n_acc"][:2].tolist() == [0, 0] and (v["y"][:2] == -1).all() and (v["x_next"][:2] == -1).all()
+    assert v["c_star"][0, 0] == 0 and (v["c_star"][1] == 0).all() and np.isfinite(v["c_star"]).all()
+    for q in range(2, R):
+        y = v["y"][q, :v["n_acc"][q] + 1]
+        assert ((y >= 64) & (y < 5000)).all(), (q, y)
+
+
 def T32(x):
     return torch.tensor(x, dtype=I32, device="cuda:0")
 
