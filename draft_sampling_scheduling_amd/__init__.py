@@ -588,7 +588,8 @@ def sps_interpolate(B_list, sps_at, B0, B1):
 # the target's side of a cycle (include/dspark_target.h): resolved on first use, so that
 # importing this package stays free of torch
 # ----------------------------------------------------------------------------------------
-_TARGET = ("cache_plan", "cache_plan_workspace_bytes", "cache_append", "tree_attention",
+_TARGET = ("cache_plan", "cache_plan_workspace_bytes", "cache_append", "qk_rope", "rope_append",
+           "cache_read", "tree_attention",
            "tree_attention_workspace_bytes", "target_logits", "cache_commit",
            "cache_commit_workspace_bytes", "TARGET_EXPORTS", "FAULT_PAGE", "FAULT_TREE",
            "FAULT_PARAM", "MAX_TREE_NODES")

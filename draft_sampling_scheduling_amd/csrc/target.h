@@ -87,6 +87,18 @@ inline bool pages_ok(int page_size, int64_t pages) {
 // element strides whose byte distances keep 16-byte loads aligned
 inline bool stride_ok(int64_t s, size_t esz) { return s >= 0 && (s * (int64_t)esz) % 16 == 0; }
 
+// Head size and strides (in bytes) of a 4-bit cache: codes in pieces of 16 bytes, and a token's
+// scale bytes of one head, D / 32 for its keys and as many for its values, in one piece.
+inline bool cache4_ok(int D, int64_t page, int64_t head, int64_t tok, int64_t s_page, int64_t s_head,
+                      int64_t s_tok) {
+  if (D != 64 && D != 128) return false;
+  for (int64_t s : {page, head, tok})
+    if (!stride_ok(s, 1)) return false;
+  for (int64_t s : {s_page, s_head, s_tok})
+    if (s < 0 || s % (D / 16) != 0) return false;
+  return true;
+}
+
 // whether two arrays of so many bytes share any
 inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;

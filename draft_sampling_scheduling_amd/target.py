@@ -1,17 +1,22 @@
 """The target's side of a decode cycle: binding of include/dspark_target.h.
 
   cache_plan      rows, pages and cache slots of a step, from lengths on the device
+  qk_rope         norms of queries and keys for each head, and the position rotation
+  rope_append     the same on the way into the paged cache
   cache_append    the step's keys and values into the paged cache
   tree_attention  the step's rows (a chain, a tree, a piece of a prompt) over the cache
   target_logits   penalties, biases and grammar masks, into the layout verify() reads
   cache_commit    after verify(): accepted path moved, lengths advanced, pages given back
+  cache_read      tokens back out of a cache of 4 bits
 
 verify() takes the plan's row_off, so that requests the plan could not serve are left out.
 As in the other calls, tensors are device tensors, work goes to the current stream (of the
 tensors' device), bad shapes and types raise before anything is enqueued, and faults in the
 data set bits of `status` ([1] int32, nullable).  A cache is [n_pages][Hkv][page_size][D]
 with any strides over contiguous rows of D: transpose(1, 2) of [n_pages][page_size][Hkv][D]
-serves too.
+serves too.  One of 4 bits is k_cache and v_cache [n_pages][Hkv][page_size][D // 2] uint8 (two
+elements a byte) with scales [n_pages][Hkv][page_size][2][D // 32] uint8 (a power of two for 32
+elements of the keys, then of the values), which the calls take as scales=.
 """
 from __future__ import annotations
 
@@ -22,12 +27,15 @@ import torch
 FAULT_PAGE, FAULT_TREE, FAULT_PARAM = 8, 16, 32
 MAX_TREE_NODES = 65
 TARGET_EXPORTS = ("dspark_cache_plan_workspace_bytes", "dspark_cache_plan",
-                  "dspark_cache_append", "dspark_tree_attention_workspace_bytes",
+                  "dspark_cache_append", "dspark_qk_rope", "dspark_rope_append",
+                  "dspark_cache4_append", "dspark_cache4_read",
+                  "dspark_tree_attention_workspace_bytes",
                   "dspark_tree_attention", "dspark_target_logits",
                   "dspark_target_logits_tree", "dspark_verify_rows",
                   "dspark_cache_commit_workspace_bytes", "dspark_cache_commit")
 
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
+_U8 = torch.uint8
 
 
 def set_argtypes(L):
@@ -39,6 +47,14 @@ def set_argtypes(L):
     L.dspark_cache_plan.argtypes = ([i] * 6 + [vp] * 7 + [i] + [vp] * 7 + [sz, vp])
     L.dspark_cache_append.argtypes = ([i] * 6 + [vp] * 2 + [i64] * 2 + [vp] * 4 + [i64] * 3 +
                                       [vp] * 2)
+    d = C.c_double
+    rope = [vp, vp, i, vp, vp, d, vp]  # position, rope, n_pos, the norms, eps, n_rows
+    L.dspark_qk_rope.argtypes = [i] * 7 + [vp, i64] * 2 + rope + [vp, i64] * 2 + [vp] * 2
+    L.dspark_rope_append.argtypes = ([i] * 9 + [vp, i64] * 3 + [vp] + rope + [vp, i64] + [vp] * 2 +
+                                     [i64] * 3 + [vp] * 2)
+    L.dspark_cache4_append.argtypes = ([i] * 9 + [vp, i64] * 3 + [vp] + rope + [vp, i64] + [vp] * 2 +
+                                       [i64] * 3 + [vp] + [i64] * 3 + [vp] * 2)
+    L.dspark_cache4_read.argtypes = ([i] * 7 + [vp] * 4 + [i64] * 4 + [vp] + [i64] * 4 + [vp] * 4)
     L.dspark_tree_attention_workspace_bytes.argtypes = [i] * 6
     L.dspark_tree_attention_workspace_bytes.restype = sz
     L.dspark_tree_attention.argtypes = ([i] * 9 + [vp, i64] + [vp] * 2 + [i64] * 3 + [vp] * 4 +
@@ -171,6 +187,29 @@ def _cache(k_cache, v_cache, dev, dims):
     return k_cache.data_ptr(), v_cache.data_ptr(), shape, st[:dims - 1]
 
 
+def _scales(scales, dev, lead, D):
+    """Address and leading strides of the scales of a 4-bit cache (`lead`: its leading sizes)."""
+    shape = (*lead, 2, D // 32)
+    if (not isinstance(scales, torch.Tensor) or scales.dtype is not _U8 or scales.shape != shape or
+            scales.get_device() != dev.index):
+        _refuse(scales, "scales", dev, shape, _U8)
+    st = _strides(scales, 2)
+    if st is None:
+        raise ValueError("a token's scales must be dense")
+    return scales.data_ptr(), st
+
+
+def _cache4(k_cache, v_cache, scales, dev, dims):
+    """_cache of a 4-bit cache and its scales: addresses, shape (with D), strides."""
+    kp, vp, shape, st = _cache(k_cache, v_cache, dev, dims)
+    if k_cache.dtype is not _U8:
+        raise TypeError(f"k_cache must be uint8 beside scales, got {k_cache.dtype}")
+    shape = (*shape[:-1], 2 * shape[-1])
+    if shape[-1] not in (64, 128):
+        raise ValueError(f"a 4-bit cache has heads of 64 or 128 elements, got {shape[-1]}")
+    return kp, vp, shape, st, *_scales(scales, dev, shape[:-1], shape[-1])
+
+
 _fns = {}
 
 
@@ -262,10 +301,15 @@ def cache_plan(lens, ctx, held, table, free_pages, n_free, page_size, *, rows, e
     return out
 
 
-def cache_append(k, v, k_cache, v_cache, slot, *, n_rows=None, status=None):
+def cache_append(k, v, k_cache, v_cache, slot, *, scales=None, n_rows=None, status=None):
     """Row i's keys and values (k, v [rows][Hkv][D], rows any stride apart, as slices of a
     fused projection are) into cache slot slot[i] (-1: skipped).  n_rows: a device int32 [1];
-    rows at and behind it are skipped (a plan's row_off[-1:])."""
+    rows at and behind it are skipped (a plan's row_off[-1:]).  scales: the cache's, if it is one
+    of 4 bits."""
+    if scales is not None:
+        rope_append(None, k, v, k_cache, v_cache, slot, None, None, scales=scales, n_rows=n_rows,
+                    status=status)
+        return
     dev = _device(k, "k")
     kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
     rows = _dims(k, "k", 3)[0]
@@ -275,6 +319,117 @@ def cache_append(k, v, k_cache, v_cache, slot, *, n_rows=None, status=None):
     _call(dev, "dspark_cache_append", rows, Hkv, D, dt, page, P, a, b, ks, vs,
           _chk(slot, "slot", dev, (rows,), _I32), _opt(n_rows, "n_rows", dev, (1,), _I32), kp, vp,
           *st, _opt(status, "status", dev, (1,), _I32))
+
+
+def _rope_rows(q, k, dev, D):
+    """Rows, dtype, and head counts, addresses and row strides of q and k (either may be None)."""
+    some, name = (q, "q") if q is not None else (k, "k")
+    rows, dtype = _dims(some, name, 3)[0], some.dtype
+    _dt(some, name)
+    Hq = 0 if q is None else _dims(q, "q", 3)[1]
+    Hkv = 0 if k is None else _dims(k, "k", 3)[1]
+    qp, qs = (None, 0) if q is None else _rows(q, "q", dev, (rows, Hq, D), dtype)
+    kp, ks = (None, 0) if k is None else _rows(k, "k", dev, (rows, Hkv, D), dtype)
+    return rows, Hq, Hkv, dtype, qp, qs, kp, ks
+
+
+def _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows):
+    """rot, and the arguments from position to n_rows."""
+    if rope is None:
+        n_pos = rot = 0
+        pp = tp = None
+    else:
+        n_pos, rot = _dims(rope, "rope", 2)
+        pp, tp = _chk(position, "position", dev, (rows,), _I32), _chk(rope, "rope", dev, (n_pos, rot), _F32)
+    return rot, (pp, tp, n_pos, _opt(q_norm, "q_norm", dev, (D,), dtype),
+                 _opt(k_norm, "k_norm", dev, (D,), dtype), eps, _opt(n_rows, "n_rows", dev, (1,), _I32))
+
+
+def qk_rope(q, k, position, rope, *, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
+            n_rows=None, out=None, status=None):
+    """Queries q [rows][Hq][D] and keys k [rows][Hkv][D] (either may be None; rows any stride apart,
+    as slices of a fused projection are), each head divided by its root mean square and multiplied
+    by q_norm, k_norm [D] where given, then its pairs (i, i + rot // 2), or with interleaved
+    (2 i, 2 i + 1), turned by row position[i] of rope [n_pos][rot] float32 (rot // 2 cosines, then the
+    sines; None: nothing turns).  Rows at and behind n_rows (a device int32 [1]), and those whose
+    position is not in the table (FAULT_PARAM), are left alone.
+    Returns dict(q, k); a caller-supplied `out` may hold q and k themselves."""
+    dev = _device(k if q is None else q, "q")
+    D = _dims(k if q is None else q, "q", 3)[2]
+    rows, Hq, Hkv, dtype, qp, qs, kp, ks = _rope_rows(q, k, dev, D)
+    rot, a = _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows)
+    if out is None:
+        out = dict(q=None if q is None else torch.empty((rows, Hq, D), dtype=dtype, device=dev),
+                   k=None if k is None else torch.empty((rows, Hkv, D), dtype=dtype, device=dev))
+    qo, qos = (None, 0) if q is None else _rows(out["q"], "out['q']", dev, (rows, Hq, D), dtype)
+    ko, kos = (None, 0) if k is None else _rows(out["k"], "out['k']", dev, (rows, Hkv, D), dtype)
+    sp = _opt(status, "status", dev, (1,), _I32)
+    if rows == 0:
+        return out
+    _call(dev, "dspark_qk_rope", rows, Hq, Hkv, D, rot, interleaved, 1 if dtype is _BF16 else 0, qp, qs,
+          kp, ks, *a, qo, qos, ko, kos, sp)
+    return out
+
+
+def rope_append(q, k, v, k_cache, v_cache, slot, position, rope, *, scales=None, q_norm=None,
+                k_norm=None, eps=1e-6, interleaved=False, n_rows=None, out=None, status=None):
+    """qk_rope on the way into the cache: row i's keys, normed and turned, and its values as they are
+    into cache slot slot[i] (-1: skipped), its queries to `out` [rows][Hq][D] (default: a new tensor;
+    may be q itself), which is returned (None without q).  scales: the cache's, if it is one of
+    4 bits."""
+    dev = _device(k, "k")
+    D = _dims(k, "k", 3)[2]
+    rows, Hq, Hkv, dtype, qp, qs, kp, ks = _rope_rows(q, k, dev, D)
+    if scales is None:
+        kc, vc, shape, st = _cache(k_cache, v_cache, dev, 4)
+        name, more = "dspark_rope_append", ()
+        if k_cache.dtype is not dtype:
+            raise TypeError(f"k_cache has dtype {k_cache.dtype}, expected {dtype}")
+    else:
+        kc, vc, shape, st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 4)
+        name, more = "dspark_cache4_append", (scp, *sst)
+    P, _, page, _ = shape
+    if shape[1] != Hkv or shape[3] != D:
+        raise ValueError(f"k has {Hkv} heads of {D}, the cache {shape[1]} of {shape[3]}")
+    vp, vs = _rows(v, "v", dev, (rows, Hkv, D), dtype)
+    rot, a = _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows)
+    sl = _chk(slot, "slot", dev, (rows,), _I32)
+    if q is None:
+        out, qo, qos = None, None, 0
+    else:
+        if out is None:
+            out = torch.empty((rows, Hq, D), dtype=dtype, device=dev)
+        qo, qos = _rows(out, "out", dev, (rows, Hq, D), dtype)
+    sp = _opt(status, "status", dev, (1,), _I32)
+    _call(dev, name, rows, Hq, Hkv, D, rot, interleaved, 1 if dtype is _BF16 else 0, page, P, qp, qs, kp, ks,
+          vp, vs, sl, *a, qo, qos, kc, vc, *st, *more, sp)
+    return out
+
+
+def cache_read(k_cache, v_cache, scales, slot, *, dtype=_BF16, n_rows=None, out=None, status=None):
+    """Tokens of a 4-bit cache as the values they stand for: dict(k, v), [rows][Hkv][D] each for slots
+    slot [rows] (of caches with a leading layer dimension [layers][rows][Hkv][D]), in bfloat16 or
+    float32 (exact in both).  Rows of slot -1, and at and behind n_rows (a device int32 [1]), are
+    left as they were."""
+    dev = _device(k_cache, "k_cache")
+    layered = k_cache.dim() == 5
+    kc, vc, shape, st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 5 if layered else 4)
+    rows, = _dims(slot, "slot", 1)
+    want = (rows, shape[-3], shape[-1])
+    if layered:
+        want = (shape[0], *want)
+    else:
+        shape, st, sst = (1, *shape), (0, *st), (0, *sst)
+    if out is None:
+        out = dict(k=torch.empty(want, dtype=dtype, device=dev), v=torch.empty(want, dtype=dtype, device=dev))
+    _dims(out["k"], "out['k']", len(want))
+    kind = out["k"].dtype
+    ko, vo = _chk(out["k"], "out['k']", dev, want, kind), _chk(out["v"], "out['v']", dev, want, kind)
+    layers, P, Hkv, page, D = shape
+    _call(dev, "dspark_cache4_read", layers, rows, Hkv, D, _dt(out["k"], "out['k']"), page, P,
+          _chk(slot, "slot", dev, (rows,), _I32), _opt(n_rows, "n_rows", dev, (1,), _I32), kc, vc, *st, scp, *sst,
+          ko, vo, _opt(status, "status", dev, (1,), _I32))
+    return out
 
 
 def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt) -> int:

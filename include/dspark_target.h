@@ -5,7 +5,8 @@
  *
  *   dspark_schedule -> ell
  *   dspark_cache_plan          rows, pages and cache slots of this step, from ell on the device
- *   per layer: dspark_cache_append, dspark_tree_attention
+ *   per layer: dspark_rope_append (or dspark_cache_append where keys are turned already) and
+ *     dspark_tree_attention; with a cache of 4 bits dspark_cache4_append, dspark_tree_attention4
  *   dspark_target_logits[_tree] penalties, biases, grammar masks; packed rows -> verify's layout
  *   dspark_verify_rows -> n_acc (-1 for requests that the plan gave no rows)
  *   dspark_cache_commit        accepted path moved, lengths advanced, finished requests' pages back
@@ -29,6 +30,18 @@
  * table[q][t / page_size]; table is [R][max_pages] int32.  ctx[q] tokens of request q are
  * committed; the block's node i is token ctx[q] + i.  n_pages * page_size < 2^31 and
  * max_pages * page_size <= 2^30.  R <= 2^20 (dspark_target_logits: 65535).
+ *
+ * Cache of 4 bits.  k_cache and v_cache hold codes, D / 2 bytes a row, strides in bytes; scales
+ * holds D / 16 bytes for each token and head, the keys' D / 32 first, with strides of its own
+ * (bytes).  Element d is four bits of byte d / 2 (the low ones where d is even): a sign and 0, .5, 1,
+ * 1.5, 2, 3, 4, 6; times 2^(b - 127), b the byte of its 32 elements (255: NaN; 253 and 254, which
+ * nothing here writes, may read as NaN).  This is the E2M1 / E8M0 block format of the OCP
+ * microscaling specification.  D in {64, 128}; codes and their strides 16-byte aligned, scales'
+ * address too, its strides multiples of D / 16.
+ * Written are, for each 32 elements x, b = 127 + e with the smallest e in [-120, 125] of
+ * max|x| <= 7 * 2^e, and the codes nearest to x / 2^e, the even one of two, 6 past 6: no value is
+ * off by more than half a step (groups above 7 * 2^125 apart).  Where an x is infinite or NaN, b is
+ * 255 and the codes 0.
  */
 #ifndef DSPARK_TARGET_H
 #define DSPARK_TARGET_H
@@ -101,6 +114,66 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
                         const int32_t *slot, const int32_t *n_rows, void *k_cache,
                         void *v_cache, int64_t page_stride, int64_t head_stride,
                         int64_t tok_stride, int32_t *dev_status, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Norm and position rotation of a step's queries and keys.
+ *   x^ = x / sqrt(mean(x^2) + eps) * w      w = q_norm, k_norm [D] in dt (each NULL: x^ = x)
+ *   a' = a cos - b sin, b' = b cos + a sin  for the pairs (a, b) of x^'s first `rot` elements:
+ *        (i, i + rot/2), or (2i, 2i+1) with interleaved != 0; the rest as it is
+ * cos, sin: row position[i] of rope [n_pos][rot] float, rot/2 cosines, then rot/2 sines (rope NULL:
+ * nothing is turned, position is not read).  In float, rounded once.
+ * q, k rows of Hq, Hkv heads of D contiguous elements, q_row and k_row elements apart (either may
+ * be NULL); outputs the same, qo_row and ko_row apart: the inputs themselves (same address and
+ * stride), or memory that shares nothing with q, k and each other; the slices of a fused
+ * projection's rows count as apart.  n_rows (device, nullable): only the first *n_rows rows exist.
+ * A position outside [0, n_pos) leaves its row alone (DSPARK_FAULT_PARAM).
+ * D % 16 == 0, 16 <= D <= 256; rot % 16 == 0, 16 <= rot <= D; eps >= 0; strides multiples of 16
+ * bytes, pointers 16-byte aligned.
+ * ------------------------------------------------------------------------------------ */
+int dspark_qk_rope(int rows, int Hq, int Hkv, int D, int rot, int interleaved, dspark_dtype dt,
+                   const void *q, int64_t q_row, const void *k, int64_t k_row,
+                   const int32_t *position, const float *rope, int n_pos, const void *q_norm,
+                   const void *k_norm, double eps, const int32_t *n_rows, void *q_out,
+                   int64_t qo_row, void *k_out, int64_t ko_row, int32_t *dev_status,
+                   hipStream_t stream);
+
+/* dspark_qk_rope on the way into the cache: q to q_out (q NULL: none), k into slot slot[i] of
+ * k_cache, v beside it as it is.  Slots as in dspark_cache_append; a row without a slot (-1, or
+ * out of range) has its q turned all the same.  Rows, and q_out, lie outside the memory from the
+ * caches' first to their last element. */
+int dspark_rope_append(int rows, int Hq, int Hkv, int D, int rot, int interleaved,
+                       dspark_dtype dt, int page_size, int n_pages, const void *q, int64_t q_row,
+                       const void *k, int64_t k_row, const void *v, int64_t v_row,
+                       const int32_t *slot, const int32_t *position, const float *rope, int n_pos,
+                       const void *q_norm, const void *k_norm, double eps, const int32_t *n_rows,
+                       void *q_out, int64_t qo_row, void *k_cache, void *v_cache,
+                       int64_t page_stride, int64_t head_stride, int64_t tok_stride,
+                       int32_t *dev_status, hipStream_t stream);
+
+/* The same into a cache of 4 bits.  Keys are normed and turned in double: their codes are those of
+ * the formula's values. */
+int dspark_cache4_append(int rows, int Hq, int Hkv, int D, int rot, int interleaved,
+                         dspark_dtype dt, int page_size, int n_pages, const void *q,
+                         int64_t q_row, const void *k, int64_t k_row, const void *v,
+                         int64_t v_row, const int32_t *slot, const int32_t *position,
+                         const float *rope, int n_pos, const void *q_norm, const void *k_norm,
+                         double eps, const int32_t *n_rows, void *q_out, int64_t qo_row,
+                         void *k_cache, void *v_cache, int64_t page_stride, int64_t head_stride,
+                         int64_t tok_stride, void *scales, int64_t s_page, int64_t s_head,
+                         int64_t s_tok, int32_t *dev_status, hipStream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Tokens of a 4-bit cache as values: k, v [layers][rows][Hkv][D] dense, in dt, row i slot slot[i] of
+ * every layer (layer strides in bytes; slots and n_rows as in dspark_cache_append, a row without a
+ * slot is left as it was).  Exact in either type.  k and v share no memory with each other or with
+ * the cache.
+ * ------------------------------------------------------------------------------------ */
+int dspark_cache4_read(int layers, int rows, int Hkv, int D, dspark_dtype dt, int page_size,
+                       int n_pages, const int32_t *slot, const int32_t *n_rows,
+                       const void *k_cache, const void *v_cache, int64_t layer_stride,
+                       int64_t page_stride, int64_t head_stride, int64_t tok_stride,
+                       const void *scales, int64_t s_layer, int64_t s_page, int64_t s_head,
+                       int64_t s_tok, void *k, void *v, int32_t *dev_status, hipStream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Attention of a step's rows over the paged cache (their own keys and values appended).
