@@ -9,7 +9,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libdspark.so")
 SOURCES = ["draft.hip", "schedule.hip", "verify.hip", "sts.hip", "train.hip", "driver.hip", "sps.hip",
-           "layout.hip", "probe.hip", "cache.hip", "attention.hip", "logits.hip", "rope.hip"]
+           "layout.hip", "probe.hip", "cache.hip", "attention.hip", "attention4.hip",
+           "logits.hip", "rope.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

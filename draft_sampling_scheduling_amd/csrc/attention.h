@@ -593,6 +593,46 @@ static inline bool att_dims_ok(int R, int rows, int Hq, int Hkv, int D, dspark_d
          (int64_t)rows * Hq <= ((int64_t)1 << 31) - 1024;  // ends of row tiles in 31 bits
 }
 
+// The arguments that the entry points share (not the cache's strides), checked and taken over.
+static inline int att_args(AttParams& p, int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt, int page_size,
+                           int max_pages, int n_pages, const void* q, int64_t q_row, const void* k_cache,
+                           const void* v_cache, const int32_t* table, const int32_t* ctx, const int32_t* row_off,
+                           const uint64_t* anc, float scale, void* o, float* lse, int32_t* dev_status, void* ws) {
+  const size_t e = dt == DSPARK_BF16 ? 2 : 4;
+  if (max_pages < 1 || !pages_ok(page_size, n_pages) || !table_ok(page_size, max_pages) || !(scale > 0.0f) ||
+      !(scale * kLog2e <= FLT_MAX) || !stride_ok(q_row, e))
+    return DSPARK_EINVAL;
+  if (R == 0 || rows == 0) return DSPARK_OK;
+  if (!q || !k_cache || !v_cache || !table || !ctx || !row_off || !o || !ws || !aligned16(q) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(ws))
+    return DSPARK_EINVAL;
+  // a row's heads may be read after another's output is written
+  const size_t row_bytes = (size_t)Hq * D * e;
+  if (overlap(q, (size_t)(rows - 1) * q_row * e + row_bytes, o, rows * row_bytes)) return DSPARK_EINVAL;
+  p.R = R;
+  p.rows = rows;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.inv_g = p.G > 1 ? ~(uint64_t)0 / p.G + 1 : 0;
+  p.lg = log2_of(page_size);
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.q = q;
+  p.q_row = q_row;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.table = table;
+  p.ctx = ctx;
+  p.row_off = row_off;
+  p.anc = anc;
+  p.scale = scale;
+  p.o = o;
+  p.lse = lse;
+  p.status = dev_status;
+  return DSPARK_OK;
+}
+
 template <class W>
 static int att_launch(typename W::Params p, hipStream_t stream) {
   using F = typename W::F;

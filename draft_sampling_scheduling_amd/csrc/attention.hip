@@ -514,47 +514,17 @@ extern "C" int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, ds
                                      const int32_t* row_off, const uint64_t* anc, float scale,
                                      void* o, float* lse, int32_t* dev_status, void* ws,
                                      size_t ws_bytes, hipStream_t stream) {
-  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || max_pages < 1 || !pages_ok(page_size, n_pages) ||
-      !table_ok(page_size, max_pages) || !(scale > 0.0f) ||
-      !(scale * kLog2e <= FLT_MAX))
-    return DSPARK_EINVAL;
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;
-  if (!stride_ok(q_row, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||
+  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||
       !stride_ok(tok_stride, e) || tok_stride > (1 << 24))
     return DSPARK_EINVAL;
-  if (R == 0 || rows == 0) return DSPARK_OK;
-  if (!q || !k_cache || !v_cache || !table || !ctx || !row_off || !o || !ws || !aligned16(q) ||
-      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned16(ws))
-    return DSPARK_EINVAL;
-  // a row's heads may be read after another's output is written
-  const size_t row_bytes = (size_t)Hq * D * e;
-  if (overlap(q, (size_t)(rows - 1) * q_row * e + row_bytes, o, rows * row_bytes))
-    return DSPARK_EINVAL;
   AttParams p{};
-  p.R = R;
-  p.rows = rows;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.G = Hq / Hkv;
-  p.inv_g = p.G > 1 ? ~(uint64_t)0 / p.G + 1 : 0;
-  p.lg = log2_of(page_size);
-  p.max_pages = max_pages;
-  p.n_pages = n_pages;
-  p.q = q;
-  p.q_row = q_row;
-  p.k = k_cache;
-  p.v = v_cache;
+  const int rc = att_args(p, R, rows, Hq, Hkv, D, dt, page_size, max_pages, n_pages, q, q_row, k_cache,
+                          v_cache, table, ctx, row_off, anc, scale, o, lse, dev_status, ws);
+  if (rc != DSPARK_OK || R == 0 || rows == 0) return rc;
   p.page_b = page_stride * (int64_t)e;
   p.head_b = head_stride * (int64_t)e;
   p.tok_b = tok_stride * (int64_t)e;
-  p.table = table;
-  p.ctx = ctx;
-  p.row_off = row_off;
-  p.anc = anc;
-  p.scale = scale;
-  p.o = o;
-  p.lse = lse;
-  p.status = dev_status;
   if (ws_bytes < att_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
   return att_variant(R, rows, p.G, D, dt, [&](auto v) {
     return att_launch<AttWave<typename decltype(v)::T, decltype(v)::D, decltype(v)::NR>>(p, stream);

@@ -1,0 +1,363 @@
+// attention4.hip -- attention of a step's rows over a paged cache held in 4 bits.
+//
+// The products, the softmax and the cutting of the work are attention.h's.  What a cache of 4 bits
+// changes is how K and V reach the matrix cores: their values, E2M1 times a power of two, are bf16
+// numbers as they are (two bits of mantissa), so gfx950's conversions, two elements an instruction,
+// the power included, make exact operands of them, and
+//   S^T = K Q^T      O^T += V^T P^T
+// are bf16 products whatever the queries' type: bf16 queries are one term, float ones the sum of three
+// bf16 terms of 8 bits each, exactly, and so are the weights P beside float queries.
+//
+// An element is 17/32 bytes (scales included), a quarter of bf16's, so at few rows HBM wants a
+// tile of 32 tokens in a quarter of the time, and the vector work of a tile (64 conversions a
+// lane at D = 128, and the softmax) is what has to fit into it.
+//   - K goes from memory to registers to the product: a lane holds half of a token's head, and as a sum
+//     over d may be taken in any order, the queries are loaded to match.
+//   - V needs tokens where memory has d, so it passes through LDS as bf16, by transposing reads.
+#include "attention.h"
+#include "fp4.h"
+
+namespace dspark {
+
+struct Att4Params : AttParams {
+  const uint8_t* scales;
+  int64_t s_page, s_head, s_tok;
+};
+
+// How a variant sits on a CU.  NR 1: the two waves of a workgroup take 32 tokens each and merge at
+// the end.  TERMS: bf16 terms of a query and a weight.
+template <int D, int NR, int TERMS>
+struct Fit4 {
+  static constexpr bool kBf = TERMS == 1;  // the output's type, attention.h asks
+  static constexpr int WAVES = 2;
+  static constexpr int THREADS = WAVES * kWave;
+  static constexpr int ROUND = 2 * kTok;
+  static constexpr int SETUP = 3;
+  static constexpr int TILE = kTok * D * 2;  // V as bf16
+  static constexpr int MERGE = 2 * (D / 64 * 16 + 2) * 64 * 4;
+  static constexpr int LDS = WAVES * TILE > MERGE ? WAVES * TILE : MERGE;
+  static constexpr int PER_SIMD = TERMS == 1 || D == 64 ? 2 : 1;
+  static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
+};
+
+// What a lane holds of a tile: half h of token n's keys and values, and their powers.
+template <int D>
+struct Raw4 {
+  static constexpr int N = D / 64;  // 16-byte pieces of half a row
+  uint4 k[N], v[N];
+  uint2 s;  // the token's scale bytes: keys', then values'
+};
+
+template <int D, int NR_, int TERMS>
+struct Att4Wave : AttRows<D> {
+  using Params = Att4Params;
+  using Out = typename std::conditional<TERMS == 1, uint16_t, float>::type;
+  using F = Fit4<D, NR_, TERMS>;
+  static constexpr int kD = D, kNR = NR_;
+  static constexpr int ND = D / 32, KSTEPS = D / 16, RB = D * 2, WORDS = D / 16;
+
+  using B = AttRows<D>;
+  using B::h;
+  using B::l;
+  using B::lane;
+  using B::len;
+  using B::n;
+  using B::node;
+  using B::o;
+  using B::see;
+  using B::seen;
+  const Att4Params& p;
+  uint32_t base;            // LDS of its V tile
+  // segment
+  const char *kh, *vh;      // cache bases of the head
+  const uint8_t* sh;
+  const int32_t* pages;     // the request's block table
+  int last_page;            // page of the last token
+  u32x4 qf[TERMS][KSTEPS];
+
+  __device__ __forceinline__ Att4Wave(const Att4Params& p_, int wave, uint32_t lds)
+      : B(p_), p(p_), base(lds + wave * F::TILE), wave_(wave) {}
+  int wave_;
+
+  // V's tile: row t is token t, 16-byte chunk c of it at chunk c ^ swz(t).  A write takes one chunk
+  // of 32 rows, a transposing read 4 neighbouring chunks of 4 rows; both spread over the banks.
+  static __device__ __forceinline__ int swz(int t) {
+    return D == 128 ? (t & 3) << 2 | ((t >> 2) & 3) : ((t >> 1) & 1) << 2 | ((t >> 2) & 3);
+  }
+
+  // page of the lane's token of tile t0 (past the last token, the last one's page)
+  __device__ __forceinline__ int page_of(int t0) const {
+    const int i = (t0 + n) >> p.lg;
+    return pages[i < last_page ? i : last_page];
+  }
+
+  // The loads of tile t0.  Rows past the last token are read inside its page, and are never used.
+  __device__ __forceinline__ void load(int t0, int pg, Raw4<D>& x) const {
+    if (pg < 0 || pg >= p.n_pages) {
+      raise_fault(p.status, DSPARK_FAULT_PAGE);
+      pg = 0;
+    }
+    const uint32_t tok = (uint32_t)(t0 + n) & ((1u << p.lg) - 1);
+    const uint64_t at = (uint64_t)(uint32_t)pg * (uint64_t)p.page_b + (uint64_t)tok * (uint32_t)p.tok_b + h * (D / 4);
+    const uint4* k = reinterpret_cast<const uint4*>(kh + at);
+    const uint4* v = reinterpret_cast<const uint4*>(vh + at);
+#pragma unroll
+    for (int i = 0; i < Raw4<D>::N; ++i) {
+      x.k[i] = k[i];
+      x.v[i] = v[i];
+    }
+    const uint8_t* s = sh + (uint64_t)(uint32_t)pg * (uint64_t)p.s_page + (uint64_t)tok * (uint32_t)p.s_tok;
+    if constexpr (D == 128)
+      x.s = *reinterpret_cast<const uint2*>(s);
+    else
+      x.s.x = *reinterpret_cast<const uint32_t*>(s);
+  }
+  // byte of the group that 8-element piece w of the lane's half lies in
+  static __device__ __forceinline__ uint32_t byte_of(const Raw4<D>& x, int h, bool values, int w) {
+    if (D == 128) return ((values ? x.s.y : x.s.x) >> (16 * h + 8 * (w / 4))) & 255u;
+    return (x.s.x >> (16 * values + 8 * h)) & 255u;
+  }
+
+  // S^T of a tile: step s takes d = 8 s .. 8 s + 7 of either half
+  __device__ __forceinline__ void scores(const Raw4<D>& x, f32x16& sc) const {
+    sc = f32x16{};
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(x.k);
+      const uint4 f = fp4_bf16x8(w[s], fp4_scale(byte_of(x, h, false, s)));
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t)
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f),
+                                                     __builtin_bit_cast(bf16x8, qf[t][s]), sc, 0, 0, 0);
+    }
+  }
+
+  // V of a tile, as bf16, to LDS.  EDGE: a token behind the last, and a group that reads NaN, are 0
+  // there (0 * NaN is none); sick[dt] has a bit for each of the 32 tokens whose group dt was NaN.
+  template <bool EDGE>
+  __device__ __forceinline__ void stage(int t0, const Raw4<D>& x, uint32_t (&sick)[ND]) const {
+    const uint32_t row = base + n * RB, c0 = h * (D / 16) ^ swz(n);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
+    if (EDGE) {
+#pragma unroll
+      for (int g = 0; g < ND; ++g) sick[g] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < KSTEPS; ++i) {
+      uint32_t code = w[i], byte = byte_of(x, h, true, i);
+      if (EDGE) {
+        const bool behind = t0 + n >= len, odd = byte >= 253;
+        if (i % 4 == 0) {
+          const uint64_t who = __ballot(odd && !behind);  // halves have different groups
+          const int g = i / 4;
+          sick[g] |= (uint32_t)who;
+          sick[ND / 2 + g] |= (uint32_t)(who >> 32);
+        }
+        code = behind || odd ? 0 : code;
+        byte = behind || odd ? 127 : byte;
+      }
+      lds_put<u32x4>(row + ((c0 ^ i) << 4), __builtin_bit_cast(u32x4, fp4_bf16x8(code, fp4_scale(byte))));
+    }
+  }
+
+  // O^T += V^T P^T, 16 tokens a step: registers 8 st .. 8 st + 7 are the lane's 8 tokens of it.  With
+  // bf16 queries the weights are rounded to bf16, each off by 2^-8 of itself at most, as o is when
+  // stored; with float ones they are three terms.
+  __device__ __forceinline__ void values(f32x16& sc) {
+    const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
+    const uint32_t vrow = here(base + r0 * RB + (j & 1) * 8);
+    const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ swz(r0)) << 4);
+#pragma unroll
+    for (int st = 0; st < 2; ++st) {
+      union {
+        s16x4 half[2];
+        bf16x8 all;
+      } a[ND];
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)  // (rows 8 apart differ in one bit of the swizzle)
+          a[dt].half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (DSPARK_LDS s16x4*)(uintptr_t)(vrow + (vx ^ (uint32_t)(dt << 6 | b << 5)) + 8 * (2 * st + b) * RB));
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t) {
+        bf16x8 pb;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float w = sc[8 * st + e];
+          if (TERMS == 1) {
+            pb[e] = (__bf16)w;
+          } else {
+            const float top = t + 1 < TERMS ? __uint_as_float(__float_as_uint(w) & 0xFFFF0000u) : w;
+            pb[e] = (__bf16)top;
+            sc[8 * st + e] = w - top;
+          }
+        }
+#pragma unroll
+        for (int dt = 0; dt < ND; ++dt)
+          o[dt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[dt].all, pb, o[dt], 0, 0, 0);
+      }
+    }
+  }
+
+  // the rows that see a token whose group was NaN have NaN there
+  __device__ __forceinline__ void spread(uint32_t vis, const uint32_t (&sick)[ND]) {
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt) {
+      // the half-waves hold 16 tokens of a row each
+      const uint32_t mine = vis & (sick[dt] >> 4 * h) & 0x0F0F0F0Fu;
+      const auto both = __builtin_amdgcn_permlane32_swap(mine, mine, false, false);
+      if (both[0] | both[1]) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) o[dt][r] = __uint_as_float(0x7FC00000u);
+      }
+    }
+  }
+
+  // rows m0 .. m0 + 31 of the request's M: d of half h in a row, 8 a step
+  __device__ __forceinline__ void queries(const AttReq& rq, int head, int m0, int M) {
+    const int mi = m0 + n;
+    const bool live = mi < M;
+    const int i = live ? node_of(p, mi) : 0, g = live ? group_of(p, mi) : 0;
+    const Out* src = static_cast<const Out*>(p.q) + (int64_t)(rq.a + i) * p.q_row +
+                     (int64_t)(head * p.G + g) * D + h * (D / 2);
+#pragma unroll
+    for (int s = 0; s < KSTEPS; ++s) {
+      if constexpr (TERMS == 1) {
+        qf[0][s] = u32x4{0, 0, 0, 0};
+        if (live) qf[0][s] = *reinterpret_cast<const u32x4*>(src + 8 * s);
+      } else {
+        float x[8];
+        if (live)
+          ld8(src + 8 * s, x);
+        else
+          for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+        // 8 bits at a time, the last rounded to what is left: the sum is the float.  An infinity or NaN
+        // is its first term's.
+        uint16_t t[TERMS][8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const bool odd = (__float_as_uint(x[e]) & 0x7F800000u) == 0x7F800000u;
+          float w = x[e];
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) {
+            const uint32_t u = __float_as_uint(w);
+            // (a NaN keeps a bit that stays)
+            t[k][e] = (uint16_t)(u >> 16) | (w != w ? 0x40 : 0);
+            w = odd ? 0.0f : w - __uint_as_float(u & 0xFFFF0000u);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[k][s][e] = (uint32_t)t[k][2 * e] | (uint32_t)t[k][2 * e + 1] << 16;
+      }
+    }
+    node = i;
+    see = p.anc ? p.anc[rq.a + i] : 0;
+  }
+
+  __device__ __forceinline__ void tile(int t0, const Raw4<D>& x) {
+    const bool edge = t0 + kTok > seen;
+    f32x16 sc;
+    scores(x, sc);
+    uint32_t vis = 0, sick[ND];
+    if (edge) {
+      vis = B::visible(t0);
+#pragma unroll
+      for (int r = 0; r < 16; ++r) sc[r] = vis & (1u << reg_row(r, 0)) ? sc[r] : -INFINITY;
+      stage<true>(t0, x, sick);
+    } else {
+      stage<false>(t0, x, sick);
+    }
+    B::weigh(sc);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    values(sc);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the tile's reads, before the next is written
+    if (edge) spread(vis, sick);
+  }
+
+  // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
+  __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr) {
+    const int M = rq.n * p.G;
+    B::begin_rows(rq, m0);
+    pages = p.table + (int64_t)q * p.max_pages;
+    kh = static_cast<const char*>(p.k) + head * p.head_b;
+    vh = static_cast<const char*>(p.v) + head * p.head_b;
+    sh = p.scales + head * p.s_head;
+    last_page = (len - 1) >> p.lg;
+    int end = uni(att_end(p, rq, m0 + NR_ * kRows));
+    end = end < (r0 + nr) * F::ROUND ? end : (r0 + nr) * F::ROUND;
+    const int first = r0 * F::ROUND + wave_ * kTok;
+    const int nt = first < end ? (end - first + F::ROUND - 1) / F::ROUND : 0;
+    queries(rq, head, m0, M);
+    if (nt > 0) {
+      Raw4<D> x;
+      load(first, page_of(first), x);
+      for (int k = 0; k < nt; ++k) {
+        const int t0 = first + k * F::ROUND;
+        Raw4<D> now = x;
+        if (k + 1 < nt) load(t0 + F::ROUND, page_of(t0 + F::ROUND), x);
+        tile(t0, now);
+      }
+    }
+    l = half_sum(l);
+  }
+};
+
+// ---------------------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------------------
+template <class F>
+static auto att4_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
+  if (dt == DSPARK_F32) return D == 64 ? f((Att4Wave<64, 1, 3>*)nullptr) : f((Att4Wave<128, 1, 3>*)nullptr);
+  return D == 64 ? f((Att4Wave<64, 1, 1>*)nullptr) : f((Att4Wave<128, 1, 1>*)nullptr);
+}
+
+static size_t att4_carve(Att4Params& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
+  return att4_variant(R, rows, G, D, dt, [&](auto* w) {
+    using W = std::remove_pointer_t<decltype(w)>;
+    return att_carve(p, ws, att_grid<typename W::F>(), kRows * W::kNR, W::kD);
+  });
+}
+
+}  // namespace dspark
+
+using namespace dspark;
+
+extern "C" size_t dspark_tree_attention4_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
+                                                         dspark_dtype dt) {
+  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) || R == 0) return 0;
+  Att4Params p{};
+  return att4_carve(p, nullptr, R, rows, Hq / Hkv, D, dt);
+}
+
+extern "C" int dspark_tree_attention4(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt,
+                                      int page_size, int max_pages, int n_pages, const void* q,
+                                      int64_t q_row, const void* k_cache, const void* v_cache,
+                                      int64_t page_stride, int64_t head_stride, int64_t tok_stride,
+                                      const void* scales, int64_t s_page, int64_t s_head, int64_t s_tok,
+                                      const int32_t* table, const int32_t* ctx, const int32_t* row_off,
+                                      const uint64_t* anc, float scale, void* o, float* lse,
+                                      int32_t* dev_status, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) ||
+      !cache4_ok(D, page_stride, head_stride, tok_stride, s_page, s_head, s_tok) || tok_stride > (1 << 24) ||
+      s_tok > (1 << 24))
+    return DSPARK_EINVAL;
+  Att4Params p{};
+  const int rc = att_args(p, R, rows, Hq, Hkv, D, dt, page_size, max_pages, n_pages, q, q_row, k_cache, v_cache,
+                          table, ctx, row_off, anc, scale, o, lse, dev_status, ws);
+  if (rc != DSPARK_OK || R == 0 || rows == 0) return rc;
+  if (!scales || !aligned16(scales)) return DSPARK_EINVAL;
+  p.page_b = page_stride;
+  p.head_b = head_stride;
+  p.tok_b = tok_stride;
+  p.scales = static_cast<const uint8_t*>(scales);
+  p.s_page = s_page;
+  p.s_head = s_head;
+  p.s_tok = s_tok;
+  if (ws_bytes < att4_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
+  return att4_variant(R, rows, p.G, D, dt, [&](auto* w) {
+    return att_launch<std::remove_pointer_t<decltype(w)>>(p, stream);
+  });
+}

@@ -431,6 +431,9 @@ struct CommitArgs {
   int layers, Hkv, chunks, n_pages;
   uint4 *k_cache, *v_cache;
   int64_t layer_stride, page_stride, head_stride, tok_stride;  // in 16-byte pieces
+  int words;         // 4 bytes of scales of a token and head (0: a cache without)
+  uint32_t* scales;
+  int64_t s_layer, s_page, s_head, s_tok;  // in words
   int32_t* status;
   CommitWs ws;
 };
@@ -505,30 +508,15 @@ __device__ __forceinline__ void commit_scan(const CommitArgs& p, const CommitWs&
   }
 }
 
-// The moves of request q in 256 of the 16-byte columns (layer, keys or values, head, piece of
-// D) of its tokens.  A thread owns its column, so the moves of one column are one thread's: a
-// batch of eight tokens is read before any of them is written, and since the path ascends
-// (its i-th node is at least i), no later batch reads a token that an earlier one wrote.
-__device__ __forceinline__ void commit_move(const CommitArgs& p, int q, int slice, int c, int h) {
+// The moves of one column (a piece E of a layer's keys, values or scales, at `at`) of a request's
+// tokens.  A thread owns its column, so the moves of one column are one thread's: a batch of eight
+// tokens is read before any of them is written, and since the path ascends (its i-th node is at
+// least i), no later batch reads a token that an earlier one wrote.
+template <class E>
+__device__ __forceinline__ void commit_column(const CommitArgs& p, int q, int c, int h, int na, bool mine,
+                                              bool tell, E* cache, int64_t at, int64_t page_stride,
+                                              int64_t tok_stride) {
   const int32_t* pages = p.table + (size_t)q * p.max_pages;
-  if (c < 0) return;
-  const int na = clamp_acc(p.n_acc[q], c, h, p.lg, p.gamma);
-  if (na < 1) return;
-  const int per_layer = 2 * p.Hkv * p.chunks;
-  const int64_t col = (int64_t)slice * 256 + threadIdx.x;
-  const bool mine = col < (int64_t)p.layers * per_layer;
-  int64_t at = 0;
-  uint4* cache = p.k_cache;
-  if (mine) {
-    const int layer = (int)(col / per_layer);
-    int r = (int)(col % per_layer);
-    if (r >= p.Hkv * p.chunks) {
-      cache = p.v_cache;
-      r -= p.Hkv * p.chunks;
-    }
-    at = layer * p.layer_stride + (int64_t)(r / p.chunks) * p.head_stride + r % p.chunks;
-  }
-  const bool tell = slice == 0 && threadIdx.x == 0;
   const int mask = (1 << p.lg) - 1;
   constexpr int kBatch = 8;
   int last = 0;
@@ -548,16 +536,49 @@ __device__ __forceinline__ void commit_move(const CommitArgs& p, int q, int slic
       const bool known = ps >= 0 && ps < p.n_pages && pd >= 0 && pd < p.n_pages;
       const bool move = !stop && n != i;
       if (move && !known && tell) raise_fault(p.status, DSPARK_FAULT_PAGE);
-      from[u] = move && known && mine ? at + ps * p.page_stride + (src & mask) * p.tok_stride : -1;
-      to[u] = at + pd * p.page_stride + (dst & mask) * p.tok_stride;
+      from[u] = move && known && mine ? at + ps * page_stride + (src & mask) * tok_stride : -1;
+      to[u] = at + pd * page_stride + (dst & mask) * tok_stride;
     }
-    uint4 x[kBatch];
+    E x[kBatch];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) x[u] = from[u] >= 0 ? cache[from[u]] : make_uint4(0, 0, 0, 0);
+    for (int u = 0; u < kBatch; ++u) x[u] = from[u] >= 0 ? cache[from[u]] : E{};
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
       if (from[u] >= 0) cache[to[u]] = x[u];
   }
+}
+
+// The moves of request q in 256 of the columns of its tokens: 16 bytes each (layer, keys or values,
+// head, piece of D), then, in a cache of 4 bits, 4 bytes each (layer, head, word of the scales).
+__device__ __forceinline__ void commit_move(const CommitArgs& p, int q, int slice, int c, int h) {
+  if (c < 0) return;
+  const int na = clamp_acc(p.n_acc[q], c, h, p.lg, p.gamma);
+  if (na < 1) return;
+  const int per_layer = 2 * p.Hkv * p.chunks;
+  const int64_t col = (int64_t)slice * 256 + threadIdx.x, wide = (int64_t)p.layers * per_layer;
+  const bool tell = slice == 0 && threadIdx.x == 0;
+  const int64_t word = col - wide;
+  if (p.words > 0 && word >= 0 && !tell) {
+    const int per = p.Hkv * p.words;
+    const int layer = (int)(word / per), r = (int)(word % per);
+    if (layer < p.layers)
+      commit_column(p, q, c, h, na, true, false, p.scales,
+                    layer * p.s_layer + (int64_t)(r / p.words) * p.s_head + r % p.words, p.s_page, p.s_tok);
+    return;
+  }
+  const bool mine = col < wide;
+  int64_t at = 0;
+  uint4* cache = p.k_cache;
+  if (mine) {
+    const int layer = (int)(col / per_layer);
+    int r = (int)(col % per_layer);
+    if (r >= p.Hkv * p.chunks) {
+      cache = p.v_cache;
+      r -= p.Hkv * p.chunks;
+    }
+    at = layer * p.layer_stride + (int64_t)(r / p.chunks) * p.head_stride + r % p.chunks;
+  }
+  commit_column(p, q, c, h, na, mine, tell, cache, at, p.page_stride, p.tok_stride);
 }
 
 // One launch, where the lengths go to memory of their own and the pages given back are few:
@@ -715,28 +736,29 @@ extern "C" size_t dspark_cache_commit_workspace_bytes(int R, int max_pages, int 
   return carve_commit(nullptr, R).bytes;
 }
 
-extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free_len,
-                                   const int32_t* n_acc, const int32_t* path,
-                                   const int32_t* done, const int32_t* ctx, int32_t* ctx_out,
-                                   int32_t* held, const int32_t* table, int32_t* free_pages,
-                                   int32_t* n_free, int layers, int Hkv, int D, dspark_dtype dt,
-                                   int n_pages, void* k_cache, void* v_cache,
-                                   int64_t layer_stride, int64_t page_stride,
-                                   int64_t head_stride, int64_t tok_stride, int32_t* dev_status,
-                                   void* ws, size_t ws_bytes, hipStream_t stream) {
+// The caches of a commit with a path: strides in bytes, a head's row `chunks` pieces of 16 bytes, its
+// scales `words` of 4.
+struct CommitCache {
+  int layers, Hkv, chunks;
+  void *k, *v;
+  int64_t layer, page, head, tok;
+  int words;
+  void* scales;
+  int64_t s_layer, s_page, s_head, s_tok;
+};
+
+static int commit_run(int R, int gamma, int page_size, int max_pages, int free_len, const int32_t* n_acc,
+                      const int32_t* path, const int32_t* done, const int32_t* ctx, int32_t* ctx_out,
+                      int32_t* held, const int32_t* table, int32_t* free_pages, int32_t* n_free,
+                      int n_pages, const CommitCache& cache, int32_t* dev_status, void* ws,
+                      size_t ws_bytes, hipStream_t stream) {
   if (R < 0 || R > kMaxRequests || max_pages < 1 || free_len < 0 ||
       !table_ok(page_size, max_pages))
     return DSPARK_EINVAL;
-  size_t e = 4;
-  if (path) {
-    e = dt == DSPARK_BF16 ? 2 : 4;
-    if (gamma < 1 || gamma > kMaxGamma || layers < 0 || Hkv < 1 || D < 8 || D % 8 != 0 ||
-        D > 1024 || (dt != DSPARK_F32 && dt != DSPARK_BF16) || !pages_ok(page_size, n_pages) ||
-        !stride_ok(layer_stride, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||
-        !stride_ok(tok_stride, e) || !k_cache || !v_cache || !aligned16(k_cache) ||
-        !aligned16(v_cache))
-      return DSPARK_EINVAL;
-  }
+  if (path && (gamma < 1 || gamma > kMaxGamma || cache.layers < 0 || cache.Hkv < 1 ||
+               !pages_ok(page_size, n_pages) || !cache.k || !cache.v || !aligned16(cache.k) ||
+               !aligned16(cache.v)))
+    return DSPARK_EINVAL;
   if (R == 0) return DSPARK_OK;
   if (!n_acc || !ctx || !ctx_out || !held || !table || !aligned16(ws) ||
       (done && (!n_free || (free_len > 0 && !free_pages))))
@@ -755,8 +777,9 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   const CommitWs w = carve_commit(ws, R);
   if (!small && !ws) return DSPARK_EINVAL;
   if (!small && ws_bytes < w.bytes) return DSPARK_EWORKSPACE;
-  const int lg = log2_of(page_size), u = (int)(16 / e), chunks = path ? D / u : 1;
-  const int64_t cols = path ? (int64_t)layers * 2 * Hkv * chunks : 1;
+  const int lg = log2_of(page_size);
+  const int64_t cols =
+      path ? (int64_t)cache.layers * cache.Hkv * (2 * cache.chunks + cache.words) : 1;
   if ((cols + 255) / 256 > 65535) return DSPARK_EINVAL;
   const int slices = cols > 256 ? (int)((cols + 255) / 256) : 1;
   CommitArgs p{};
@@ -775,16 +798,22 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   p.table = table;
   p.free_pages = free_pages;
   p.n_free = n_free;
-  p.layers = layers;
-  p.Hkv = Hkv;
-  p.chunks = chunks;
+  p.layers = cache.layers;
+  p.Hkv = cache.Hkv;
+  p.chunks = cache.chunks;
   p.n_pages = n_pages;
-  p.k_cache = static_cast<uint4*>(k_cache);
-  p.v_cache = static_cast<uint4*>(v_cache);
-  p.layer_stride = layer_stride / u;
-  p.page_stride = page_stride / u;
-  p.head_stride = head_stride / u;
-  p.tok_stride = tok_stride / u;
+  p.k_cache = static_cast<uint4*>(cache.k);
+  p.v_cache = static_cast<uint4*>(cache.v);
+  p.layer_stride = cache.layer / 16;
+  p.page_stride = cache.page / 16;
+  p.head_stride = cache.head / 16;
+  p.tok_stride = cache.tok / 16;
+  p.words = cache.words;
+  p.scales = static_cast<uint32_t*>(cache.scales);
+  p.s_layer = cache.s_layer / 4;
+  p.s_page = cache.s_page / 4;
+  p.s_head = cache.s_head / 4;
+  p.s_tok = cache.s_tok / 4;
   p.status = dev_status;
   p.ws = w;
   const int64_t blocks = path ? (int64_t)R * slices : 0;
@@ -796,4 +825,51 @@ extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_page
   commit_scan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
   if (path || done) commit_move_kernel<<<dim3(R, slices), 256, 0, stream>>>(p);
   return launch_status();
+}
+
+extern "C" int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free_len,
+                                   const int32_t* n_acc, const int32_t* path,
+                                   const int32_t* done, const int32_t* ctx, int32_t* ctx_out,
+                                   int32_t* held, const int32_t* table, int32_t* free_pages,
+                                   int32_t* n_free, int layers, int Hkv, int D, dspark_dtype dt,
+                                   int n_pages, void* k_cache, void* v_cache,
+                                   int64_t layer_stride, int64_t page_stride,
+                                   int64_t head_stride, int64_t tok_stride, int32_t* dev_status,
+                                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  CommitCache cache{};
+  if (path) {
+    const size_t e = dt == DSPARK_BF16 ? 2 : 4;
+    if (D < 8 || D % 8 != 0 || D > 1024 || (dt != DSPARK_F32 && dt != DSPARK_BF16) ||
+        !stride_ok(layer_stride, e) || !stride_ok(page_stride, e) || !stride_ok(head_stride, e) ||
+        !stride_ok(tok_stride, e))
+      return DSPARK_EINVAL;
+    const int64_t b = (int64_t)e;
+    cache = {layers, Hkv, (int)(D * e / 16), k_cache, v_cache, layer_stride * b, page_stride * b,
+             head_stride * b, tok_stride * b, 0, nullptr, 0, 0, 0, 0};
+  }
+  return commit_run(R, gamma, page_size, max_pages, free_len, n_acc, path, done, ctx, ctx_out, held,
+                    table, free_pages, n_free, n_pages, cache, dev_status, ws, ws_bytes, stream);
+}
+
+extern "C" int dspark_cache4_commit(int R, int gamma, int page_size, int max_pages, int free_len,
+                                    const int32_t* n_acc, const int32_t* path, const int32_t* done,
+                                    const int32_t* ctx, int32_t* ctx_out, int32_t* held,
+                                    const int32_t* table, int32_t* free_pages, int32_t* n_free,
+                                    int layers, int Hkv, int D, int n_pages, void* k_cache,
+                                    void* v_cache, int64_t layer_stride, int64_t page_stride,
+                                    int64_t head_stride, int64_t tok_stride, void* scales,
+                                    int64_t s_layer, int64_t s_page, int64_t s_head, int64_t s_tok,
+                                    int32_t* dev_status, void* ws, size_t ws_bytes,
+                                    hipStream_t stream) {
+  CommitCache cache{};
+  if (path) {
+    if (!cache4_ok(D, page_stride, head_stride, tok_stride, s_page, s_head, s_tok) ||
+        !stride_ok(layer_stride, 1) || s_layer < 0 || s_layer % (D / 16) != 0 || !scales ||
+        !aligned16(scales))
+      return DSPARK_EINVAL;
+    cache = {layers, Hkv, D / 32, k_cache, v_cache, layer_stride, page_stride, head_stride, tok_stride,
+             D / 64, scales, s_layer, s_page, s_head, s_tok};
+  }
+  return commit_run(R, gamma, page_size, max_pages, free_len, n_acc, path, done, ctx, ctx_out, held,
+                    table, free_pages, n_free, n_pages, cache, dev_status, ws, ws_bytes, stream);
 }

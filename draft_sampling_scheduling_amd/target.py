@@ -30,9 +30,10 @@ TARGET_EXPORTS = ("dspark_cache_plan_workspace_bytes", "dspark_cache_plan",
                   "dspark_cache_append", "dspark_qk_rope", "dspark_rope_append",
                   "dspark_cache4_append", "dspark_cache4_read",
                   "dspark_tree_attention_workspace_bytes",
-                  "dspark_tree_attention", "dspark_target_logits",
+                  "dspark_tree_attention", "dspark_tree_attention4_workspace_bytes",
+                  "dspark_tree_attention4", "dspark_target_logits",
                   "dspark_target_logits_tree", "dspark_verify_rows",
-                  "dspark_cache_commit_workspace_bytes", "dspark_cache_commit")
+                  "dspark_cache_commit_workspace_bytes", "dspark_cache_commit", "dspark_cache4_commit")
 
 _I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 _U8 = torch.uint8
@@ -59,6 +60,10 @@ def set_argtypes(L):
     L.dspark_tree_attention_workspace_bytes.restype = sz
     L.dspark_tree_attention.argtypes = ([i] * 9 + [vp, i64] + [vp] * 2 + [i64] * 3 + [vp] * 4 +
                                         [f] + [vp] * 4 + [sz, vp])
+    L.dspark_tree_attention4_workspace_bytes.argtypes = [i] * 6
+    L.dspark_tree_attention4_workspace_bytes.restype = sz
+    L.dspark_tree_attention4.argtypes = ([i] * 9 + [vp, i64] + [vp] * 2 + [i64] * 3 + [vp] + [i64] * 3 +
+                                         [vp] * 4 + [f] + [vp] * 4 + [sz, vp])
     L.dspark_target_logits.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 4 + [i] + [vp] * 7 +
                                        [i, vp, i, i] + [vp] * 4)
     L.dspark_target_logits_tree.argtypes = ([i] * 4 + [vp, i64, i] + [vp] * 5 + [i] + [vp] * 7 +
@@ -69,6 +74,8 @@ def set_argtypes(L):
     L.dspark_cache_commit_workspace_bytes.restype = sz
     L.dspark_cache_commit.argtypes = ([i] * 5 + [vp] * 9 + [i] * 5 + [vp] * 2 + [i64] * 4 +
                                       [vp] * 2 + [sz, vp])
+    L.dspark_cache4_commit.argtypes = ([i] * 5 + [vp] * 9 + [i] * 4 + [vp] * 2 + [i64] * 4 + [vp] +
+                                       [i64] * 4 + [vp] * 2 + [sz, vp])
     for name in TARGET_EXPORTS:
         if not name.endswith("_bytes"):
             getattr(L, name).restype = i
@@ -432,23 +439,31 @@ def cache_read(k_cache, v_cache, scales, slot, *, dtype=_BF16, n_rows=None, out=
     return out
 
 
-def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt) -> int:
-    return _fn("dspark_tree_attention_workspace_bytes")(R, rows, Hq, Hkv, D, dt)
+def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four=False) -> int:
+    """four: over a cache of 4 bits."""
+    name = "dspark_tree_attention4_workspace_bytes" if four else "dspark_tree_attention_workspace_bytes"
+    return _fn(name)(R, rows, Hq, Hkv, D, dt)
 
 
-def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=None, out=None,
+def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, scales=None, anc=None, scale=None, out=None,
                    ws=None, status=None):
     """Attention of a step's packed rows q [rows][Hq][D] over the paged cache, their own keys
     and values appended: every row sees its request's ctx tokens, the anchor (node 0), and of
     the block's further nodes those up to its own (anc=None), or those whose bit is set in
-    anc [rows] int64 (a plan's).  scale: of the scores, default D ** -0.5.
+    anc [rows] int64 (a plan's).  scales: the cache's, if it is one of 4 bits (q bfloat16 or float32).
+    scale: of the scores, default D ** -0.5.
     Returns dict(o [rows][Hq][D], lse [rows][Hq] float32); a caller-supplied `out` may leave
     "lse" out.  Rows behind row_off[-1] are left as they were."""
     dev = _device(q, "q")
-    kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
     dt = _dt(q, "q")
+    if scales is None:
+        kp, vp, (P, Hkv, page, D), st = _cache(k_cache, v_cache, dev, 4)
+        name, kind = "dspark_tree_attention", k_cache.dtype
+    else:
+        kp, vp, (P, Hkv, page, D), st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 4)
+        name, kind, st = "dspark_tree_attention4", q.dtype, (*st, scp, *sst)
     rows, Hq, _ = _dims(q, "q", 3)
-    qp, qs = _rows(q, "q", dev, (rows, Hq, D), k_cache.dtype)
+    qp, qs = _rows(q, "q", dev, (rows, Hq, D), kind)
     R, W = _dims(table, "table", 2)
     a = [_chk(table, "table", dev, (R, W), _I32), _chk(ctx, "ctx", dev, (R,), _I32),
          _chk(row_off, "row_off", dev, (R + 1,), _I32), _opt(anc, "anc", dev, (rows,), _I64)]
@@ -461,18 +476,19 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, anc=None, scale=
     if R == 0 or rows == 0:
         return out
     if ws is None:
+        four = scales is not None
         if _current_device() == dev.index:
-            nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
+            nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four)
         else:  # the size goes by the device's compute units
             with torch.cuda.device(dev):
-                nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt)
+                nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four)
         if nbytes == 0:
             from . import EINVAL, DsparkError
-            raise DsparkError("dspark_tree_attention_workspace_bytes", EINVAL)
+            raise DsparkError(name + "_workspace_bytes", EINVAL)
         ws, wp, wb = _workspace(nbytes, dev)
     else:
         ws, wp, wb = _given(ws, dev)
-    _call(dev, "dspark_tree_attention", R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st,
+    _call(dev, name, R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st,
           *a, D ** -0.5 if scale is None else scale, *b, wp, wb)
     return out
 
@@ -550,13 +566,13 @@ def cache_commit_workspace_bytes(R, max_pages, moves_in_place=False) -> int:
 
 
 def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path=None, done=None,
-                 k_cache=None, v_cache=None, out=None, ws=None, status=None):
+                 k_cache=None, v_cache=None, scales=None, out=None, ws=None, status=None):
     """After verification: the lengths with the anchor and the n_acc accepted nodes of each
     request committed ([R] int32; `out` may be ctx itself).  path [R][gamma] (trees): the
     accepted nodes, ascending; their keys and values move to the places behind the anchor, in
-    the caches ([n_pages][Hkv][page_size][D], or with a leading layer dimension).  done [R]:
-    finished requests (nonzero) give their pages back: free_pages and n_free grow, held and
-    the length become 0."""
+    the caches ([n_pages][Hkv][page_size][D], or with a leading layer dimension; scales: theirs, if
+    they are of 4 bits).  done [R]: finished requests (nonzero) give their pages back: free_pages
+    and n_free grow, held and the length become 0."""
     dev = _device(n_acc, "n_acc")
     per = R, = _dims(n_acc, "n_acc", 1)
     W, F = _dims(table, "table", 2)[1], _dims(free_pages, "free_pages", 1)[0]
@@ -568,19 +584,26 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
     b = [_chk(out, "out", dev, per, _I32), _chk(held, "held", dev, per, _I32),
          _chk(table, "table", dev, (R, W), _I32), _chk(free_pages, "free_pages", dev, (F,), _I32),
          _chk(n_free, "n_free", dev, (1,), _I32)]
-    c = [0, 0, 0, 0, 0, None, None, 0, 0, 0, 0]
+    name, c = "dspark_cache_commit", [0, 0, 0, 0, 0, None, None, 0, 0, 0, 0]
     if path is not None:
         if k_cache is None or v_cache is None:
             raise ValueError("a path needs the caches")
         if gamma == 0:
             raise ValueError("path has no places")
-        layered = isinstance(k_cache, torch.Tensor) and k_cache.dim() == 5
-        kp, vp, shape, st = _cache(k_cache, v_cache, dev, 5 if layered else 4)
-        if len(shape) == 4:
+        dims = 5 if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 5 else 4
+        if scales is None:
+            kp, vp, shape, st = _cache(k_cache, v_cache, dev, dims)
+        else:
+            kp, vp, shape, st, scp, sst = _cache4(k_cache, v_cache, scales, dev, dims)
+        if dims == 4:
             shape, st = (1, *shape), [0, *st]
         if shape[3] != page_size:
             raise ValueError(f"the caches have pages of {shape[3]} tokens, expected {page_size}")
-        c = [shape[0], shape[2], shape[4], _dt(k_cache, "k_cache"), shape[1], kp, vp, *st]
+        if scales is None:
+            c = [shape[0], shape[2], shape[4], _dt(k_cache, "k_cache"), shape[1], kp, vp, *st]
+        else:
+            name = "dspark_cache4_commit"
+            c = [shape[0], shape[2], shape[4], shape[1], kp, vp, *st, scp, *([0] if dims == 4 else []), *sst]
     sp = _opt(status, "status", dev, (1,), _I32)
     if R == 0:
         return out
@@ -589,5 +612,5 @@ def cache_commit(n_acc, ctx, held, table, free_pages, n_free, page_size, *, path
             cache_commit_workspace_bytes(R, W, path is not None and a[3] == b[0]), dev)
     else:
         ws, wp, wb = _given(ws, dev)
-    _call(dev, "dspark_cache_commit", R, gamma, page_size, W, F, *a, *b, *c, sp, wp, wb)
+    _call(dev, name, R, gamma, page_size, W, F, *a, *b, *c, sp, wp, wb)
     return out

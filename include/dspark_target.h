@@ -205,6 +205,21 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
                           const uint64_t *anc, float scale, void *o, float *lse,
                           int32_t *dev_status, void *ws, size_t ws_bytes, hipStream_t stream);
 
+/* The same over a cache of 4 bits; q and o in dt.  The cache's values are exact operands, and rows
+ * are as above: bf16 rows have their weights rounded to bf16, float ones are in float throughout.
+ * A group that reads NaN reaches the 32 elements of o it stands for, of rows that see its token. */
+size_t dspark_tree_attention4_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
+                                              dspark_dtype dt);
+
+int dspark_tree_attention4(int R, int rows, int Hq, int Hkv, int D, dspark_dtype dt,
+                           int page_size, int max_pages, int n_pages, const void *q,
+                           int64_t q_row, const void *k_cache, const void *v_cache,
+                           int64_t page_stride, int64_t head_stride, int64_t tok_stride,
+                           const void *scales, int64_t s_page, int64_t s_head, int64_t s_tok,
+                           const int32_t *table, const int32_t *ctx, const int32_t *row_off,
+                           const uint64_t *anc, float scale, void *o, float *lse,
+                           int32_t *dev_status, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------------------------------
  * Target logits: the rows of a step, with the request's penalties, biases and grammar masks,
  * in the layout dspark_verify reads.  Row j = 0..ell[q] of request q is the target's
@@ -312,6 +327,18 @@ int dspark_cache_commit(int R, int gamma, int page_size, int max_pages, int free
                         void *v_cache, int64_t layer_stride, int64_t page_stride,
                         int64_t head_stride, int64_t tok_stride, int32_t *dev_status, void *ws,
                         size_t ws_bytes, hipStream_t stream);
+
+/* The same for caches of 4 bits: codes and scales of an accepted path move together (strides of both
+ * in bytes).  Workspace: dspark_cache_commit_workspace_bytes. */
+int dspark_cache4_commit(int R, int gamma, int page_size, int max_pages, int free_len,
+                         const int32_t *n_acc, const int32_t *path, const int32_t *done,
+                         const int32_t *ctx, int32_t *ctx_out, int32_t *held,
+                         const int32_t *table, int32_t *free_pages, int32_t *n_free, int layers,
+                         int Hkv, int D, int n_pages, void *k_cache, void *v_cache,
+                         int64_t layer_stride, int64_t page_stride, int64_t head_stride,
+                         int64_t tok_stride, void *scales, int64_t s_layer, int64_t s_page,
+                         int64_t s_head, int64_t s_tok, int32_t *dev_status, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -99,3 +99,42 @@ def test_binding_wants_device_tensors(ds):
         ds.qk_rope([0], None, i, None)
     with pytest.raises(TypeError):
         ds.qk_rope(None, None, i, None)
+
+
+def test_attention4_refusals(ds):
+    ws = ds.tree_attention_workspace_bytes(4, 20, 8, 2, 64, ds.BF16, True)
+    assert ws > 0 and ds.tree_attention_workspace_bytes(4, 20, 8, 2, 96, ds.BF16, True) == 0
+    assert ds.tree_attention_workspace_bytes(0, 20, 8, 2, 64, ds.BF16, True) == 0
+
+    def call(R=4, rows=20, Hq=8, Hkv=2, D=64, dt=ds.BF16, page=16, W=10, n=40, q=P(), q_row=512, k=P(), ps=2048, st=1024,
+             tok=32, sc=P(), sp=128, s_tok=4, table=P(), scale=0.125, o=P(0x200000), wsp=P(), ws_bytes=ws):
+        return ds.lib().dspark_tree_attention4(R, rows, Hq, Hkv, D, dt, page, W, n, q, q_row, k, P(), ps, st, tok, sc, sp, 64,
+                                               s_tok, table, P(), P(), None, scale, o, None, None, wsp, ws_bytes, None)
+
+    for bad in (dict(R=(1 << 20) + 1), dict(Hq=9), dict(Hkv=0), dict(D=80), dict(dt=2), dict(page=10), dict(W=0),
+                dict(W=(1 << 26) + 1), dict(n=0), dict(q=None), dict(q=P(0x100002)), dict(q_row=511), dict(k=None),
+                dict(k=P(0x100008)), dict(ps=8), dict(st=1), dict(tok=-64), dict(tok=1 << 25), dict(sc=None),
+                dict(sc=P(0x100004)), dict(sp=2), dict(s_tok=-4), dict(s_tok=1 << 25), dict(table=None),
+                dict(scale=0.0), dict(scale=float("nan")), dict(scale=3e38), dict(o=None), dict(o=P()), dict(wsp=None),
+                dict(wsp=P(0x100008)), dict(rows=-1), dict(rows=1 << 28)):
+        assert call(**bad) == ds.EINVAL, bad
+    assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
+    assert call(R=0) == ds.OK and call(rows=0) == ds.OK
+
+
+def test_commit4_refusals(ds):
+    ws = ds.cache_commit_workspace_bytes(4, 10, True)
+
+    def call(R=4, gamma=4, page=16, W=10, n_acc=P(), path=P(), layers=1, Hkv=2, D=64, n=40, k=P(), ls=0, st=1024, tok=32, sc=P(),
+             sl=0, s_tok=4, ws_bytes=ws, ctx=P(0x200000), out=P(0x200000)):
+        return ds.lib().dspark_cache4_commit(R, gamma, page, W, 8, n_acc, path, None, ctx, out, P(0x300000), P(), P(), P(),
+                                             layers, Hkv, D, n, k, P(), ls, 2048, st, tok, sc, sl, 128, 64, s_tok, None, P(),
+                                             ws_bytes, None)
+
+    for bad in (dict(R=-1), dict(gamma=0), dict(gamma=65), dict(page=20), dict(W=0), dict(n_acc=None), dict(layers=-1),
+                dict(Hkv=0), dict(D=32), dict(D=256), dict(n=0), dict(k=None), dict(k=P(0x100008)), dict(ls=8), dict(st=8),
+                dict(tok=-16), dict(sc=None), dict(sc=P(0x100004)), dict(sl=-4), dict(sl=2), dict(s_tok=2), dict(out=P(0x200004)),
+                dict(out=P())):
+        assert call(**bad) == ds.EINVAL, bad
+    assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
+    assert call(R=0) == ds.OK
