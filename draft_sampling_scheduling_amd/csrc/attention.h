@@ -211,13 +211,12 @@ struct AttRows {
 // costs the later piece's set-up and the join; moving cuts to a near end lost more in balance
 // than it saved in joins (120 requests of 180 to 254 tokens in tables of more, lists of 6 to 8
 // rounds: 32 us with these kept whole, 27 cut), unless no list need be cut at all: block tables of
-// no more than kWhole rounds leave every list whole and launch no join.  Kernels alone, whole
+// no more than WHOLE tokens leave every list whole and launch no join.  Kernels alone, whole
 // against cut, bf16, tables of 256 tokens, 32 heads on 8: 32 requests 15.4 and 17.1 us, 120 23.8
 // and 27.5, 512 79 and 84; 17 rows, tables of 128: 32 requests 16.8 and 24.2.  In float a list's
 // products take longer, and it is the call, a launch shorter, that gains: 4 requests of up to 204
 // tokens 17 against 18 to 20 us a call, 19 against 13 captured in a graph.  A list that is cut has
 // its pieces in the workspace; the first workgroup that begins inside one says so in joint[b].
-constexpr int kWhole = 4;
 
 // a / b, both at least 0; a 64-bit division is some hundred instructions
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -266,7 +265,8 @@ __global__ void __launch_bounds__(W::F::THREADS, W::F::PER_SIMD)
   auto even = [&](const AttReq& r) { return p.anc != nullptr || r.n <= (r.ctx + r.n) / 8; };
   auto list = [&](const AttReq& r, int mt) -> int64_t {
     const int end = even(r) ? r.ctx + r.n : att_end(p, r, (mt + 1) * MR);
-    return (end + kRound - 1) / kRound + kSetup;
+    const int round = W::round(r.n * p.G);
+    return (end + round - 1) / round + kSetup;
   };
   // Units of the first mt lists.  kPeriod * G row tiles on, a chain's lists are kMore rounds
   // longer, so a sum takes one period's lists at most.
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(W::F::THREADS, W::F::PER_SIMD)
             (m + __builtin_amdgcn_logf(l)) * kLn2;
       }
     };
-    if constexpr (NR > 1) {
+    const auto rows_apart = [&]() {
       const int row = kRows * wave + wv.n;
       if (mt0 * MR + row < M) {
         const float f = !whole ? 1.0f : (wv.l == 0.0f ? 0.0f : 1.0f / wv.l);
@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(W::F::THREADS, W::F::PER_SIMD)
           }
         if (wv.h == 0) put_sums(row, wv.m, wv.l);
       }
-    } else {
-      // The waves' sums, through LDS: each gives the other half of its O, and finishes its own
-      // half.
+    };
+    const auto rows_shared = [&]() {
+      // the waves' sums, through LDS: each gives the other half of its O, and finishes its own half
       constexpr int HD = ND / 2, kGive = (HD * 16 + 2) * 64;
       float* x = reinterpret_cast<float*>(lds);
       auto give = [&](auto self) {
@@ -470,6 +470,14 @@ __global__ void __launch_bounds__(W::F::THREADS, W::F::PER_SIMD)
       __syncthreads();
       if (wave == 0) finish(First{});
       else finish(Second{});
+    };
+    if constexpr (W::kMix) {
+      if (M > kRows) rows_apart();
+      else rows_shared();
+    } else if constexpr (NR > 1) {
+      rows_apart();
+    } else {
+      rows_shared();
     }
     // this workgroup begins inside a list: the first to do so if the one before it did not
     if (tid == 0 && r0 > 0 && cut.begin(b - 1) <= s + kSetup)
@@ -641,12 +649,20 @@ static int att_launch(typename W::Params p, hipStream_t stream) {
   auto kern = attention_kernel<W>;
   const int grid = att_grid<F>();
   ensure_dynamic_lds(reinterpret_cast<const void*>(kern), F::LDS, raised);
-  p.whole = ((int64_t)p.max_pages << p.lg) <= kWhole * F::ROUND ? kWhole : 0;
+  p.whole = ((int64_t)p.max_pages << p.lg) <= F::WHOLE ? F::WHOLE / F::ROUND : 0;
   kern<<<grid, F::THREADS, F::LDS, stream>>>(p);
   if (p.whole > 0) return launch_status();
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
-  const int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
+  int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
+  if (W::kMix) {
+    // Twice as many workgroups here, each with a joint at most: so many slices that all of them about
+    // fit the chip twice (256 requests of 512 to 4096 tokens, of 4 bits: 4 slices 168, 9 172 us; 64 of
+    // 100 to 2048, a quarter of whose workgroups have joints: 31 and 28.5).
+    const int64_t lists = (int64_t)p.R * p.Hkv, joints = lists < grid ? lists : grid;
+    const int most = (int)(4 * grid / joints);
+    slices = slices < most ? slices : most;
+  }
   // Workgroups go to the eight dies in turn.  The joints lie some workgroups apart, often all
   // with the same remainder by 8 or two of them, so where there is much to read (112 row tiles
   // of 128: 12 to 29 us) neighbours are the slices of one joint (13 us); where there is little,

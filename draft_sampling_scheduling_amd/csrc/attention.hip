@@ -72,6 +72,7 @@ struct Fit {
   static constexpr int WAVES = NR == 1 ? 2 : NR;
   static constexpr int THREADS = WAVES * kWave;
   static constexpr int ROUND = NR == 1 ? 2 * kTok : kTok;  // tokens of a round
+  static constexpr int WHOLE = 4 * ROUND;  // tokens of block tables that leave every list whole
   // what a list costs beside its tokens, in rounds: 6 to 8 us, where a round of 64 tokens takes 3,
   // of float ones more (at 3 there 16 requests of 128 rows took 136 us, at 2 133), and one of 32
   // about 1 (at 3 a prompt of 8192 rows took 750 us, at 6 704)
@@ -108,6 +109,9 @@ struct AttWave : AttRows<D> {
   using Out = T;
   using F = Fit<T, D, NR_>;
   static constexpr int kD = D, kNR = NR_;
+  static constexpr bool kMix = false;
+  // tokens of a round of a request with M query rows to a cache head
+  static __device__ constexpr int round(int) { return F::ROUND; }
 
   using L = Tile<T, D>;
   static constexpr int NR = NR_, ND = D / 32;

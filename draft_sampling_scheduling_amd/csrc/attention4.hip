@@ -19,23 +19,29 @@
 
 namespace dspark {
 
+// Strides in bytes.  Within a page, and from page to page, they fit 32 bits, so that a lane's address
+// takes one multiplication of 32 bits each.
 struct Att4Params : AttParams {
+  uint32_t page_b4, tok_b4;
   const uint8_t* scales;
-  int64_t s_page, s_head, s_tok;
+  uint32_t s_page, s_tok;
+  int64_t s_head;
 };
 
-// How a variant sits on a CU.  NR 1: the two waves of a workgroup take 32 tokens each and merge at
-// the end.  TERMS: bf16 terms of a query and a weight.
-template <int D, int NR, int TERMS>
+// How a variant sits on a CU.  A workgroup's two waves have their tiles to themselves.  Up to 32
+// query rows they take 32 tokens each and merge at the end; more, they take 32 rows each, and the
+// same tokens, which HBM sees once.  TERMS: bf16 terms of a query and a weight.
+template <int D, int TERMS>
 struct Fit4 {
-  static constexpr bool kBf = TERMS == 1;  // the output's type, attention.h asks
+  static constexpr bool kBf = TERMS == 1;  // the output's type
   static constexpr int WAVES = 2;
   static constexpr int THREADS = WAVES * kWave;
-  static constexpr int ROUND = 2 * kTok;
+  static constexpr int ROUND = kTok;  // of a list of 64 rows
+  static constexpr int WHOLE = 256;   // tokens of block tables that leave every list whole
   static constexpr int SETUP = 3;
   static constexpr int TILE = kTok * D * 2;  // V as bf16
-  static constexpr int MERGE = 2 * (D / 64 * 16 + 2) * 64 * 4;
-  static constexpr int LDS = WAVES * TILE > MERGE ? WAVES * TILE : MERGE;
+  static constexpr int MERGE = (D / 4 + 2) * kWave * 4;  // half of a wave's O, m and l
+  static constexpr int LDS = WAVES * (TILE > MERGE ? TILE : MERGE) + 256;
   static constexpr int PER_SIMD = TERMS == 1 || D == 64 ? 2 : 1;
   static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
 };
@@ -48,12 +54,14 @@ struct Raw4 {
   uint2 s;  // the token's scale bytes: keys', then values'
 };
 
-template <int D, int NR_, int TERMS>
+template <int D, int TERMS>
 struct Att4Wave : AttRows<D> {
   using Params = Att4Params;
   using Out = typename std::conditional<TERMS == 1, uint16_t, float>::type;
-  using F = Fit4<D, NR_, TERMS>;
-  static constexpr int kD = D, kNR = NR_;
+  using F = Fit4<D, TERMS>;
+  static constexpr int kD = D, kNR = 2;
+  static constexpr bool kMix = true;
+  static __device__ constexpr int round(int M) { return M <= kRows ? 2 * kTok : F::ROUND; }
   static constexpr int ND = D / 32, KSTEPS = D / 16, RB = D * 2, WORDS = D / 16;
 
   using B = AttRows<D>;
@@ -67,7 +75,8 @@ struct Att4Wave : AttRows<D> {
   using B::see;
   using B::seen;
   const Att4Params& p;
-  uint32_t base;            // LDS of its V tile
+  int wave_;
+  uint32_t base;            // LDS of its V tile, 256-byte aligned: chunks are found by exclusive or
   // segment
   const char *kh, *vh;      // cache bases of the head
   const uint8_t* sh;
@@ -76,8 +85,7 @@ struct Att4Wave : AttRows<D> {
   u32x4 qf[TERMS][KSTEPS];
 
   __device__ __forceinline__ Att4Wave(const Att4Params& p_, int wave, uint32_t lds)
-      : B(p_), p(p_), base(lds + wave * F::TILE), wave_(wave) {}
-  int wave_;
+      : B(p_), p(p_), wave_(wave), base(((lds + 255) & ~255u) + wave * F::TILE) {}
 
   // V's tile: row t is token t, 16-byte chunk c of it at chunk c ^ swz(t).  A write takes one chunk
   // of 32 rows, a transposing read 4 neighbouring chunks of 4 rows; both spread over the banks.
@@ -85,20 +93,29 @@ struct Att4Wave : AttRows<D> {
     return D == 128 ? (t & 3) << 2 | ((t >> 2) & 3) : ((t >> 1) & 1) << 2 | ((t >> 2) & 3);
   }
 
-  // page of the lane's token of tile t0 (past the last token, the last one's page)
-  __device__ __forceinline__ int page_of(int t0) const {
-    const int i = (t0 + n) >> p.lg;
-    return pages[i < last_page ? i : last_page];
+  // Pages of tile t0, a page per 8 tokens (aligned, so they share one); past the last token, its page.
+  // Scalar loads: they are waited for apart from the vector loads under way.
+  struct Pages {
+    int a, b, c, d;
+  };
+  __device__ __forceinline__ int page_id(int t) const {
+    const int i = t >> p.lg;
+    return sload(pages, i < last_page ? i : last_page);
+  }
+  __device__ __forceinline__ Pages page_ids(int t0) const {
+    return {page_id(t0), page_id(t0 + 8), page_id(t0 + 16), page_id(t0 + 24)};
   }
 
   // The loads of tile t0.  Rows past the last token are read inside its page, and are never used.
-  __device__ __forceinline__ void load(int t0, int pg, Raw4<D>& x) const {
-    if (pg < 0 || pg >= p.n_pages) {
+  __device__ __forceinline__ void load(int t0, Pages id, Raw4<D>& x) const {
+    const int lo = n & 8 ? id.b : id.a, hi = n & 8 ? id.d : id.c;
+    uint32_t pg = (uint32_t)(n & 16 ? hi : lo);
+    if (pg >= (uint32_t)p.n_pages) {
       raise_fault(p.status, DSPARK_FAULT_PAGE);
       pg = 0;
     }
     const uint32_t tok = (uint32_t)(t0 + n) & ((1u << p.lg) - 1);
-    const uint64_t at = (uint64_t)(uint32_t)pg * (uint64_t)p.page_b + (uint64_t)tok * (uint32_t)p.tok_b + h * (D / 4);
+    const uint64_t at = (uint64_t)pg * p.page_b4 + (tok * p.tok_b4 + h * (D / 4));
     const uint4* k = reinterpret_cast<const uint4*>(kh + at);
     const uint4* v = reinterpret_cast<const uint4*>(vh + at);
 #pragma unroll
@@ -106,7 +123,7 @@ struct Att4Wave : AttRows<D> {
       x.k[i] = k[i];
       x.v[i] = v[i];
     }
-    const uint8_t* s = sh + (uint64_t)(uint32_t)pg * (uint64_t)p.s_page + (uint64_t)tok * (uint32_t)p.s_tok;
+    const uint8_t* s = sh + ((uint64_t)pg * p.s_page + tok * p.s_tok);
     if constexpr (D == 128)
       x.s = *reinterpret_cast<const uint2*>(s);
     else
@@ -118,45 +135,38 @@ struct Att4Wave : AttRows<D> {
     return (x.s.x >> (16 * values + 8 * h)) & 255u;
   }
 
-  // S^T of a tile: step s takes d = 8 s .. 8 s + 7 of either half
-  __device__ __forceinline__ void scores(const Raw4<D>& x, f32x16& sc) const {
-    sc = f32x16{};
-#pragma unroll
-    for (int s = 0; s < KSTEPS; ++s) {
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(x.k);
-      const uint4 f = fp4_bf16x8(w[s], fp4_scale(byte_of(x, h, false, s)));
-#pragma unroll
-      for (int t = 0; t < TERMS; ++t)
-        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f),
-                                                     __builtin_bit_cast(bf16x8, qf[t][s]), sc, 0, 0, 0);
-    }
-  }
-
-  // V of a tile, as bf16, to LDS.  EDGE: a token behind the last, and a group that reads NaN, are 0
-  // there (0 * NaN is none); sick[dt] has a bit for each of the 32 tokens whose group dt was NaN.
+  // S^T of a tile, and its V, as bf16, to LDS.  Step s of the product takes d = 8 s .. 8 s + 7 of either
+  // half; V's conversions go between the steps, which have products to wait for.
+  // EDGE: in V a token behind the last, and a group that reads NaN, are 0 (0 * NaN is none); sick[dt]
+  // has a bit for each of the 32 tokens whose group dt was NaN.
   template <bool EDGE>
-  __device__ __forceinline__ void stage(int t0, const Raw4<D>& x, uint32_t (&sick)[ND]) const {
-    const uint32_t row = base + n * RB, c0 = h * (D / 16) ^ swz(n);
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x.v);
+  __device__ __forceinline__ void scores(int t0, const Raw4<D>& x, f32x16& sc, uint32_t (&sick)[ND]) const {
+    const uint32_t row = base + n * RB + ((h * (D / 16) ^ swz(n)) << 4);
+    const uint32_t *k = reinterpret_cast<const uint32_t*>(x.k), *v = reinterpret_cast<const uint32_t*>(x.v);
     if (EDGE) {
 #pragma unroll
       for (int g = 0; g < ND; ++g) sick[g] = 0;
     }
+    sc = f32x16{};
 #pragma unroll
-    for (int i = 0; i < KSTEPS; ++i) {
-      uint32_t code = w[i], byte = byte_of(x, h, true, i);
+    for (int s = 0; s < KSTEPS; ++s) {
+      const uint4 f = fp4_bf16x8(k[s], fp4_scale(byte_of(x, h, false, s)));
+#pragma unroll
+      for (int t = 0; t < TERMS; ++t)
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, f),
+                                                     __builtin_bit_cast(bf16x8, qf[t][s]), sc, 0, 0, 0);
+      uint32_t code = v[s], byte = byte_of(x, h, true, s);
       if (EDGE) {
         const bool behind = t0 + n >= len, odd = byte >= 253;
-        if (i % 4 == 0) {
+        if (s % 4 == 0) {
           const uint64_t who = __ballot(odd && !behind);  // halves have different groups
-          const int g = i / 4;
-          sick[g] |= (uint32_t)who;
-          sick[ND / 2 + g] |= (uint32_t)(who >> 32);
+          sick[s / 4] |= (uint32_t)who;
+          sick[ND / 2 + s / 4] |= (uint32_t)(who >> 32);
         }
         code = behind || odd ? 0 : code;
         byte = behind || odd ? 127 : byte;
       }
-      lds_put<u32x4>(row + ((c0 ^ i) << 4), __builtin_bit_cast(u32x4, fp4_bf16x8(code, fp4_scale(byte))));
+      lds_put<u32x4>(row ^ (uint32_t)(s << 4), __builtin_bit_cast(u32x4, fp4_bf16x8(code, fp4_scale(byte))));
     }
   }
 
@@ -165,8 +175,7 @@ struct Att4Wave : AttRows<D> {
   // stored; with float ones they are three terms.
   __device__ __forceinline__ void values(f32x16& sc) {
     const int j = lane & 15, g = (lane >> 4) & 1, r0 = 4 * h + (j >> 2);
-    const uint32_t vrow = here(base + r0 * RB + (j & 1) * 8);
-    const uint32_t vx = here((uint32_t)((2 * g + ((j >> 1) & 1)) ^ swz(r0)) << 4);
+    const uint32_t at = here(base + r0 * RB + (j & 1) * 8 + (((2 * g + ((j >> 1) & 1)) ^ swz(r0)) << 4));
 #pragma unroll
     for (int st = 0; st < 2; ++st) {
       union {
@@ -178,7 +187,7 @@ struct Att4Wave : AttRows<D> {
 #pragma unroll
         for (int b = 0; b < 2; ++b)  // (rows 8 apart differ in one bit of the swizzle)
           a[dt].half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (DSPARK_LDS s16x4*)(uintptr_t)(vrow + (vx ^ (uint32_t)(dt << 6 | b << 5)) + 8 * (2 * st + b) * RB));
+              (DSPARK_LDS s16x4*)(uintptr_t)((at ^ (uint32_t)(dt << 6 | b << 5)) + 8 * (2 * st + b) * RB));
 #pragma unroll
       for (int t = 0; t < TERMS; ++t) {
         bf16x8 pb;
@@ -257,48 +266,61 @@ struct Att4Wave : AttRows<D> {
     see = p.anc ? p.anc[rq.a + i] : 0;
   }
 
-  __device__ __forceinline__ void tile(int t0, const Raw4<D>& x) {
+  // one tile; next(): the loads that may go out once its own registers are free
+  template <class Next>
+  __device__ __forceinline__ void tile(int t0, const Raw4<D>& x, Next next) {
     const bool edge = t0 + kTok > seen;
     f32x16 sc;
-    scores(x, sc);
     uint32_t vis = 0, sick[ND];
+    // (a wave's LDS instructions take effect in their order: its reads follow its writes without a
+    // wait, and the next tile's writes the reads; the fences keep the compiler to that order)
     if (edge) {
+      scores<true>(t0, x, sc, sick);
       vis = B::visible(t0);
 #pragma unroll
       for (int r = 0; r < 16; ++r) sc[r] = vis & (1u << reg_row(r, 0)) ? sc[r] : -INFINITY;
-      stage<true>(t0, x, sick);
     } else {
-      stage<false>(t0, x, sick);
+      scores<false>(t0, x, sc, sick);
     }
+    next();
     B::weigh(sc);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    asm volatile("" ::: "memory");
     values(sc);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the tile's reads, before the next is written
+    asm volatile("" ::: "memory");
     if (edge) spread(vis, sick);
   }
 
   // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
   __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr) {
     const int M = rq.n * p.G;
+    const bool all = M <= kRows;  // the waves share the rows
+    if (!all) m0 += wave_ * kRows;
     B::begin_rows(rq, m0);
     pages = p.table + (int64_t)q * p.max_pages;
     kh = static_cast<const char*>(p.k) + head * p.head_b;
     vh = static_cast<const char*>(p.v) + head * p.head_b;
     sh = p.scales + head * p.s_head;
     last_page = (len - 1) >> p.lg;
-    int end = uni(att_end(p, rq, m0 + NR_ * kRows));
-    end = end < (r0 + nr) * F::ROUND ? end : (r0 + nr) * F::ROUND;
-    const int first = r0 * F::ROUND + wave_ * kTok;
-    const int nt = first < end ? (end - first + F::ROUND - 1) / F::ROUND : 0;
-    queries(rq, head, m0, M);
+    const int step = all ? 2 * kTok : kTok;
+    int end = uni(att_end(p, rq, m0 + kRows));
+    end = end < (r0 + nr) * step ? end : (r0 + nr) * step;
+    const int first = r0 * step + (all ? wave_ : 0) * kTok;
+    const int nt = m0 < M && first < end ? (end - first + step - 1) / step : 0;
     if (nt > 0) {
+      // A tile is under way while the one before it is computed, its page ids one further (two or
+      // three tiles under way were no faster: 171, 173 and 175 us for 256 requests of 512 to 4096
+      // tokens).  What would be asked for past the end is the last tile again: a load that is always
+      // made leaves the compiler's wait for the one before exact.
+      const int last = first + (nt - 1) * step;
+      const auto next = [&](int t0) { return t0 < last ? t0 : last; };
       Raw4<D> x;
-      load(first, page_of(first), x);
-      for (int k = 0; k < nt; ++k) {
-        const int t0 = first + k * F::ROUND;
-        Raw4<D> now = x;
-        if (k + 1 < nt) load(t0 + F::ROUND, page_of(t0 + F::ROUND), x);
-        tile(t0, now);
+      load(first, page_ids(first), x);
+      Pages id = page_ids(next(first + step));
+      queries(rq, head, m0, M);
+      for (int t0 = first; t0 <= last; t0 += step) {
+        const Pages then = page_ids(next(t0 + 2 * step));
+        tile(t0, x, [&] { load(next(t0 + step), id, x); });
+        id = then;
       }
     }
     l = half_sum(l);
@@ -310,8 +332,8 @@ struct Att4Wave : AttRows<D> {
 // ---------------------------------------------------------------------------------------
 template <class F>
 static auto att4_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
-  if (dt == DSPARK_F32) return D == 64 ? f((Att4Wave<64, 1, 3>*)nullptr) : f((Att4Wave<128, 1, 3>*)nullptr);
-  return D == 64 ? f((Att4Wave<64, 1, 1>*)nullptr) : f((Att4Wave<128, 1, 1>*)nullptr);
+  if (dt == DSPARK_F32) return D == 64 ? f((Att4Wave<64, 3>*)nullptr) : f((Att4Wave<128, 3>*)nullptr);
+  return D == 64 ? f((Att4Wave<64, 1>*)nullptr) : f((Att4Wave<128, 1>*)nullptr);
 }
 
 static size_t att4_carve(Att4Params& p, void* ws, int R, int rows, int G, int D, dspark_dtype dt) {
@@ -341,21 +363,21 @@ extern "C" int dspark_tree_attention4(int R, int rows, int Hq, int Hkv, int D, d
                                       const uint64_t* anc, float scale, void* o, float* lse,
                                       int32_t* dev_status, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (!att_dims_ok(R, rows, Hq, Hkv, D, dt) ||
-      !cache4_ok(D, page_stride, head_stride, tok_stride, s_page, s_head, s_tok) || tok_stride > (1 << 24) ||
-      s_tok > (1 << 24))
+      !cache4_ok(D, page_stride, head_stride, tok_stride, s_page, s_head, s_tok) || tok_stride > (1 << 21) ||
+      s_tok > (1 << 21) || page_stride >= ((int64_t)1 << 32) || s_page >= ((int64_t)1 << 32))
     return DSPARK_EINVAL;
   Att4Params p{};
   const int rc = att_args(p, R, rows, Hq, Hkv, D, dt, page_size, max_pages, n_pages, q, q_row, k_cache, v_cache,
                           table, ctx, row_off, anc, scale, o, lse, dev_status, ws);
   if (rc != DSPARK_OK || R == 0 || rows == 0) return rc;
   if (!scales || !aligned16(scales)) return DSPARK_EINVAL;
-  p.page_b = page_stride;
+  p.page_b4 = (uint32_t)page_stride;
+  p.tok_b4 = (uint32_t)tok_stride;
   p.head_b = head_stride;
-  p.tok_b = tok_stride;
   p.scales = static_cast<const uint8_t*>(scales);
-  p.s_page = s_page;
+  p.s_page = (uint32_t)s_page;
+  p.s_tok = (uint32_t)s_tok;
   p.s_head = s_head;
-  p.s_tok = s_tok;
   if (ws_bytes < att4_carve(p, ws, R, rows, p.G, D, dt)) return DSPARK_EWORKSPACE;
   return att4_variant(R, rows, p.G, D, dt, [&](auto* w) {
     return att_launch<std::remove_pointer_t<decltype(w)>>(p, stream);
