@@ -14,7 +14,7 @@
 //   - K goes from memory to registers to the product: a lane holds half of a token's head, and as a sum
 //     over d may be taken in any order, the queries are loaded to match.
 //   - V needs tokens where memory has d, so it passes through LDS as bf16, by transposing reads.
-#include "attention.h"
+#include "attention_wave.h"
 #include "fp4.h"
 
 namespace dspark {
@@ -42,7 +42,10 @@ struct Fit4 {
   static constexpr int TILE = kTok * D * 2;  // V as bf16
   static constexpr int MERGE = (D / 4 + 2) * kWave * 4;  // half of a wave's O, m and l
   static constexpr int LDS = WAVES * (TILE > MERGE ? TILE : MERGE) + 256;
-  static constexpr int PER_SIMD = TERMS == 1 || D == 64 ? 2 : 1;
+  // Waves a SIMD: at D = 64 registers allow three (256 requests of 512 to 4096 tokens 105 us, two 121; one
+  // token over 115000 41 and 47).  At D = 128 three can be had by taking addresses anew for each tile,
+  // and lose: 178 against 168 us there.
+  static constexpr int PER_SIMD = D == 64 ? (TERMS == 1 ? 3 : 2) : (TERMS == 1 ? 2 : 1);
   static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
 };
 
@@ -328,11 +331,139 @@ struct Att4Wave : AttRows<D> {
 };
 
 // ---------------------------------------------------------------------------------------
+// Many rows: four waves of 32 rows each share every tile, as bf16 in LDS, two tiles deep, with a
+// barrier per tile.  Each of them converts the keys and values of 8 of the tile's tokens, a group of
+// 32 elements a lane, and the products are those over a bf16 cache.
+// ---------------------------------------------------------------------------------------
+// V's swizzle spreads writes of one chunk of 4 rows as well as the reads.
+template <int D>
+struct Tile4 : Tile<uint16_t, D> {
+  static __host__ __device__ constexpr int vswz(int r) {
+    return D == 128 ? (r & 3) << 2 | (r & 3) : ((r >> 1) & 1) << 2 | ((r >> 1) & 3);
+  }
+};
+
+template <int D>
+struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
+  using A = AttWave<uint16_t, D, 4, Tile4<D>>;
+  using Params = Att4Params;
+  using F = typename A::F;
+  using L = Tile4<D>;
+  static constexpr int GROUPS = D / 32, LANES = 8 * GROUPS;  // lanes that a wave's 8 tokens' keys take
+
+  using A::B::h;
+  using A::B::l;
+  using A::B::lane;
+  using A::B::len;
+  using A::B::n;
+  using A::B::seen;
+  using A::base;
+  using A::last_page;
+  using A::mine;
+  using A::pages;
+  using A::wave;
+  const Att4Params& p;
+  bool keys, any;           // the lane converts keys, or anything at all (D = 64: half of them)
+  int tok, group;           // its token of the wave's 8, and group of 32
+  uint32_t at;              // LDS of its first chunk, in a stage
+  const char* codes;        // segment: its group's codes and scale byte at the head's first token
+  const uint8_t* bytes;
+
+  __device__ __forceinline__ Att4Shared(const Att4Params& p_, int wave_, uint32_t lds) : A(p_, wave_, lds), p(p_) {
+    keys = lane < LANES;
+    any = lane < 2 * LANES;
+    const int i = lane % LANES;
+    tok = i / GROUPS;
+    group = i % GROUPS;
+    const int x = keys ? L::kswz(mine + tok) : L::vswz(mine + tok);
+    at = (uint32_t)(keys ? 0 : L::BYTES) + (uint32_t)(mine + tok) * L::RB + ((4 * group ^ x) << 4);
+  }
+
+  __device__ __forceinline__ int page_id(int t0) const {
+    const int i = (t0 + mine) >> p.lg;
+    return sload(pages, i < last_page ? i : last_page);
+  }
+  // the lane's codes and byte of tile t0; rows past the last token are read inside its page
+  __device__ __forceinline__ void load(int t0, int id, uint4& x, uint32_t& byte) const {
+    if ((uint32_t)id >= (uint32_t)p.n_pages) {
+      if (lane == 0) raise_fault(p.status, DSPARK_FAULT_PAGE);
+      id = 0;
+    }
+    const uint32_t t = (uint32_t)(t0 + mine) & ((1u << p.lg) - 1);  // the 8 tokens lie in one page
+    x = *reinterpret_cast<const uint4*>(codes + ((uint64_t)(uint32_t)id * p.page_b4 + t * p.tok_b4));
+    byte = bytes[(uint64_t)(uint32_t)id * p.s_page + t * p.s_tok];
+  }
+  // as bf16 to stage s
+  __device__ __forceinline__ void convert(uint4 x, uint32_t byte, int s) const {
+    const uint32_t to = here(at), stage = base + s * F::TILE;
+    const float scale = fp4_scale(byte);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&x);
+    if (any) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        lds_put<u32x4>(stage + (to ^ (uint32_t)(j << 4)), __builtin_bit_cast(u32x4, fp4_bf16x8(w[j], scale)));
+    }
+  }
+
+  // tokens of rounds r0 .. r0 + nr of the row tile that starts at query row m0
+  __device__ __forceinline__ void segment(const AttReq& rq, int q, int head, int m0, int r0, int nr) {
+    const int M = rq.n * p.G;
+    A::begin(rq, q, head, m0);
+    const uint32_t row = (uint32_t)tok * p.tok_b4, s_row = (uint32_t)tok * p.s_tok;
+    codes = (keys ? A::kh : A::vh) + row + (any ? group * 16 : 0);
+    bytes = p.scales + head * p.s_head + s_row + (keys ? 0 : GROUPS) + group;
+    int end = uni(att_end(p, rq, m0 + 4 * kRows));
+    end = end < (r0 + nr) * F::ROUND ? end : (r0 + nr) * F::ROUND;
+    const int first = r0 * F::ROUND, nt = first < end ? (end - first + F::ROUND - 1) / F::ROUND : 0;
+    if (nt > 0) {
+      const int last = first + (nt - 1) * F::ROUND, mw = m0 + wave * kRows;
+      const auto next = [&](int t) { return t < last ? t : last; };
+      uint4 x;
+      uint32_t byte;
+      load(first, page_id(first), x, byte);
+      A::queries(rq, head, mw, M);
+      convert(x, byte, 0);
+      load(next(first + F::ROUND), page_id(next(first + F::ROUND)), x, byte);
+      int id = page_id(next(first + 2 * F::ROUND));
+      const bool live = mw < M;
+      int s = 0;
+      for (int t0 = first; t0 <= last; t0 += F::ROUND) {
+        stage_barrier();  // the whole tile is there, and every wave is done with the one before
+        convert(x, byte, s ^ 1);  // (of the last tile: itself again, for nobody)
+        load(next(t0 + 2 * F::ROUND), id, x, byte);
+        id = page_id(next(t0 + 3 * F::ROUND));
+        const uint32_t ks = base + s * F::TILE, vs = ks + L::BYTES;
+        f32x16 sc = f32x16{};
+        if (live) {
+          A::scores(ks, sc);
+          if (t0 + kTok > seen) A::B::mask(t0, sc);
+          __builtin_amdgcn_s_setprio(1);  // (see AttWave)
+          A::B::weigh(sc);
+          __builtin_amdgcn_s_setprio(0);
+        }
+        if (t0 + kTok > seen && A::clean_values(t0, vs)) A::odd_values(ks, vs, sc);
+        if (live) A::values(vs, sc);
+        s ^= 1;
+      }
+      stage_barrier();  // the next segment's tiles overwrite the stages
+    }
+    l = half_sum(l);
+  }
+};
+
+// ---------------------------------------------------------------------------------------
 // host
 // ---------------------------------------------------------------------------------------
+// f(the variant that runs these shapes).  Past 64 query rows to a cache head (rows / R, the bound that the
+// host knows, times heads to a cache head) waves that share tiles save the others' conversions: 8192 rows
+// from an empty cache 667 against 791 us, 2048 behind 4048 239 and 253, 64 requests of 72 over 500 to
+// 4000 114 and 123; over short contexts the barriers cost as much (16 requests of 128 rows behind 1000
+// tokens 39 and 37).  Up to 64 they lose: 36 rows 343 and 242 us, 45 37 and 29.
 template <class F>
 static auto att4_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
   if (dt == DSPARK_F32) return D == 64 ? f((Att4Wave<64, 3>*)nullptr) : f((Att4Wave<128, 3>*)nullptr);
+  const int64_t m = (int64_t)((rows + R - 1) / R) * G;
+  if (m > 64) return D == 64 ? f((Att4Shared<64>*)nullptr) : f((Att4Shared<128>*)nullptr);
   return D == 64 ? f((Att4Wave<64, 1>*)nullptr) : f((Att4Wave<128, 1>*)nullptr);
 }
 

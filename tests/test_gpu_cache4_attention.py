@@ -141,8 +141,6 @@ def test_unseen_groups_hold_anything(Hq, D, dtype):
     see = ref.sees(n, anc)
     for sick, byte in ((0, 255), (1, 255), (1, 254), (1, 253), (0, 253)):
         c = c4.Cache4(9, [ctx], [n], 2, D, 16)
-        c.vc[:] |= 0x22  # (no zeros: of a large power too they would be finite)
-        c.renew()
         table = torch.from_numpy(c.table).to("cuda:0")
 
         def go():
@@ -161,9 +159,11 @@ def test_unseen_groups_hold_anything(Hq, D, dtype):
         well = [i for i in range(n) if i not in (2, 5)]
         assert (np.abs(after - w[0]) <= tol(w, ctx + n, D, dtype is BF)[0])[well].all()
         bad = ~np.isfinite(after[[2, 5]])
+        if byte != 255:  # (past the largest float in part: what its own rows read is not said)
+            continue
         if sick == 1:
             assert bad[..., 32:64].all() and not bad[..., :32].any() and not bad[..., 64:].any()
-        elif byte == 255:
+        else:
             assert bad.all()
     assert see[5, 2] and not see[4, 2]
 
