@@ -194,27 +194,35 @@ def _cache(k_cache, v_cache, dev, dims):
     return k_cache.data_ptr(), v_cache.data_ptr(), shape, st[:dims - 1]
 
 
-def _scales(scales, dev, lead, D):
-    """Address and leading strides of the scales of a 4-bit cache (`lead`: its leading sizes)."""
-    shape = (*lead, 2, D // 32)
-    if (not isinstance(scales, torch.Tensor) or scales.dtype is not _U8 or scales.shape != shape or
-            scales.get_device() != dev.index):
-        _refuse(scales, "scales", dev, shape, _U8)
-    st = _strides(scales, 2)
-    if st is None:
-        raise ValueError("a token's scales must be dense")
-    return scales.data_ptr(), st
-
-
 def _cache4(k_cache, v_cache, scales, dev, dims):
     """_cache of a 4-bit cache and its scales: addresses, shape (with D), strides."""
+    Tensor, i = torch.Tensor, dev.index
+    if (isinstance(k_cache, Tensor) and isinstance(v_cache, Tensor) and isinstance(scales, Tensor) and
+            k_cache.dtype is _U8 and v_cache.dtype is _U8 and scales.dtype is _U8):
+        shape, st, sst = k_cache.shape, k_cache.stride(), scales.stride()
+        *lead, half = shape
+        g = half // 16
+        if (len(lead) == dims - 1 and (g == 2 or g == 4) and 1 not in lead and st[-1] == 1 and
+                v_cache.shape == shape and v_cache.stride() == st and scales.shape == (*lead, 2, g) and
+                sst[-1] == 1 and sst[-2] == g and half == 16 * g and k_cache.get_device() == i and
+                v_cache.get_device() == i and scales.get_device() == i):
+            return (k_cache.data_ptr(), v_cache.data_ptr(), (*lead, 2 * half), st[:-1],
+                    scales.data_ptr(), sst[:-2])
+    # what is wrong, or a dimension of size 1, whose stride is never used
     kp, vp, shape, st = _cache(k_cache, v_cache, dev, dims)
     if k_cache.dtype is not _U8:
         raise TypeError(f"k_cache must be uint8 beside scales, got {k_cache.dtype}")
     shape = (*shape[:-1], 2 * shape[-1])
     if shape[-1] not in (64, 128):
         raise ValueError(f"a 4-bit cache has heads of 64 or 128 elements, got {shape[-1]}")
-    return kp, vp, shape, st, *_scales(scales, dev, shape[:-1], shape[-1])
+    want = (*shape[:-1], 2, shape[-1] // 32)
+    if (not isinstance(scales, Tensor) or scales.dtype is not _U8 or scales.shape != want or
+            scales.get_device() != i):
+        _refuse(scales, "scales", dev, want, _U8)
+    sst = _strides(scales, 2)
+    if sst is None:
+        raise ValueError("a token's scales must be dense")
+    return kp, vp, shape, st, scales.data_ptr(), sst
 
 
 _fns = {}
@@ -328,28 +336,16 @@ def cache_append(k, v, k_cache, v_cache, slot, *, scales=None, n_rows=None, stat
           *st, _opt(status, "status", dev, (1,), _I32))
 
 
-def _rope_rows(q, k, dev, D):
-    """Rows, dtype, and head counts, addresses and row strides of q and k (either may be None)."""
-    some, name = (q, "q") if q is not None else (k, "k")
-    rows, dtype = _dims(some, name, 3)[0], some.dtype
-    _dt(some, name)
-    Hq = 0 if q is None else _dims(q, "q", 3)[1]
-    Hkv = 0 if k is None else _dims(k, "k", 3)[1]
-    qp, qs = (None, 0) if q is None else _rows(q, "q", dev, (rows, Hq, D), dtype)
-    kp, ks = (None, 0) if k is None else _rows(k, "k", dev, (rows, Hkv, D), dtype)
-    return rows, Hq, Hkv, dtype, qp, qs, kp, ks
-
-
 def _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows):
     """rot, and the arguments from position to n_rows."""
-    if rope is None:
-        n_pos = rot = 0
-        pp = tp = None
-    else:
+    n_pos = rot = 0
+    pp = tp = None
+    if rope is not None:
         n_pos, rot = _dims(rope, "rope", 2)
         pp, tp = _chk(position, "position", dev, (rows,), _I32), _chk(rope, "rope", dev, (n_pos, rot), _F32)
-    return rot, (pp, tp, n_pos, _opt(q_norm, "q_norm", dev, (D,), dtype),
-                 _opt(k_norm, "k_norm", dev, (D,), dtype), eps, _opt(n_rows, "n_rows", dev, (1,), _I32))
+    return rot, (pp, tp, n_pos, None if q_norm is None else _chk(q_norm, "q_norm", dev, (D,), dtype),
+                 None if k_norm is None else _chk(k_norm, "k_norm", dev, (D,), dtype), eps,
+                 None if n_rows is None else _chk(n_rows, "n_rows", dev, (1,), _I32))
 
 
 def qk_rope(q, k, position, rope, *, q_norm=None, k_norm=None, eps=1e-6, interleaved=False,
@@ -361,20 +357,25 @@ def qk_rope(q, k, position, rope, *, q_norm=None, k_norm=None, eps=1e-6, interle
     sines; None: nothing turns).  Rows at and behind n_rows (a device int32 [1]), and those whose
     position is not in the table (FAULT_PARAM), are left alone.
     Returns dict(q, k); a caller-supplied `out` may hold q and k themselves."""
-    dev = _device(k if q is None else q, "q")
-    D = _dims(k if q is None else q, "q", 3)[2]
-    rows, Hq, Hkv, dtype, qp, qs, kp, ks = _rope_rows(q, k, dev, D)
+    some, name = (k, "k") if q is None else (q, "q")
+    dev = _device(some, name)
+    rows, _, D = _dims(some, name, 3)
+    dtype, dt = some.dtype, _dt(some, name)
+    Hq = 0 if q is None else some.shape[1]
+    Hkv = 0 if k is None else _dims(k, "k", 3)[1]
+    qp, qs = (None, 0) if q is None else _rows(q, "q", dev, (rows, Hq, D), dtype)
+    kp, ks = (None, 0) if k is None else _rows(k, "k", dev, (rows, Hkv, D), dtype)
     rot, a = _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows)
     if out is None:
         out = dict(q=None if q is None else torch.empty((rows, Hq, D), dtype=dtype, device=dev),
                    k=None if k is None else torch.empty((rows, Hkv, D), dtype=dtype, device=dev))
     qo, qos = (None, 0) if q is None else _rows(out["q"], "out['q']", dev, (rows, Hq, D), dtype)
     ko, kos = (None, 0) if k is None else _rows(out["k"], "out['k']", dev, (rows, Hkv, D), dtype)
-    sp = _opt(status, "status", dev, (1,), _I32)
+    sp = None if status is None else _chk(status, "status", dev, (1,), _I32)
     if rows == 0:
         return out
-    _call(dev, "dspark_qk_rope", rows, Hq, Hkv, D, rot, interleaved, 1 if dtype is _BF16 else 0, qp, qs,
-          kp, ks, *a, qo, qos, ko, kos, sp)
+    _call(dev, "dspark_qk_rope", rows, Hq, Hkv, D, rot, interleaved, dt, qp, qs, kp, ks, *a, qo, qos, ko, kos,
+          sp)
     return out
 
 
@@ -385,31 +386,33 @@ def rope_append(q, k, v, k_cache, v_cache, slot, position, rope, *, scales=None,
     may be q itself), which is returned (None without q).  scales: the cache's, if it is one of
     4 bits."""
     dev = _device(k, "k")
-    D = _dims(k, "k", 3)[2]
-    rows, Hq, Hkv, dtype, qp, qs, kp, ks = _rope_rows(q, k, dev, D)
+    rows, Hkv, D = shape = _dims(k, "k", 3)
+    dtype, dt = k.dtype, _dt(k, "k")
     if scales is None:
-        kc, vc, shape, st = _cache(k_cache, v_cache, dev, 4)
+        kc, vc, (P, heads, page, size), st = _cache(k_cache, v_cache, dev, 4)
         name, more = "dspark_rope_append", ()
         if k_cache.dtype is not dtype:
             raise TypeError(f"k_cache has dtype {k_cache.dtype}, expected {dtype}")
     else:
-        kc, vc, shape, st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 4)
+        kc, vc, (P, heads, page, size), st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 4)
         name, more = "dspark_cache4_append", (scp, *sst)
-    P, _, page, _ = shape
-    if shape[1] != Hkv or shape[3] != D:
-        raise ValueError(f"k has {Hkv} heads of {D}, the cache {shape[1]} of {shape[3]}")
-    vp, vs = _rows(v, "v", dev, (rows, Hkv, D), dtype)
+    if heads != Hkv or size != D:
+        raise ValueError(f"k has {Hkv} heads of {D}, the cache {heads} of {size}")
+    kp, ks = _rows(k, "k", dev, shape, dtype)
+    vp, vs = _rows(v, "v", dev, shape, dtype)
     rot, a = _rope_args(dev, rows, D, dtype, position, rope, q_norm, k_norm, eps, n_rows)
     sl = _chk(slot, "slot", dev, (rows,), _I32)
     if q is None:
-        out, qo, qos = None, None, 0
+        Hq, qp, qs, out, qo, qos = 0, None, 0, None, None, 0
     else:
+        Hq = _dims(q, "q", 3)[1]
+        qp, qs = _rows(q, "q", dev, (rows, Hq, D), dtype)
         if out is None:
             out = torch.empty((rows, Hq, D), dtype=dtype, device=dev)
         qo, qos = _rows(out, "out", dev, (rows, Hq, D), dtype)
-    sp = _opt(status, "status", dev, (1,), _I32)
-    _call(dev, name, rows, Hq, Hkv, D, rot, interleaved, 1 if dtype is _BF16 else 0, page, P, qp, qs, kp, ks,
-          vp, vs, sl, *a, qo, qos, kc, vc, *st, *more, sp)
+    sp = None if status is None else _chk(status, "status", dev, (1,), _I32)
+    _call(dev, name, rows, Hq, Hkv, D, rot, interleaved, dt, page, P, qp, qs, kp, ks, vp, vs, sl, *a, qo, qos,
+          kc, vc, *st, *more, sp)
     return out
 
 
@@ -419,23 +422,24 @@ def cache_read(k_cache, v_cache, scales, slot, *, dtype=_BF16, n_rows=None, out=
     float32 (exact in both).  Rows of slot -1, and at and behind n_rows (a device int32 [1]), are
     left as they were."""
     dev = _device(k_cache, "k_cache")
-    layered = k_cache.dim() == 5
-    kc, vc, shape, st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 5 if layered else 4)
-    rows, = _dims(slot, "slot", 1)
-    want = (rows, shape[-3], shape[-1])
-    if layered:
-        want = (shape[0], *want)
+    if k_cache.dim() == 5:
+        kc, vc, (layers, P, Hkv, page, D), st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 5)
+        rows, = _dims(slot, "slot", 1)
+        want = (layers, rows, Hkv, D)
     else:
-        shape, st, sst = (1, *shape), (0, *st), (0, *sst)
+        kc, vc, (P, Hkv, page, D), st, scp, sst = _cache4(k_cache, v_cache, scales, dev, 4)
+        rows, = _dims(slot, "slot", 1)
+        layers, st, sst, want = 1, (0, *st), (0, *sst), (rows, Hkv, D)
     if out is None:
         out = dict(k=torch.empty(want, dtype=dtype, device=dev), v=torch.empty(want, dtype=dtype, device=dev))
-    _dims(out["k"], "out['k']", len(want))
-    kind = out["k"].dtype
-    ko, vo = _chk(out["k"], "out['k']", dev, want, kind), _chk(out["v"], "out['v']", dev, want, kind)
-    layers, P, Hkv, page, D = shape
-    _call(dev, "dspark_cache4_read", layers, rows, Hkv, D, _dt(out["k"], "out['k']"), page, P,
-          _chk(slot, "slot", dev, (rows,), _I32), _opt(n_rows, "n_rows", dev, (1,), _I32), kc, vc, *st, scp, *sst,
-          ko, vo, _opt(status, "status", dev, (1,), _I32))
+    k, v = out["k"], out["v"]
+    dt = _dt(k, "out['k']") if isinstance(k, torch.Tensor) else _refuse(k, "out['k']", dev, want, dtype)
+    ko, vo = _chk(k, "out['k']", dev, want, k.dtype), _chk(v, "out['v']", dev, want, k.dtype)
+    sl = _chk(slot, "slot", dev, (rows,), _I32)
+    np = None if n_rows is None else _chk(n_rows, "n_rows", dev, (1,), _I32)
+    sp = None if status is None else _chk(status, "status", dev, (1,), _I32)
+    _call(dev, "dspark_cache4_read", layers, rows, Hkv, D, dt, page, P, sl, np, kc, vc, *st, scp, *sst, ko, vo,
+          sp)
     return out
 
 
@@ -443,6 +447,20 @@ def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four=False) -> int:
     """four: over a cache of 4 bits."""
     name = "dspark_tree_attention4_workspace_bytes" if four else "dspark_tree_attention_workspace_bytes"
     return _fn(name)(R, rows, Hq, Hkv, D, dt)
+
+
+def _attention_bytes(name, dev, *sizes):
+    """The workspace of a call of these sizes on `dev`, whose compute units it goes by."""
+    f = _fn(name + "_workspace_bytes")
+    if _current_device() == dev.index:
+        nbytes = f(*sizes)
+    else:
+        with torch.cuda.device(dev):
+            nbytes = f(*sizes)
+    if nbytes == 0:
+        from . import EINVAL, DsparkError
+        raise DsparkError(name + "_workspace_bytes", EINVAL)
+    return nbytes
 
 
 def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, scales=None, anc=None, scale=None, out=None,
@@ -466,26 +484,18 @@ def tree_attention(q, k_cache, v_cache, table, ctx, row_off, *, scales=None, anc
     qp, qs = _rows(q, "q", dev, (rows, Hq, D), kind)
     R, W = _dims(table, "table", 2)
     a = [_chk(table, "table", dev, (R, W), _I32), _chk(ctx, "ctx", dev, (R,), _I32),
-         _chk(row_off, "row_off", dev, (R + 1,), _I32), _opt(anc, "anc", dev, (rows,), _I64)]
+         _chk(row_off, "row_off", dev, (R + 1,), _I32),
+         None if anc is None else _chk(anc, "anc", dev, (rows,), _I64)]
     if out is None:
         out = dict(o=torch.empty((rows, Hq, D), dtype=q.dtype, device=dev),
                    lse=torch.empty((rows, Hq), dtype=_F32, device=dev))
     b = [_chk(out["o"], "o", dev, (rows, Hq, D), q.dtype),
          _opt(out.get("lse"), "lse", dev, (rows, Hq), _F32),
-         _opt(status, "status", dev, (1,), _I32)]
+         None if status is None else _chk(status, "status", dev, (1,), _I32)]
     if R == 0 or rows == 0:
         return out
     if ws is None:
-        four = scales is not None
-        if _current_device() == dev.index:
-            nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four)
-        else:  # the size goes by the device's compute units
-            with torch.cuda.device(dev):
-                nbytes = tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four)
-        if nbytes == 0:
-            from . import EINVAL, DsparkError
-            raise DsparkError(name + "_workspace_bytes", EINVAL)
-        ws, wp, wb = _workspace(nbytes, dev)
+        ws, wp, wb = _workspace(_attention_bytes(name, dev, R, rows, Hq, Hkv, D, dt), dev)
     else:
         ws, wp, wb = _given(ws, dev)
     _call(dev, name, R, rows, Hq, Hkv, D, dt, page, W, P, qp, qs, kp, vp, *st,
