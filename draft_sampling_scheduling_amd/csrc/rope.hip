@@ -8,10 +8,11 @@
 // sines come from the row of a table that the row's position names.  About six operations an
 // element, so HBM bounds it: each element is read and written once.
 //
-// A lane has 8 elements of a head, as many lanes as hold a head (8, 16 or 32) work on it, and go
-// through the heads of their row with the row's cosines and sines in registers.  The other
-// halves of the pairs are loaded beside a lane's own (the same lines, so HBM sees them once); all
-// of a head's loads return before any of it is stored, so rows may be turned in place.
+// A lane has two pieces of 8 elements of a head that hold both halves of its pairs, so a cosine and a
+// sine are loaded for each pair once; D / 16 lanes work on a head, and go through heads of their row with
+// the row's cosines and sines in registers.  (A piece a lane, the other halves loaded beside it, took
+// twice the loads: 32 against 23 us for 1280 rows of 32 and 8 heads of 128 into 4 bits.)  All of a
+// head's loads return before any of it is stored, so rows may be turned in place.
 // float throughout, rounded once; but keys on their way to 4 bits are taken in double: a code's
 // step is up to half of its value, so at a border the last bit of a float decides about that
 // much, and in double the code is that of the formula's value.
@@ -77,15 +78,13 @@ struct Eight {  // 8 elements as they lie in memory
   }
 };
 
-// sum over the LPR lanes (8, 16 or 32, aligned) that hold a head, the same in each
-template <int LPR>
-__device__ __forceinline__ float head_sum(float v) {
-  v += __uint_as_float(xlane_partner<0>(__float_as_uint(v)));
-  v += __uint_as_float(xlane_partner<1>(__float_as_uint(v)));
-  v += __uint_as_float(xlane_partner<2>(__float_as_uint(v)));
-  if (LPR > 8) v += __uint_as_float(xlane_partner<3>(__float_as_uint(v)));
-  if (LPR > 16) v += __uint_as_float(xlane_partner<4>(__float_as_uint(v)));
-  return v;
+template <int STEP>
+__device__ __forceinline__ uint32_t partner(uint32_t v) {
+  return xlane_partner<STEP>(v);
+}
+template <int STEP>
+__device__ __forceinline__ float partner(float v) {
+  return __uint_as_float(xlane_partner<STEP>(__float_as_uint(v)));
 }
 template <int STEP>
 __device__ __forceinline__ double partner(double v) {
@@ -93,159 +92,188 @@ __device__ __forceinline__ double partner(double v) {
   const uint64_t lo = xlane_partner<STEP>((uint32_t)u), hi = xlane_partner<STEP>((uint32_t)(u >> 32));
   return __longlong_as_double((long long)(hi << 32 | lo));
 }
-template <int LPR>
-__device__ __forceinline__ double head_sum(double v) {
-  v += partner<0>(v);
-  v += partner<1>(v);
-  v += partner<2>(v);
-  if (LPR > 8) v += partner<3>(v);
-  if (LPR > 16) v += partner<4>(v);
+// over the LPR lanes (4, 8 or 16, aligned) that hold a head, the same in each
+template <int LPR, class V, class Op>
+__device__ __forceinline__ V head_reduce(V v, Op op) {
+  v = op(v, partner<0>(v));
+  v = op(v, partner<1>(v));
+  if (LPR > 4) v = op(v, partner<2>(v));
+  if (LPR > 8) v = op(v, partner<3>(v));
   return v;
 }
 
 // What a lane knows of its row and its place in a head.
 template <class T, int LPR>
 struct RopeLane {
-  static constexpr int kE = sizeof(T);
-  int at, other;     // its first element, and that of the other halves of its pairs
-  bool live, apart;  // it has elements at all; pairs are not neighbours
-  float c[8], s[8];  // y = x c + (other of the pair) s
+  int ca, cb;         // its pieces of 8 elements
+  int pair;           // of its pairs the first, by eights
+  bool live, turns;   // it has any; its pairs turn
+  bool apart;         // pairs are one element of either piece, not neighbours in one
+  float c[8], s[8];   // of its pairs
 
-  __device__ __forceinline__ void begin(const RopeArgs& p, int chunk, int pos) {
-    live = 8 * chunk < p.D;
-    at = live ? 8 * chunk : 0;
-    other = at;
+  __device__ __forceinline__ void place(const RopeArgs& p, int l) {
+    live = 16 * l < p.D;
+    l = live ? l : 0;  // (lanes past the head do as the first, and store nothing)
+    pair = l;
     apart = !p.interleaved;
-    const int half = p.rot / 2;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      c[e] = 1.0f;
-      s[e] = 0.0f;
-    }
-    if (!p.rope || at >= p.rot) return;
-    const float* line = p.rope + (int64_t)pos * p.rot;
-    if (apart) {
-      const bool first = at < half;
-      other = first ? at + half : at - half;
-      const int i = first ? at : other;
-      ld8(line + i, c);
-      ld8(line + half + i, s);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = first ? -s[e] : s[e];
-    } else {
-      const float4 x = *reinterpret_cast<const float4*>(line + at / 2);
-      const float4 y = *reinterpret_cast<const float4*>(line + half + at / 2);
-      const float cs[4] = {x.x, x.y, x.z, x.w}, sn[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e] = cs[e / 2];
-        s[e] = e % 2 ? sn[e / 2] : -sn[e / 2];
-      }
+    const int half = p.rot / 16;  // pieces that hold the first halves
+    turns = p.rope && l < half;
+    ca = 2 * l;
+    cb = ca + 1;
+    if (apart) {  // those behind the turned ones are taken in order
+      ca = turns ? l : 2 * half + 2 * (l - half);
+      cb = turns ? l + half : ca + 1;
     }
   }
+  __device__ __forceinline__ void angles(const RopeArgs& p, int pos) {
+    if (!turns) return;
+    const float* line = p.rope + (int64_t)pos * p.rot + 8 * pair;
+    ld8(line, c);
+    ld8(line + p.rot / 2, s);
+  }
 
-  // a lane's elements of a head, in F (float or double), of its own and its pairs' other halves
+  // a lane's pieces of a head, normed and turned, in F (float or double)
   template <class F, bool NORM>
-  __device__ __forceinline__ void turn(const RopeArgs& p, const Eight<T>& own, const Eight<T>& far,
-                                       const Eight<T>& w, const Eight<T>& wf, F (&y)[8]) const {
-    F x[8], z[8];
+  __device__ __forceinline__ void turn(const RopeArgs& p, const Eight<T>& a, const Eight<T>& b, const Eight<T>& wa,
+                                       const Eight<T>& wb, F (&ya)[8], F (&yb)[8]) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      x[e] = (F)own.at(e);
-      z[e] = (F)(apart ? far.at(e) : own.at(e ^ 1));
+      ya[e] = (F)a.at(e);
+      yb[e] = (F)b.at(e);
     }
     if (NORM) {
       F sum = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += x[e] * x[e];
-      sum = head_sum<LPR>(live ? sum : (F)0);
+      for (int e = 0; e < 8; ++e) sum += ya[e] * ya[e];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += yb[e] * yb[e];
+      sum = head_reduce<LPR>(live ? sum : (F)0, [](F x, F y) { return x + y; });
       const F f = (F)1 / sqrt(sum / (F)p.D + (F)p.eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = x[e] * f * (F)w.at(e);
-        z[e] = z[e] * f * (F)(apart ? wf.at(e) : w.at(e ^ 1));
+        ya[e] = ya[e] * f * (F)wa.at(e);
+        yb[e] = yb[e] * f * (F)wb.at(e);
       }
     }
-    // (a lane without pairs has c = 1, s = 0: whatever z is, it must not reach y)
-    const bool turns = p.rope && at < p.rot;
+    if (!turns) return;
+    if (apart) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = turns ? x[e] * (F)c[e] + z[e] * (F)s[e] : x[e];
+      for (int e = 0; e < 8; ++e) {
+        const F x = ya[e], y = yb[e];
+        ya[e] = x * (F)c[e] - y * (F)s[e];
+        yb[e] = y * (F)c[e] + x * (F)s[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        F* z = e < 4 ? ya + 2 * e : yb + 2 * (e - 4);
+        const F x = z[0], y = z[1];
+        z[0] = x * (F)c[e] - y * (F)s[e];
+        z[1] = y * (F)c[e] + x * (F)s[e];
+      }
+    }
+  }
+
+  // a lane's pieces into a 4-bit cache: their groups' largest values meet, then their codes
+  template <class F>
+  __device__ __forceinline__ void put4(const RopeArgs& p, int c0, int c1, const F (&ya)[8], const F (&yb)[8],
+                                       char* codes, uint8_t* scale) const {
+    uint32_t a[8], b[8], ta = 0, tb = 0, ba = 0, bb = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      a[e] = fp4_bits(ya[e]);
+      b[e] = fp4_bits(yb[e]);
+      ta = max(ta, a[e] & 0x7FFFFFFFu);
+      tb = max(tb, b[e] & 0x7FFFFFFFu);
+    }
+    const int ga = c0 / 4, gb = c1 / 4;
+#pragma unroll
+    for (int g = 0; g < LPR / 2; ++g) {  // (heads of 64 have four lanes, of 128 eight)
+      const uint32_t mine = max(ga == g ? ta : 0u, gb == g ? tb : 0u);
+      const uint32_t byte = fp4_byte(head_reduce<LPR>(mine, [](uint32_t x, uint32_t y) { return max(x, y); }));
+      ba = ga == g ? byte : ba;
+      bb = gb == g ? byte : bb;
+    }
+    reinterpret_cast<uint32_t*>(codes)[c0] = fp4_codes(a, ba);
+    reinterpret_cast<uint32_t*>(codes)[c1] = fp4_codes(b, bb);
+    if (c0 % 4 == 0) scale[ga] = (uint8_t)ba;
+    if (c1 % 4 == 0) scale[gb] = (uint8_t)bb;
   }
 };
 
-// the largest of four neighbouring lanes, which hold a group
-__device__ __forceinline__ uint32_t group_top(uint32_t u) {
-  u = max(u, xlane_partner<0>(u));
-  return max(u, xlane_partner<1>(u));
-}
-
-template <class F>
-__device__ __forceinline__ void put4(const F (&y)[8], int chunk, char* codes, uint8_t* scale) {
-  uint32_t bits[8], top = 0;
+// A row's heads from one source (q, k or v), every slices-th of them: those of a batch are loaded
+// together.
+template <class T>
+struct Heads {
+  static constexpr int kBatch = 2;  // (four: 40 to 44 us where two take 37, 8192 rows of 32 and 8 heads)
+  Eight<T> a[kBatch], b[kBatch];
+  __device__ __forceinline__ void load(const T* x, int D, int ca, int cb, int h, int step, int heads) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    bits[e] = fp4_bits(y[e]);
-    top = max(top, bits[e] & 0x7FFFFFFFu);
+    for (int u = 0; u < kBatch; ++u)
+      if (h + u * step < heads) {
+        a[u].load(x + (int64_t)(h + u * step) * D + 8 * ca);
+        b[u].load(x + (int64_t)(h + u * step) * D + 8 * cb);
+      }
   }
-  const uint32_t byte = fp4_byte(group_top(top));
-  reinterpret_cast<uint32_t*>(codes)[chunk] = fp4_codes(bits, byte);
-  if (chunk % 4 == 0) scale[chunk / 4] = (uint8_t)byte;
-}
+};
 
 template <class T, int LPR, RopeTo TO, bool NORM>
 __global__ void __launch_bounds__(256) rope_kernel(RopeArgs p) {
+  using H = Heads<T>;
   const int64_t group = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;
   const int i = (int)(group / p.slices), slice = (int)(group - (int64_t)i * p.slices);
-  const int live = p.n_rows ? min(p.rows, *p.n_rows) : p.rows;
-  if (i >= live) return;
-  const int chunk = threadIdx.x % LPR;
-  const bool tell = slice == 0 && chunk == 0;
-  int pos = 0;
-  if (p.rope) {
-    pos = p.position[i];
-    if (pos < 0 || pos >= p.n_pos) {
-      if (tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
-      return;
-    }
-  }
+  if (i >= p.rows) return;
+  const int l = threadIdx.x % LPR;
   RopeLane<T, LPR> r;
-  r.begin(p, chunk, pos);
-  // `heads` heads of a row, from head `h0` on: f(head, own, far, w, wf)
-  const auto each = [&](const void* src, int64_t row, const void* norm, int h0, int heads, auto f) {
-    const T* x = static_cast<const T*>(src) + i * row;
-    Eight<T> w{}, wf{};
+  r.place(p, l);
+  // what a row is needs a trip to memory each, and so do its heads: all are asked for before any is
+  // looked at (a row past *n_rows, or of no position, is read and not used)
+  const int live = p.n_rows ? *p.n_rows : p.rows;
+  const int pos = p.rope ? p.position[i] : 0;
+  const int s = TO != kToRows ? p.slot[i] : 0;
+  H x;
+  int h = slice;
+  if (p.q) x.load(static_cast<const T*>(p.q) + i * p.q_row, p.D, r.ca, r.cb, h, p.slices, p.Hq);
+  const bool tell = slice == 0 && l == 0;
+  if (i >= live) return;
+  if (p.rope && (pos < 0 || pos >= p.n_pos)) {
+    if (tell) raise_fault(p.status, DSPARK_FAULT_PARAM);
+    return;
+  }
+  r.angles(p, pos);
+  // the heads from h on, their first batch loaded already if `loaded`: f(head, a, b, wa, wb)
+  const auto each = [&](const void* src, int64_t row, const void* norm, int heads, bool loaded, auto f) {
+    const T* y = static_cast<const T*>(src) + i * row;
+    Eight<T> wa{}, wb{};
     if (NORM && norm) {
-      w.load(static_cast<const T*>(norm) + r.at);
-      wf.load(static_cast<const T*>(norm) + r.other);
+      wa.load(static_cast<const T*>(norm) + 8 * r.ca);
+      wb.load(static_cast<const T*>(norm) + 8 * r.cb);
     }
-    constexpr int kBatch = 4;  // heads whose loads are under way together
-    for (int h = h0; h < heads; h += kBatch * p.slices) {
-      Eight<T> own[kBatch], far[kBatch];
+    for (; h < heads; h += H::kBatch * p.slices) {
+      if (!loaded) x.load(y, p.D, r.ca, r.cb, h, p.slices, heads);
+      loaded = false;
 #pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int hu = min(h + u * p.slices, heads - 1);
-        own[u].load(x + (int64_t)hu * p.D + r.at);
-        far[u].load(x + (int64_t)hu * p.D + r.other);
-      }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int hu = h + u * p.slices;
-        if (hu < heads) f(hu, own[u], far[u], w, wf);
-      }
+      for (int u = 0; u < H::kBatch; ++u)
+        if (h + u * p.slices < heads) f(h + u * p.slices, x.a[u], x.b[u], wa, wb);
     }
   };
-  int h = slice;
+  const auto put = [&](T* to, const float (&ya)[8], const float (&yb)[8]) {
+    Eight<T> out;
+    if (!r.live) return;
+    out.set(ya);
+    out.store(to + 8 * r.ca);
+    out.set(yb);
+    out.store(to + 8 * r.cb);
+  };
   if (p.q) {
-    each(p.q, p.q_row, p.q_norm, h, p.Hq, [&](int head, const Eight<T>& own, const Eight<T>& far,
-                                              const Eight<T>& w, const Eight<T>& wf) {
-      float y[8];
+    each(p.q, p.q_row, p.q_norm, p.Hq, true, [&](int head, const Eight<T>& a, const Eight<T>& b,
+                                                 const Eight<T>& wa, const Eight<T>& wb) {
+      float ya[8], yb[8];
       if (NORM && p.q_norm)
-        r.template turn<float, true>(p, own, far, w, wf, y);
+        r.template turn<float, true>(p, a, b, wa, wb, ya, yb);
       else
-        r.template turn<float, false>(p, own, far, w, wf, y);
-      Eight<T> out;
-      out.set(y);
-      if (r.live) out.store(static_cast<T*>(p.q_out) + i * p.qo_row + (int64_t)head * p.D + r.at);
+        r.template turn<float, false>(p, a, b, wa, wb, ya, yb);
+      put(static_cast<T*>(p.q_out) + i * p.qo_row + (int64_t)head * p.D, ya, yb);
     });
     // the heads after these go on with the slices where they stopped
     h = (slice + p.slices - p.Hq % p.slices) % p.slices;
@@ -254,7 +282,6 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs p) {
   char *kc = nullptr, *vc = nullptr;
   uint8_t* sc = nullptr;
   if (TO != kToRows) {
-    const int s = p.slot[i];
     if (s < 0 || (s >> p.lg) >= p.n_pages) {
       if (s != -1 && tell) raise_fault(p.status, DSPARK_FAULT_PAGE);
       return;
@@ -264,39 +291,40 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeArgs p) {
     vc = p.v_cache + page * p.page_b + tok * p.tok_b;
     if (TO == kToCache4) sc = p.scales + page * p.s_page + tok * p.s_tok;
   }
-  each(p.k, p.k_row, p.k_norm, h, p.Hkv, [&](int head, const Eight<T>& own, const Eight<T>& far,
-                                             const Eight<T>& w, const Eight<T>& wf) {
+  const int k0 = h;
+  each(p.k, p.k_row, p.k_norm, p.Hkv, false, [&](int head, const Eight<T>& a, const Eight<T>& b,
+                                                 const Eight<T>& wa, const Eight<T>& wb) {
     typedef typename std::conditional<TO == kToCache4, double, float>::type F;
-    F y[8];
+    F ya[8], yb[8];
     if (NORM && p.k_norm)
-      r.template turn<F, true>(p, own, far, w, wf, y);
+      r.template turn<F, true>(p, a, b, wa, wb, ya, yb);
     else
-      r.template turn<F, false>(p, own, far, w, wf, y);
-    if constexpr (TO == kToCache4) {
-      put4(y, chunk, kc + head * p.head_b, sc + head * p.s_head);
-    } else {
-      Eight<T> out;
-      out.set(y);
-      T* to = TO == kToRows ? static_cast<T*>(p.k_out) + i * p.ko_row + (int64_t)head * p.D
-                            : reinterpret_cast<T*>(kc + head * p.head_b);
-      if (r.live) out.store(to + r.at);
-    }
+      r.template turn<F, false>(p, a, b, wa, wb, ya, yb);
+    if constexpr (TO == kToCache4)
+      r.put4(p, r.ca, r.cb, ya, yb, kc + head * p.head_b, sc + head * p.s_head);
+    else if (TO == kToRows)
+      put(static_cast<T*>(p.k_out) + i * p.ko_row + (int64_t)head * p.D, ya, yb);
+    else
+      put(reinterpret_cast<T*>(kc + head * p.head_b), ya, yb);
   });
   if (TO == kToRows) return;
-  h = (h + p.slices - p.Hkv % p.slices) % p.slices;
-  const T* x = static_cast<const T*>(p.v) + i * p.v_row;
-  for (; h < p.Hkv; h += p.slices) {
-    Eight<T> own;
-    own.load(x + (int64_t)h * p.D + r.at);
+  h = (k0 + p.slices - p.Hkv % p.slices) % p.slices;
+  each(p.v, p.v_row, nullptr, p.Hkv, false, [&](int head, const Eight<T>& a, const Eight<T>& b,
+                                                const Eight<T>&, const Eight<T>&) {
     if constexpr (TO == kToCache4) {
-      float y[8];
+      float ya[8], yb[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = own.at(e);
-      put4(y, chunk, vc + h * p.head_b, sc + h * p.s_head + p.D / kGroup4);
-    } else {
-      if (r.live) own.store(reinterpret_cast<T*>(vc + h * p.head_b) + r.at);
+      for (int e = 0; e < 8; ++e) {
+        ya[e] = a.at(e);
+        yb[e] = b.at(e);
+      }
+      r.put4(p, r.ca, r.cb, ya, yb, vc + head * p.head_b, sc + head * p.s_head + p.D / kGroup4);
+    } else if (r.live) {
+      T* to = reinterpret_cast<T*>(vc + head * p.head_b);
+      a.store(to + 8 * r.ca);
+      b.store(to + 8 * r.cb);
     }
-  }
+  });
 }
 
 // Tokens of a 4-bit cache as values: a thread per eight elements of a token's keys and values.
@@ -362,32 +390,38 @@ static bool rows_meet(const void* a, int64_t a_row, int64_t na, const void* b, i
   return r < na || r + nb > a_row;
 }
 
-// Groups of lanes (a head each at a time) that a row's heads are spread over: few rows want all
-// lanes they can get; many go through their heads in turn, the cosines and sines loaded once.
-static int rope_slices(int rows, int heads) {
-  const int64_t want = 32768 / (int64_t)rows;
-  return want < 1 ? 1 : (want > heads ? heads : (int)want);
+// Groups of lanes (a head each at a time) that a row's heads are spread over: few rows want all lanes
+// they can get; of many, a group goes through several heads with the row's cosines and sines, loaded
+// once.  us for 1, 2, 4, 8, 16 groups a row: 8192 rows to rows, 40 heads of 128, 45, 44, 41, 37, 40; to the
+// cache, 48 heads, 59, 51, 48, 44, 47; into 4 bits with norms, in whose double precision a group's weights
+// cost more, 68, 61, 60, 66, 74; 1280 rows of that, for 6, 12 and 25 groups, 24, 23, 25.
+static int rope_slices(int rows, int heads, bool slow) {
+  int least = 1;  // groups a row has at the least: a group takes 8 (16) heads at the most
+  while (least * (slow ? 16 : 8) < heads) least *= 2;
+  int64_t want = (slow ? 16384 : 32768) / (int64_t)rows;
+  want = want < least ? least : want;
+  return want > heads ? heads : (int)want;
 }
 
 template <class T, RopeTo TO, bool NORM>
 static int rope_launch(const RopeArgs& p, hipStream_t stream) {
-  const int lpr = p.D <= 64 ? 8 : (p.D <= 128 ? 16 : 32);
+  const int lpr = p.D <= 64 ? 4 : (p.D <= 128 ? 8 : 16);
   const int64_t blocks = ((int64_t)p.rows * p.slices * lpr + 255) / 256;
   if (blocks >= (1 << 24)) return DSPARK_EINVAL;  // a grid holds 2^32 threads
-  if (lpr == 8)
+  if (lpr == 4)
+    rope_kernel<T, 4, TO, NORM><<<(unsigned)blocks, 256, 0, stream>>>(p);
+  else if (lpr == 8)
     rope_kernel<T, 8, TO, NORM><<<(unsigned)blocks, 256, 0, stream>>>(p);
-  else if (lpr == 16)
-    rope_kernel<T, 16, TO, NORM><<<(unsigned)blocks, 256, 0, stream>>>(p);
   else if constexpr (TO != kToCache4)
-    rope_kernel<T, 32, TO, NORM><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    rope_kernel<T, 16, TO, NORM><<<(unsigned)blocks, 256, 0, stream>>>(p);
   return launch_status();
 }
 
 template <RopeTo TO>
 static int rope_run(RopeArgs p, dspark_dtype dt, hipStream_t stream) {
   const int heads = (p.q ? p.Hq : 0) + (p.k ? p.Hkv : 0) + (p.v ? p.Hkv : 0);
-  p.slices = rope_slices(p.rows, heads);
   const bool norm = p.q_norm || p.k_norm;
+  p.slices = rope_slices(p.rows, heads, TO == kToCache4 && norm);
   if (dt == DSPARK_BF16)
     return norm ? rope_launch<uint16_t, TO, true>(p, stream) : rope_launch<uint16_t, TO, false>(p, stream);
   return norm ? rope_launch<float, TO, true>(p, stream) : rope_launch<float, TO, false>(p, stream);
