@@ -433,7 +433,7 @@ static int rope_args(RopeArgs& p, int rows, int Hq, int Hkv, int D, int rot, int
                      const float* rope, int n_pos, const void* q_norm, const void* k_norm, double eps,
                      const int32_t* n_rows, int32_t* status) {
   if (rows < 0 || Hkv < 0 || Hq < 0 || D < 16 || D % 16 != 0 || D > 256 || Hq > (1 << 20) || Hkv > (1 << 20) ||
-      (dt != DSPARK_F32 && dt != DSPARK_BF16) || !(eps >= 0.0) || !(eps <= 1e30))
+      (dt != DSPARK_F32 && dt != DSPARK_BF16) || !(eps <= 1e30) || !(eps == 0.0 || eps >= 1e-30))
     return DSPARK_EINVAL;
   if (rope && (rot < 16 || rot % 16 != 0 || rot > D || n_pos < 1)) return DSPARK_EINVAL;
   const size_t e = dt == DSPARK_BF16 ? 2 : 4;

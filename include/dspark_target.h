@@ -121,14 +121,15 @@ int dspark_cache_append(int rows, int Hkv, int D, dspark_dtype dt, int page_size
  *   a' = a cos - b sin, b' = b cos + a sin  for the pairs (a, b) of x^'s first `rot` elements:
  *        (i, i + rot/2), or (2i, 2i+1) with interleaved != 0; the rest as it is
  * cos, sin: row position[i] of rope [n_pos][rot] float, rot/2 cosines, then rot/2 sines (rope NULL:
- * nothing is turned, position is not read).  In float, rounded once.
+ * nothing is turned, position is not read).  In float, the squares too, rounded once.
  * q, k rows of Hq, Hkv heads of D contiguous elements, q_row and k_row elements apart (either may
  * be NULL); outputs the same, qo_row and ko_row apart: the inputs themselves (same address and
  * stride), or memory that shares nothing with q, k and each other; the slices of a fused
- * projection's rows count as apart.  n_rows (device, nullable): only the first *n_rows rows exist.
+ * projection's rows count as apart.  n_rows (device, nullable): only the first *n_rows rows exist;
+ * those behind, up to `rows`, may be read and are left as they were.
  * A position outside [0, n_pos) leaves its row alone (DSPARK_FAULT_PARAM).
- * D % 16 == 0, 16 <= D <= 256; rot % 16 == 0, 16 <= rot <= D; eps >= 0; strides multiples of 16
- * bytes, pointers 16-byte aligned.
+ * D % 16 == 0, 16 <= D <= 256; rot % 16 == 0, 16 <= rot <= D; eps 0, or 1e-30 .. 1e30; strides
+ * multiples of 16 bytes, pointers 16-byte aligned.
  * ------------------------------------------------------------------------------------ */
 int dspark_qk_rope(int rows, int Hq, int Hkv, int D, int rot, int interleaved, dspark_dtype dt,
                    const void *q, int64_t q_row, const void *k, int64_t k_row,
@@ -151,7 +152,7 @@ int dspark_rope_append(int rows, int Hq, int Hkv, int D, int rot, int interleave
                        int32_t *dev_status, hipStream_t stream);
 
 /* The same into a cache of 4 bits.  Keys are normed and turned in double: their codes are those of
- * the formula's values. */
+ * the formula's values.  Of rows with the same slot, codes of the one may meet scales of the other. */
 int dspark_cache4_append(int rows, int Hq, int Hkv, int D, int rot, int interleaved,
                          dspark_dtype dt, int page_size, int n_pages, const void *q,
                          int64_t q_row, const void *k, int64_t k_row, const void *v,
@@ -207,7 +208,8 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
 
 /* The same over a cache of 4 bits; q and o in dt.  The cache's values are exact operands, and rows
  * are as above: bf16 rows have their weights rounded to bf16, float ones are in float throughout.
- * A group that reads NaN reaches the 32 elements of o it stands for, of rows that see its token. */
+ * A group that reads NaN reaches the 32 elements of o it stands for, of rows that see its token.
+ * Token strides up to 2^21 bytes, page strides below 2^32. */
 size_t dspark_tree_attention4_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
                                               dspark_dtype dt);
 

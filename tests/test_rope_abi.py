@@ -138,3 +138,11 @@ def test_commit4_refusals(ds):
         assert call(**bad) == ds.EINVAL, bad
     assert call(ws_bytes=ws - 1) == ds.EWORKSPACE
     assert call(R=0) == ds.OK
+
+
+def test_eps_that_float_loses(ds):
+    """An eps that is nothing as a float would turn a head of zeros into NaN: refused."""
+    for eps, rc in ((1e-46, ds.EINVAL), (9e-31, ds.EINVAL), (1.1e30, ds.EINVAL), (0.0, ds.OK), (1e-30, ds.OK),
+                    (1e30, ds.OK)):
+        assert ds.lib().dspark_qk_rope(0, 4, 2, 64, 64, 0, ds.BF16, P(), 512, P(0x200000), 512, P(), P(), 10, None,
+                                       None, eps, None, P(0x300000), 256, P(0x400000), 128, None, None) == rc, eps
