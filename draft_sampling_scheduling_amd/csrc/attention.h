@@ -544,7 +544,9 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p, bool a
     };
     // few loads where there are few pieces: those of missing ones take their time too
     constexpr int kMost = DEEP ? 12 : 4;
-    if (jt.count <= 2 * NP) {
+    if (jt.count <= NP) {
+      take(std::integral_constant<int, 1>{}, 0);
+    } else if (jt.count <= 2 * NP) {
       take(std::integral_constant<int, 2>{}, 0);
     } else if (DEEP && jt.count <= 4 * NP) {
       take(std::integral_constant<int, 4>{}, 0);
@@ -655,11 +657,13 @@ static int att_launch(typename W::Params p, hipStream_t stream) {
   // a wave per row of a row tile, as far as the host knows how many rows there are
   const int64_t m = (int64_t)((p.rows + p.R - 1) / p.R) * p.G;
   int slices = m < kRows * NR ? (int)(m + 3) / 4 : 8 * NR;
-  if (W::kMix) {
-    // Twice as many workgroups here, each with a joint at most: so many slices that all of them about
-    // fit the chip twice (256 requests of 512 to 4096 tokens, of 4 bits: 4 slices 168, 9 172 us; 64 of
-    // 100 to 2048, a quarter of whose workgroups have joints: 31 and 28.5).
-    const int64_t lists = (int64_t)p.R * p.Hkv, joints = lists < grid ? lists : grid;
+  const int64_t tiles = (m + kRows * NR - 1) / (kRows * NR);
+  if (W::kMix || tiles > 1) {
+    // Many workgroups have joints, each one at most: so many slices that all of them about fit the
+    // chip twice (256 requests of 512 to 4096 tokens, of 4 bits: 4 slices 168, 9 172 us; 64 of 100 to
+    // 2048, a quarter of whose workgroups have joints: 31 and 28.5; 2048 rows behind 4048 tokens, in 512
+    // pieces of 128 rows: 4 slices 231, 16 233, 32 237).
+    const int64_t lists = (int64_t)p.R * p.Hkv * (W::kMix ? 1 : tiles), joints = lists < grid ? lists : grid;
     const int most = (int)(4 * grid / joints);
     slices = slices < most ? slices : most;
   }

@@ -456,7 +456,7 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
 // ---------------------------------------------------------------------------------------
 // f(the variant that runs these shapes).  Past 64 query rows to a cache head (rows / R, the bound that the
 // host knows, times heads to a cache head) waves that share tiles save the others' conversions: 8192 rows
-// from an empty cache 667 against 791 us, 2048 behind 4048 239 and 253, 64 requests of 72 over 500 to
+// from an empty cache 667 against 791 us, 2048 behind 4048 231 and 253, 64 requests of 72 over 500 to
 // 4000 114 and 123; over short contexts the barriers cost as much (16 requests of 128 rows behind 1000
 // tokens 39 and 37).  Up to 64 they lose: 36 rows 343 and 242 us, 45 37 and 29.
 template <class F>
