@@ -11,7 +11,8 @@
 // the rate of a copy; a commit of 64 paths in 4 layers 5.8 us.  With their launches: a plan of one
 // prompt of 20000 rows 23 us, a commit that gives back the pages of 256 requests of 257 pages 8.8
 // us (two launches, as all of more table entries), of 64 paths of up to 16 nodes in 4 layers 12.1
-// us in memory of its own and 16.0 in place (two launches).
+// us in memory of its own and 16.0 in place (two launches).  Of a cache of 4 bits, 64 paths of up to 8
+// nodes in 4 layers of 4 heads of 128, codes and scales: 7.3 us.
 #include <atomic>
 
 #include "target.h"

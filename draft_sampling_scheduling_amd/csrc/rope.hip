@@ -6,7 +6,10 @@
 //   a' = a cos - b sin,   b' = b cos + a sin
 // for the pairs (a, b) of its first `rot` elements: (i, i + rot/2), or (2i, 2i + 1); cosines and
 // sines come from the row of a table that the row's position names.  About six operations an
-// element, so HBM bounds it: each element is read and written once.
+// element, so HBM bounds it: each element is read and written once.  Measured, kernels alone, bf16, heads
+// of 128: 8192 rows of 32 and 8 heads with norms to rows (172 MB) 36 us, 4.7 TB/s; 1280 rows of those and
+// 8 heads of values into the cache (32 MB) 11; 8192 rows of 40, 8 and 8 heads into 4 bits (212 MB) 51,
+// 4.2 TB/s; 8224 tokens of 8 heads back out (43 MB) 11.
 //
 // A lane has two pieces of 8 elements of a head that hold both halves of its pairs, so a cosine and a
 // sine are loaded for each pair once; D / 16 lanes work on a head, and go through heads of their row with
