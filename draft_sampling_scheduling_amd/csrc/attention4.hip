@@ -16,10 +16,10 @@
 //   - V needs tokens where memory has d, so it passes through LDS as bf16, by transposing reads.
 // Measured, bf16, D = 128, both kernels: 256 requests of 512 to 4096 tokens, 32 heads on 8, up to nine rows
 // (664 MB) 168 us, 4.0 TB/s where a copy gets 5.0 (vector instructions issue for 46 % of the time, LDS is
-// busy for 31 %, the matrix cores for 24 %); with three rows at most 147, with nine each, 36 to a cache
+// busy for 19 %, the matrix cores for 24 %); with three rows at most 147, with nine each, 36 to a cache
 // head, 240.  Two single tokens over 100001 to 131071, 40 heads on 8 (251 MB) 62 us; 64 trees over 100 to
 // 2048, 20 heads on 4 (41 MB) 26 to 29.  Prompts are bound by the softmax's vector work as over bf16: 2048
-// rows behind 4048 tokens 230 us, 740 TFLOP/s of the pairs seen, 8192 rows 667, 820.
+// rows behind 4048 tokens 230 us, 740 TFLOP/s of the pairs seen, 8192 rows 655, 840.
 #include "attention_wave.h"
 #include "fp4.h"
 
@@ -56,6 +56,14 @@ struct Fit4 {
   static constexpr int PER_SIMD = D == 64 ? (TERMS == 1 ? 3 : 2) : (TERMS == 1 ? 2 : 1);
   static constexpr int PER_CU = 4 * PER_SIMD / WAVES;
 };
+
+// How far V's 16-byte chunks of row t of a tile are moved, by exclusive or.  LDS takes writes of 16 bytes
+// a lane from 8 lanes at a time, over 32 banks, and here those hold one chunk of 8 rows; transposing reads
+// from 32 lanes, over 64 banks, 4 neighbouring chunks of 4 rows.  Neither meets itself.
+template <int D>
+__host__ __device__ constexpr int vswz4(int t) {
+  return D == 128 ? (t & 1) << 2 ^ ((t >> 1) & 1) * 10 ^ ((t >> 2) & 1) : (t & 3) << 1 ^ ((t >> 2) & 1);
+}
 
 // What a lane holds of a tile: half h of token n's keys and values, and their powers.
 template <int D>
@@ -98,11 +106,8 @@ struct Att4Wave : AttRows<D> {
   __device__ __forceinline__ Att4Wave(const Att4Params& p_, int wave, uint32_t lds)
       : B(p_), p(p_), wave_(wave), base(((lds + 255) & ~255u) + wave * F::TILE) {}
 
-  // V's tile: row t is token t, 16-byte chunk c of it at chunk c ^ swz(t).  A write takes one chunk
-  // of 32 rows, a transposing read 4 neighbouring chunks of 4 rows; both spread over the banks.
-  static __device__ __forceinline__ int swz(int t) {
-    return D == 128 ? (t & 3) << 2 | ((t >> 2) & 3) : ((t >> 1) & 1) << 2 | ((t >> 2) & 3);
-  }
+  // V's tile: row t is token t, 16-byte chunk c of it at chunk c ^ swz(t)
+  static __device__ __forceinline__ int swz(int t) { return vswz4<D>(t); }
 
   // Pages of tile t0, a page per 8 tokens (aligned, so they share one); past the last token, its page.
   // Scalar loads: they are waited for apart from the vector loads under way.
@@ -196,9 +201,9 @@ struct Att4Wave : AttRows<D> {
 #pragma unroll
       for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)  // (rows 8 apart differ in one bit of the swizzle)
+        for (int b = 0; b < 2; ++b)  // (rows 8 apart share a swizzle)
           a[dt].half[b] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (DSPARK_LDS s16x4*)(uintptr_t)((at ^ (uint32_t)(dt << 6 | b << 5)) + 8 * (2 * st + b) * RB));
+              (DSPARK_LDS s16x4*)(uintptr_t)((at ^ (uint32_t)(dt << 6)) + 8 * (2 * st + b) * RB));
 #pragma unroll
       for (int t = 0; t < TERMS; ++t) {
         bf16x8 pb;
@@ -343,12 +348,11 @@ struct Att4Wave : AttRows<D> {
 // barrier per tile.  Each of them converts the keys and values of 8 of the tile's tokens, a group of
 // 32 elements a lane, and the products are those over a bf16 cache.
 // ---------------------------------------------------------------------------------------
-// V's swizzle spreads writes of one chunk of 4 rows as well as the reads.
+// (K's chunks: read from 16 rows at a time, over 64 banks, and written as V's)
 template <int D>
 struct Tile4 : Tile<uint16_t, D> {
-  static __host__ __device__ constexpr int vswz(int r) {
-    return D == 128 ? (r & 3) << 2 | (r & 3) : ((r >> 1) & 1) << 2 | ((r >> 1) & 3);
-  }
+  static __host__ __device__ constexpr int vswz(int r) { return vswz4<D>(r); }
+  static __host__ __device__ constexpr int kswz(int r) { return D == 128 ? r & 15 : ((r >> 1) & 7) ^ (r & 1) << 2; }
 };
 
 template <int D>
@@ -381,8 +385,8 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
     keys = lane < LANES;
     any = lane < 2 * LANES;
     const int i = lane % LANES;
-    tok = i / GROUPS;
-    group = i % GROUPS;
+    tok = i % 8;
+    group = i / 8;
     const int x = keys ? L::kswz(mine + tok) : L::vswz(mine + tok);
     at = (uint32_t)(keys ? 0 : L::BYTES) + (uint32_t)(mine + tok) * L::RB + ((4 * group ^ x) << 4);
   }
@@ -464,7 +468,7 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
 // ---------------------------------------------------------------------------------------
 // f(the variant that runs these shapes).  Past 64 query rows to a cache head (rows / R, the bound that the
 // host knows, times heads to a cache head) waves that share tiles save the others' conversions: 8192 rows
-// from an empty cache 667 against 791 us, 2048 behind 4048 231 and 253, 64 requests of 72 over 500 to
+// from an empty cache 655 against 791 us, 2048 behind 4048 230 and 253, 64 requests of 72 over 500 to
 // 4000 114 and 123; over short contexts the barriers cost as much (16 requests of 128 rows behind 1000
 // tokens 39 and 37).  Up to 64 they lose: 36 rows 343 and 242 us, 45 37 and 29.
 template <class F>
