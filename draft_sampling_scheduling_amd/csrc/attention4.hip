@@ -352,14 +352,26 @@ struct Att4Wave : AttRows<D> {
 template <int D>
 struct Tile4 : Tile<uint16_t, D> {
   static __host__ __device__ constexpr int vswz(int r) { return vswz4<D>(r); }
-  static __host__ __device__ constexpr int kswz(int r) { return D == 128 ? r & 15 : ((r >> 1) & 7) ^ (r & 1) << 2; }
+  static __host__ __device__ constexpr int kswz(int r) {
+    return D == 128 ? r & 15 : ((r >> 1) & 7) ^ (r & 1) << 2;
+  }
+};
+
+// Three waves a SIMD at D = 64, two at D = 128.  64: 8192 rows 433 us, two waves 482; 2048 behind 4048 tokens
+// 164 and 176; 64 requests of 72 over 500 to 4000 85 and 95; 16 of 128 behind 1000 32.8 and 31.4.  128, where
+// three leave registers for half of the reads under way at a time: 641 and 650, 236 and 230, 119 and 122,
+// 42 and 39.
+template <int D>
+struct Fit4Shared : Fit<uint16_t, D, 4> {
+  static constexpr int PER_SIMD = D == 64 ? 3 : 2;
+  static constexpr int PER_CU = PER_SIMD;  // (four waves each)
 };
 
 template <int D>
 struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
   using A = AttWave<uint16_t, D, 4, Tile4<D>>;
   using Params = Att4Params;
-  using F = typename A::F;
+  using F = Fit4Shared<D>;
   using L = Tile4<D>;
   static constexpr int GROUPS = D / 32, LANES = 8 * GROUPS;  // lanes that a wave's 8 tokens' keys take
 
