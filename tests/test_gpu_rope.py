@@ -177,6 +177,28 @@ def test_a_bad_position_appends_nothing():
     assert int(st) == ds.FAULT_PARAM and torch.equal(k, k0) and torch.equal(v, v0)
 
 
+@pytest.mark.parametrize("four", [False, True])
+def test_rows_of_one_slot(four):
+    """Of rows with the same slot either's elements (codes, scales) remain, and nobody else's change."""
+    import draft_sampling_scheduling_amd as ds
+    r = Rows(11, 6, 2, 3, 128, 128, BF)
+    slots = [17, 4, 17, 9, 17, 4]
+    alone = []
+    for order in ([0, 1, 3], [2, 5, 3], [4, 1, 3]):  # each row as the only one of its slot
+        g = np.random.default_rng(1)
+        d = c4.Cache4(1, [40], [1], 3, 128, 16).dev4() if four else caches(g, 3, 3, 16, 128, BF, "phtd")
+        kw = dict(scales=d[2]) if four else {}
+        x = r.qkv[order].contiguous()
+        ds.rope_append(None, *r.split(x)[1:], d[0], d[1], T([slots[i] for i in order]), T(r.pos[order]), r.at()[1], **kw)
+        alone.append(d)
+    g = np.random.default_rng(1)
+    d = c4.Cache4(1, [40], [1], 3, 128, 16).dev4() if four else caches(g, 3, 3, 16, 128, BF, "phtd")
+    kw = dict(scales=d[2]) if four else {}
+    ds.rope_append(None, *r.split(r.qkv)[1:], d[0], d[1], T(slots), *r.at(), **kw)
+    for got, *want in zip(d, *alone):
+        assert torch.stack([got == w for w in want]).any(0).all()
+
+
 def edges(g, rows, heads, D, dtype):
     """Values whose groups try the quantising: borders, zeros, one large, tiny, huge, infinite, NaN."""
     x = g.standard_normal((rows, heads, D)).astype(np.float32)
