@@ -199,16 +199,18 @@ def _cache4(k_cache, v_cache, scales, dev, dims):
     Tensor, i = torch.Tensor, dev.index
     if (isinstance(k_cache, Tensor) and isinstance(v_cache, Tensor) and isinstance(scales, Tensor) and
             k_cache.dtype is _U8 and v_cache.dtype is _U8 and scales.dtype is _U8):
-        shape, st, sst = k_cache.shape, k_cache.stride(), scales.stride()
+        shape, st, vst, sst = k_cache.shape, k_cache.stride(), v_cache.stride(), scales.stride()
         *lead, half = shape
         g = half // 16
-        if (len(lead) == dims - 1 and (g == 2 or g == 4) and 1 not in lead and st[-1] == 1 and
-                v_cache.shape == shape and v_cache.stride() == st and scales.shape == (*lead, 2, g) and
+        if 1 in lead:  # a dimension of size 1, whose stride is never used
+            st, vst, sst = [[0 if n == 1 else a for a, n in zip(x, (*lead, 2, 2))] for x in (st, vst, sst)]
+        if (len(lead) == dims - 1 and (g == 2 or g == 4) and st[-1] == 1 and
+                v_cache.shape == shape and vst == st and scales.shape == (*lead, 2, g) and
                 sst[-1] == 1 and sst[-2] == g and half == 16 * g and k_cache.get_device() == i and
                 v_cache.get_device() == i and scales.get_device() == i):
             return (k_cache.data_ptr(), v_cache.data_ptr(), (*lead, 2 * half), st[:-1],
                     scales.data_ptr(), sst[:-2])
-    # what is wrong, or a dimension of size 1, whose stride is never used
+    # what is wrong
     kp, vp, shape, st = _cache(k_cache, v_cache, dev, dims)
     if k_cache.dtype is not _U8:
         raise TypeError(f"k_cache must be uint8 beside scales, got {k_cache.dtype}")

@@ -251,3 +251,18 @@ def test_refusals():
             go(**a)
     with pytest.raises(TypeError):  # codes without their scales
         ds.tree_attention(q, k, v, t, T([40]), T([0, 3]))
+
+
+def test_strides_that_are_never_used():
+    """A dimension of size 1 may have any stride, another one in each tensor."""
+    import draft_sampling_scheduling_amd as ds
+    c = c4.Cache4(3, [40], [3], 1, 64, 16)
+    k, v, s = c.dev4()
+    t = torch.from_numpy(c.table).to("cuda:0")
+    q = torch.randn(3, 4, 64, device="cuda:0").to(BF)
+    want = ds.tree_attention(q, k, v, t, T([40]), T([0, 3]), scales=s)
+    odd = [x.as_strided(x.shape, (x.stride(0), w, *x.stride()[2:])) for x, w in ((k, 7), (v, 3), (s, 1))]
+    got = ds.tree_attention(q, odd[0], odd[1], t, T([40]), T([0, 3]), scales=odd[2])
+    assert torch.equal(got["o"], want["o"]) and torch.equal(got["lse"], want["lse"])
+    back = ds.cache_read(*odd, T([5, 9]))
+    assert all(torch.equal(back[x], y) for x, y in ds.cache_read(k, v, s, T([5, 9])).items())
