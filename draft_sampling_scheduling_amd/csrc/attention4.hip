@@ -15,9 +15,9 @@
 //     over d may be taken in any order, the queries are loaded to match.
 //   - V needs tokens where memory has d, so it passes through LDS as bf16, by transposing reads.
 // Measured, bf16, D = 128, both kernels: 256 requests of 512 to 4096 tokens, 32 heads on 8, up to nine rows
-// (664 MB) 168 us, 4.0 TB/s where a copy gets 5.0 (vector instructions issue for 46 % of the time, LDS is
+// (664 MB) 166 us, 4.0 TB/s where a copy gets 5.0 (vector instructions issue for 46 % of the time, LDS is
 // busy for 19 %, the matrix cores for 24 %); with three rows at most 147, with nine each, 36 to a cache
-// head, 240.  Two single tokens over 100001 to 131071, 40 heads on 8 (251 MB) 62 us; 64 trees over 100 to
+// head, 235.  Two single tokens over 100001 to 131071, 40 heads on 8 (251 MB) 62 us; 64 trees over 100 to
 // 2048, 20 heads on 4 (41 MB) 26 to 29.  Prompts are bound by the softmax's vector work as over bf16: 2048
 // rows behind 4048 tokens 230 us, 740 TFLOP/s of the pairs seen, 8192 rows 655, 840.
 #include "attention_wave.h"
@@ -288,6 +288,9 @@ struct Att4Wave : AttRows<D> {
     const bool edge = t0 + kTok > seen;
     f32x16 sc;
     uint32_t vis = 0, sick[ND];
+    // Products and conversions go before another wave's exponentials: 256 requests of 36 query rows 242 ->
+    // 233 us, of 63 264 -> 256, of up to nine rows 168 -> 166.
+    __builtin_amdgcn_s_setprio(1);
     // (a wave's LDS instructions take effect in their order: its reads follow its writes without a
     // wait, and the next tile's writes the reads; the fences keep the compiler to that order)
     if (edge) {
@@ -299,10 +302,13 @@ struct Att4Wave : AttRows<D> {
       scores<false>(t0, x, sc, sick);
     }
     next();
+    __builtin_amdgcn_s_setprio(0);
     B::weigh(sc);
+    __builtin_amdgcn_s_setprio(1);
     asm volatile("" ::: "memory");
     values(sc);
     asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_setprio(0);
     if (edge) spread(vis, sick);
   }
 
@@ -461,14 +467,17 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
         if (live) {
           A::scores(ks, sc);
           if (t0 + kTok > seen) A::B::mask(t0, sc);
-          __builtin_amdgcn_s_setprio(1);  // (see AttWave)
-          A::B::weigh(sc);
+          // the exponentials behind all else (before it 8192 rows take 663 for 657 us, of heads of 64
+          // 434 for 420; over bf16, whose tiles are not converted, they go first)
           __builtin_amdgcn_s_setprio(0);
+          A::B::weigh(sc);
+          __builtin_amdgcn_s_setprio(1);
         }
         if (t0 + kTok > seen && A::clean_values(t0, vs)) A::odd_values(ks, vs, sc);
         if (live) A::values(vs, sc);
         s ^= 1;
       }
+      __builtin_amdgcn_s_setprio(0);
       stage_barrier();  // the next segment's tiles overwrite the stages
     }
     l = half_sum(l);
