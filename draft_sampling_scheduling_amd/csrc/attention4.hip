@@ -473,7 +473,14 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
           A::B::weigh(sc);
           __builtin_amdgcn_s_setprio(1);
         }
-        if (t0 + kTok > seen && A::clean_values(t0, vs)) A::odd_values(ks, vs, sc);
+        if (t0 + kTok > seen && A::clean_values(t0, vs)) {
+          // a group that reads NaN reaches the rows that see its token, whatever its weight, as 0 * NaN
+          // makes it in tiles without edges: what a row does not see has a weight below 0 instead
+          const uint32_t vis = A::B::visible(t0);
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sc[r] = vis & (1u << reg_row(r, 0)) ? sc[r] : -1.0f;
+          A::template odd_values<true>(ks, vs, sc);
+        }
         if (live) A::values(vs, sc);
         s ^= 1;
       }

@@ -248,10 +248,11 @@ struct AttWave : AttRows<D> {
     return __ballot(bad) != 0;
   }
 
-  // The product with a V tile that holds infinities or NaN: a weight of 0 leaves a token out
-  // (a matrix product would make 0 * inf of it).  The weights go through the K tile's LDS,
+  // The product with a V tile that holds infinities or NaN: a weight of 0 (MARKED: below 0) leaves a
+  // token out (a matrix product would make 0 * inf of it).  The weights go through the K tile's LDS,
   // which the scores no longer need, a wave at a time; the V tile is 0 afterwards, so that
   // values() adds nothing.
+  template <bool MARKED = false>
   __device__ __forceinline__ void odd_values(uint32_t ks, uint32_t vs, const f32x16& sc) {
 #pragma unroll 1
     for (int w = 0; w < NR; ++w) {
@@ -265,7 +266,7 @@ struct AttWave : AttRows<D> {
 #pragma unroll 1
       for (int t = 0; t < kTok; ++t) {
         const float wt = lds_get<float>(ks + (t * 32 + n) * 4);
-        if (wt == 0.0f) continue;
+        if (MARKED ? wt < 0.0f : wt == 0.0f) continue;
 #pragma unroll
         for (int dt = 0; dt < ND; ++dt) {
 #pragma unroll
