@@ -79,7 +79,7 @@ struct Att4Wave : AttRows<D> {
   using Out = typename std::conditional<TERMS == 1, uint16_t, float>::type;
   using F = Fit4<D, TERMS>;
   static constexpr int kD = D, kNR = 2;
-  static constexpr bool kMix = true;
+  static constexpr bool kMix = true, kNan = true;
   static __device__ constexpr int round(int M) { return M <= kRows ? 2 * kTok : F::ROUND; }
   static constexpr int ND = D / 32, KSTEPS = D / 16, RB = D * 2, WORDS = D / 16;
 
@@ -379,6 +379,7 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
   using Params = Att4Params;
   using F = Fit4Shared<D>;
   using L = Tile4<D>;
+  static constexpr bool kNan = true;
   static constexpr int GROUPS = D / 32, LANES = 8 * GROUPS;  // lanes that a wave's 8 tokens' keys take
 
   using A::B::h;

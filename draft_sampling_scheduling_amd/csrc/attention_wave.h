@@ -86,6 +86,7 @@ struct AttWave : AttRows<D> {
   using F = Fit<T, D, NR_>;
   static constexpr int kD = D, kNR = NR_;
   static constexpr bool kMix = false;
+  static constexpr bool kNan = false;  // NaN of a value reaches all rows that see it, whatever its weight
   // tokens of a round of a request with M query rows to a cache head
   static __device__ constexpr int round(int) { return F::ROUND; }
 

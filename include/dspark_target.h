@@ -186,7 +186,8 @@ int dspark_cache4_read(int layers, int rows, int Hkv, int D, dspark_dtype dt, in
  *   lse[row][a] = ln sum_t exp(scale * q . K[t])        (nullable, float)
  * Scores, maxima, sums and o are held in float; with bf16 operands the weights exp(s - max)
  * are rounded to bf16 for the product with V.  What lies in the cache at tokens that a row
- * does not see (stale, infinite or NaN) does not reach it.
+ * does not see (stale, infinite or NaN) does not reach it; of what it sees, an infinity or
+ * NaN of V may stay away where its weight is 0 in float.
  * q [rows][Hq][D] with rows q_row elements apart; o [rows][Hq][D] dense, apart from q.
  * D in {64, 128}; Hq a multiple of Hkv; rows * Hq <= 2^31 - 1024; dt as the cache's; strides
  * multiples of 16 bytes, pointers 16-byte aligned.  ctx + n beyond max_pages pages, ctx < 0 or
@@ -208,7 +209,8 @@ int dspark_tree_attention(int R, int rows, int Hq, int Hkv, int D, dspark_dtype 
 
 /* The same over a cache of 4 bits; q and o in dt.  The cache's values are exact operands, and rows
  * are as above: bf16 rows have their weights rounded to bf16, float ones are in float throughout.
- * A group that reads NaN reaches the 32 elements of o it stands for, of rows that see its token.
+ * A group of values that reads NaN reaches the 32 elements of o it stands for, of rows that see its
+ * token, whatever its weight; one of keys all of such a row, o and lse.
  * Token strides up to 2^21 bytes, page strides below 2^32. */
 size_t dspark_tree_attention4_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
                                               dspark_dtype dt);

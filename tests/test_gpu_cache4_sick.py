@@ -1,6 +1,7 @@
 """Groups of a 4-bit cache that read NaN, at tokens whose weight underflows to 0 in float as at others:
 values' reach their 32 elements of o of every row that sees the token, keys' all of such a row, and
-nothing else, whichever variant takes the rows and wherever the token lies in its tile."""
+nothing else, whichever variant takes the rows, wherever the token lies in its tile, and whether the
+list is cut or not."""
 import numpy as np
 import pytest
 import torch
@@ -71,3 +72,16 @@ def test_one_list(n, G, tree, D, dtype):
             c, q, anc = scene(n, G, ctx, D, dtype, low, tree)
             for keys in (False, True):
                 check(c, q, ctx, anc, dtype, [t], keys)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", SIZES)
+def test_cut_list(n, G, D, dtype):
+    """Pieces whose rows have no weight beside others', and pieces that have all of it."""
+    ctx = 6000
+    for low, sick in ((range(3000), [7]), (range(3000), [1500, 2990]), (range(3000), [4000]),
+                      (range(3000, ctx + n), [ctx - 1]), (range(3000, ctx + n), [ctx + n - 1]), ((), [100, 5999])):
+        c, q, anc = scene(n, G, ctx, D, dtype, low)
+        for keys in (False, True):
+            check(c, q, ctx, anc, dtype, sick, keys)
