@@ -85,3 +85,27 @@ def test_cut_list(n, G, D, dtype):
         c, q, anc = scene(n, G, ctx, D, dtype, low)
         for keys in (False, True):
             check(c, q, ctx, anc, dtype, sick, keys)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", SIZES)
+@pytest.mark.parametrize("ctx", [50, 4000])
+def test_odd_queries(ctx, n, G, D, dtype):
+    """Infinite and NaN queries are their own row's affair."""
+    import draft_sampling_scheduling_amd as ds
+    c = c4.Cache4(3, [ctx], [n], 2, D, 16, fill=255)
+    g = np.random.default_rng(n)
+    q = torch.from_numpy(g.standard_normal((n, 2 * G, D), np.float32)).to(dtype)
+    w = ref.attention(q.double().numpy(), c.tokens(c.k, 0, ctx + n), c.tokens(c.v, 0, ctx + n), ctx, D ** -0.5, ref.sees(n))
+    odd = [(0, 0), (n // 2, G), (n - 1, 2 * G - 1)]
+    for at, x in zip(odd, ("nan", "inf", "-inf")):
+        q[(*at, 7)] = float(x)
+    d = c.dev4()
+    got = ds.tree_attention(q.to("cuda:0"), d[0], d[1], torch.from_numpy(c.table).to("cuda:0"), T([ctx]), T([0, n]), scales=d[2])
+    o = got["o"].double().cpu().numpy()
+    well = np.ones(o.shape[:2], bool)
+    for at in odd:
+        well[at] = False
+        assert np.isnan(o[at]).any()
+    assert (np.abs(o - w[0]) <= tol(w, ctx + n, D, dtype is BF)[0])[well].all()
