@@ -591,10 +591,13 @@ static int att_grid() {
   return device_cus() * F::PER_CU;
 }
 
-// The workspace of a grid whose row tiles have MR rows.
+// The workspace of a grid whose row tiles have MR rows.  Pieces take as much in variants of more rows
+// or more; joints are counted for the most workgroups of any, so that the size does not fall where a
+// step's rows take it to a variant of fewer, and a workspace for many rows serves few.
+constexpr int kMostPerCu = 6;
 static inline size_t att_carve(AttParams& p, void* ws, int grid, int MR, int D) {
   Carve cv(ws);
-  p.joint = cv.take<AttJoint>((size_t)grid);
+  p.joint = cv.take<AttJoint>((size_t)device_cus() * kMostPerCu);
   p.part = cv.take<float>((size_t)grid * 2 * MR * (D + 2));
   return cv.bytes();
 }
@@ -649,6 +652,7 @@ template <class W>
 static int att_launch(typename W::Params p, hipStream_t stream) {
   using F = typename W::F;
   constexpr int NR = W::kNR;
+  static_assert(F::PER_CU <= kMostPerCu, "a workgroup has a joint each");
   static std::atomic<uint64_t> raised;
   auto kern = attention_kernel<W>;
   const int grid = att_grid<F>();

@@ -194,7 +194,8 @@ int dspark_cache4_read(int layers, int rows, int Hkv, int D, dspark_dtype dt, in
  * row_off out of order are clamped (DSPARK_FAULT_LEN); a page id outside [0, n_pages) reads page 0
  * (DSPARK_FAULT_PAGE); with anc, nodes past 64 are seen by nobody but through ctx
  * (DSPARK_FAULT_TREE).
- * Workspace: ws_bytes >= dspark_tree_attention_workspace_bytes(...) (0: sizes out of range).
+ * Workspace: ws_bytes >= dspark_tree_attention_workspace_bytes(...) (0: sizes out of range).  It does
+ * not fall as rows / R grows: the size for one request with the most rows of any step serves them all.
  * ------------------------------------------------------------------------------------ */
 size_t dspark_tree_attention_workspace_bytes(int R, int rows, int Hq, int Hkv, int D,
                                              dspark_dtype dt);
