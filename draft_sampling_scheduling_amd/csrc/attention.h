@@ -535,12 +535,12 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttParams p, bool a
       for (int u = 0; u < kBatch; ++u) {
         // where a piece has no weight its row stays out (0 * inf is none); its sum is finite, or
         // NaN where the row's scores are.  Of a cache of 4 bits NaN comes along: a group of a token
-        // that the row sees, and within a piece 0 * NaN keeps it.
+        // that the row sees, and within a piece 0 * NaN keeps it.  (A lane's elements share a group.)
         f = __builtin_amdgcn_exp2f(pm[u] - ref);
         l = fmaf(pl[u], f, l);
+        const bool in = f != 0.0f || (W::kNan && x[u][0] != x[u][0]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[e] = f != 0.0f || (W::kNan && x[u][e] != x[u][e]) ? fmaf(x[u][e], f, acc[e]) : acc[e];
+        for (int e = 0; e < 4; ++e) acc[e] = in ? fmaf(x[u][e], f, acc[e]) : acc[e];
       }
       m = mn;
     };
