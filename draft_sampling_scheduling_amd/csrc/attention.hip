@@ -26,7 +26,7 @@
 // tokens over 100001 to 131071, 40 heads on 8 (0.95 GB) 161 to 180 us; 64 trees over 100 to
 // 2048, 20 heads on 4 (145 MB) 42 to 45 us, of which 29 us are the bytes at a copy's rate.  Prompts are
 // bound by the softmax's vector work, which takes as long as the products and overlaps them in
-// part: 8192 rows, 32 heads on 8, 677 to 700 us, 800 TFLOP/s of the pairs seen.
+// part: 8192 rows, 32 heads on 8, 677 to 730 us, 750 to 810 TFLOP/s of the pairs seen.
 #include "attention_wave.h"
 
 namespace dspark {

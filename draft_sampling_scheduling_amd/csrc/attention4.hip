@@ -499,7 +499,9 @@ struct Att4Shared : AttWave<uint16_t, D, 4, Tile4<D>> {
 // host knows, times heads to a cache head) waves that share tiles save the others' conversions: 8192 rows
 // from an empty cache 655 against 791 us, 2048 behind 4048 230 and 253, 64 requests of 72 over 500 to
 // 4000 114 and 123; over short contexts the barriers cost as much (16 requests of 128 rows behind 1000
-// tokens 39 and 37).  Up to 64 they lose: 36 rows 343 and 242 us, 45 37 and 29.
+// tokens 39 and 37).  Up to 64 they lose: 36 rows 343 and 242 us, 45 37 and 29, 64 rows 374 and 254, of
+// heads of 64 224 and 160 (256 requests of 512 to 4096 tokens), but not in one list cut to small pieces:
+// one request of 64 behind 16000 31 and 39.
 template <class F>
 static auto att4_variant(int R, int rows, int G, int D, dspark_dtype dt, F f) {
   if (dt == DSPARK_F32) return D == 64 ? f((Att4Wave<64, 3>*)nullptr) : f((Att4Wave<128, 3>*)nullptr);

@@ -8,13 +8,14 @@
 // sines come from the row of a table that the row's position names.  About six operations an
 // element, so HBM bounds it: each element is read and written once.  Measured, kernels alone, bf16, heads
 // of 128: 8192 rows of 32 and 8 heads with norms to rows (172 MB) 36 us, 4.7 TB/s; 1280 rows of those and
-// 8 heads of values into the cache (32 MB) 11; 8192 rows of 40, 8 and 8 heads into 4 bits (212 MB) 51,
-// 4.2 TB/s; 8224 tokens of 8 heads back out (43 MB) 11.
+// 8 heads of values into the cache (32 MB) 11, into 4 bits (28 MB) 13; 8192 rows with norms into 4 bits
+// (181 MB) 50, 3.6 TB/s; 8192 rows of 40, 8 and 8 heads without (212 MB) 51, 4.2 TB/s; 8224 tokens of 8
+// heads back out (43 MB) 11.
 //
 // A lane has two pieces of 8 elements of a head that hold both halves of its pairs, so a cosine and a
 // sine are loaded for each pair once; D / 16 lanes work on a head, and go through heads of their row with
 // the row's cosines and sines in registers.  (A piece a lane, the other halves loaded beside it, took
-// twice the loads: 32 against 23 us for 1280 rows of 32 and 8 heads of 128 into 4 bits.)  All of a
+// twice the loads: 32 against 23 us for 1280 rows of 32 and 8 heads of 128 into 4 bits and back out.)  All of a
 // head's loads return before any of it is stored, so rows may be turned in place.
 // float throughout, rounded once; but keys on their way to 4 bits are taken in double: a code's
 // step is up to half of its value, so at a border the last bit of a float decides about that
@@ -397,7 +398,8 @@ static bool rows_meet(const void* a, int64_t a_row, int64_t na, const void* b, i
 // they can get; of many, a group goes through several heads with the row's cosines and sines, loaded
 // once.  us for 1, 2, 4, 8, 16 groups a row: 8192 rows to rows, 40 heads of 128, 45, 44, 41, 37, 40; to the
 // cache, 48 heads, 59, 51, 48, 44, 47; into 4 bits with norms, in whose double precision a group's weights
-// cost more, 68, 61, 60, 66, 74; 1280 rows of that, for 6, 12 and 25 groups, 24, 23, 25.
+// cost more, and back out (11), 68, 61, 60, 66, 74; 1280 rows of that (10), for 6, 12 and 25 groups, 24,
+// 23, 25.
 static int rope_slices(int rows, int heads, bool slow) {
   int least = 1;  // groups a row has at the least: a group takes 8 (16) heads at the most
   while (least * (slow ? 16 : 8) < heads) least *= 2;

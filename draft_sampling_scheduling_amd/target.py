@@ -446,7 +446,8 @@ def cache_read(k_cache, v_cache, scales, slot, *, dtype=_BF16, n_rows=None, out=
 
 
 def tree_attention_workspace_bytes(R, rows, Hq, Hkv, D, dt, four=False) -> int:
-    """four: over a cache of 4 bits."""
+    """four: over a cache of 4 bits.  The size for one request with the most rows of any step (R = 1)
+    serves all of them."""
     name = "dspark_tree_attention4_workspace_bytes" if four else "dspark_tree_attention_workspace_bytes"
     return _fn(name)(R, rows, Hq, Hkv, D, dt)
 
